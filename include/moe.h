@@ -342,6 +342,44 @@ moe_status moe_layer_prefill_noalloc(const moe_shape *shape, const void *X,
                                      moe_stream stream);
 
 /*
+ * The layer for a few tokens: the answering steps that follow a prompt, on
+ * the same resident arena (every expert Ready in it). Same router and top-k
+ * as moe_layer_prefill, bit for bit, then
+ *   H_i = SiLU(W_g x_t) * (W_u x_t),  o_i = alpha_i * (W_d H_i),
+ *   Y[t] += o_i over the token's routes i = t*K'..t*K'+K'-1, ascending,
+ * in fp32: unlike the prompt layer's bf16 H, H is not rounded, so the outputs
+ * of the two differ by that rounding. Each expert hit is read once. Y is
+ * bitwise run-to-run identical and independent of phi and P.
+ *   shape    T <= MOE_DECODE_MAX_T tokens, T * K' <= MOE_DECODE_MAX_ROUTES
+ *            (MOE_ERR_UNSUPPORTED otherwise); every dtype; `capacity` is not
+ *            used. T, k, ldx and ldy may differ from the arena's shape.
+ *   X        16-byte aligned; fp32 X needs ldx % 4 == 0
+ *   W_r, bias, logits, Y: as in moe_layer_prefill
+ *   routes   topk_idx and topk_w [T][K'] are written; the other descriptors
+ *            are neither read nor written and may be NULL
+ *   ws       at least moe_decode_workspace_bytes(shape) bytes, prepared once
+ *            by moe_decode_workspace_init with any shape at least as large in
+ *            T; 256-byte aligned. Its contents do not outlive a call, so one
+ *            workspace may serve any number of layers and of shapes with no
+ *            more bytes, one call at a time (calls on several streams, or
+ *            graphs replayed on several, need one each).
+ * Into a stream that is being captured the call records its kernels only, no
+ * event: every slot's load must have completed by then (MOE_ERR_SLOT_STATE
+ * otherwise), and before a slot that the graph reads is loaded again the
+ * caller has to wait for the graph's replays.
+ */
+#define MOE_DECODE_MAX_T 64
+#define MOE_DECODE_MAX_ROUTES 1024
+size_t moe_decode_workspace_bytes(const moe_shape *shape);
+moe_status moe_decode_workspace_init(const moe_shape *shape, void *ws,
+                                     size_t ws_bytes, moe_stream stream);
+moe_status moe_layer_decode(const moe_shape *shape, const void *X,
+                            const float *W_r, const float *bias,
+                            const float *logits, float *Y, moe_arena *arena,
+                            const moe_routes *routes, void *ws,
+                            size_t ws_bytes, moe_stream stream);
+
+/*
  * Weight packing (section 3.3, "Offline NPU-Consumable Weight Layout":
  * experts are stored in the layout the kernels consume).
  *

@@ -46,6 +46,8 @@ MOE_FFN_SIMPLE_KERNEL = 4
 MOE_FFN_FUSED = 8
 MOE_SLOT_AVAILABLE, MOE_SLOT_FILLING, MOE_SLOT_READY, MOE_SLOT_IN_USE = 0, 1, 2, 3
 MOE_MAX_EXPERTS = 512
+MOE_DECODE_MAX_T = 64
+MOE_DECODE_MAX_ROUTES = 1024
 
 
 class MoEError(RuntimeError):
@@ -82,6 +84,9 @@ _SIGS = {
     "moe_expert_ffn": ([_VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], _I32),
     "moe_layer_prefill": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _VP], _I32),
     "moe_layer_prefill_noalloc": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], _I32),
+    "moe_decode_workspace_bytes": ([_VP], _SZ),
+    "moe_decode_workspace_init": ([_VP, _VP, _SZ, _VP], _I32),
+    "moe_layer_decode": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP], _I32),
     "moe_pack_gate_up": ([_VP, _VP, _VP, _VP, _I32, _I64, _I64, _VP], _I32),
     "moe_pack_gate_up_host": ([_VP, _VP, _VP, _VP], _I32),
     "moe_pack_down": ([_VP, _VP, _VP, _I32, _I64, _I64, _VP], _I32),
@@ -161,7 +166,7 @@ def make_shape(T, d, f, E, k, n_shared=0, P=None, capacity=None, dtype="bf16", r
 
 
 def routes_struct(r: dict) -> moe_routes:
-    return moe_routes(*[_ptr(r[k]) for k in ("topk_idx", "topk_w", "slot_count", "slot_offset",
+    return moe_routes(*[_ptr(r.get(k)) for k in ("topk_idx", "topk_w", "slot_count", "slot_offset",
                                               "rec_token", "rec_route", "route_pos")])
 
 
@@ -240,6 +245,22 @@ def moe_layer_prefill_noalloc(shape, X, W_r, bias, logits, Y, arena, routes: dic
                                             _ptr(Y), arena.handle, ctypes.byref(rs), _stream(stream)))
 
 
+def moe_decode_workspace_bytes(shape: moe_shape) -> int:
+    return int(load().moe_decode_workspace_bytes(ctypes.byref(shape)))
+
+
+def moe_decode_workspace_init(shape, ws, stream=None):
+    _check(load().moe_decode_workspace_init(ctypes.byref(shape), _ptr(ws), ws.numel() * ws.element_size(),
+                                            _stream(stream)))
+
+
+def moe_layer_decode(shape, X, W_r, bias, logits, Y, arena, routes: dict, ws, stream=None):
+    rs = routes_struct(routes)
+    _check(load().moe_layer_decode(ctypes.byref(shape), _ptr(X), _ptr(W_r), _ptr(bias), _ptr(logits), _ptr(Y),
+                                   arena.handle, ctypes.byref(rs), _ptr(ws), ws.numel() * ws.element_size(),
+                                   _stream(stream)))
+
+
 def moe_pack_gate_up(shape, Wg, Wu, dst, n, src_stride, dst_stride, stream=None):
     _check(load().moe_pack_gate_up(ctypes.byref(shape), _ptr(Wg), _ptr(Wu), _ptr(dst), n,
                                    src_stride, dst_stride, _stream(stream)))
@@ -303,6 +324,19 @@ def moe_selftest_mfma_layout(out, stream=None):
 
 
 # ------------------------------------------------------- buffer helpers --
+def row_stride(t: torch.Tensor) -> int:
+    """Elements between rows; a single row's stride says nothing."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+
+
+def check_rows(t: torch.Tensor, dtype, cols: int, name: str) -> None:
+    """A matrix on the GPU whose rows are contiguous and do not overlap."""
+    if t.dim() != 2 or t.dtype != dtype or t.shape[1] != cols or not t.is_cuda:
+        raise ValueError(f"{name}: need a GPU matrix [rows][{cols}] of {dtype}")
+    if cols > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+
+
 def alloc_routes(shape: moe_shape, device="cuda") -> dict:
     kp = shape.k + shape.n_shared
     i32 = dict(dtype=torch.int32, device=device)
@@ -323,6 +357,17 @@ def alloc_workspace(shape: moe_shape, device="cuda") -> torch.Tensor:
     off = (-buf.data_ptr()) % 256
     ws = buf[off:off + n]
     moe_workspace_init(shape, ws)
+    return ws
+
+
+def alloc_decode_workspace(shape: moe_shape, device="cuda") -> torch.Tensor:
+    n = moe_decode_workspace_bytes(shape)
+    if n == 0:
+        _check(MOE_ERR_INVALID_ARG)
+    buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    ws = buf[off:off + n]
+    moe_decode_workspace_init(shape, ws)
     return ws
 
 

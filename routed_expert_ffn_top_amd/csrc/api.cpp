@@ -21,6 +21,7 @@
 #include <vector>
 
 #include "common.h"
+#include "decode.h"
 #include "residency.h"
 
 using namespace moe;
@@ -198,6 +199,16 @@ struct HipBackend {
     int record(Event e, Stream s) { return (last = hipEventRecord(e, s)) != hipSuccess; }
     int wait(Stream s, Event e) { return (last = hipStreamWaitEvent(s, e, 0)) != hipSuccess; }
     int sync(Event e) { return (last = hipEventSynchronize(e)) != hipSuccess; }
+    bool done(Event e)
+    {
+        // queried while this thread captures a stream: the query belongs to no
+        // capture, so it is made in the mode that leaves captures alone
+        hipStreamCaptureMode m = hipStreamCaptureModeRelaxed;
+        (void)hipThreadExchangeStreamCaptureMode(&m);
+        const hipError_t e2 = hipEventQuery(e);
+        (void)hipThreadExchangeStreamCaptureMode(&m);
+        return e2 == hipSuccess;
+    }
 };
 
 }  // namespace
@@ -699,6 +710,134 @@ moe_status moe_selftest_mfma_layout(float *out, moe_stream stream)
     if (!out) return fail(MOE_ERR_INVALID_ARG, "out is NULL");
     HIP_TRY(launch_selftest_mfma(out, S(stream)), "self-test launch");
     return MOE_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// the layer for a few tokens
+
+namespace {
+
+moe_status check_decode_shape(const moe_shape *s)
+{
+    MOE_TRY(check_shape(s));
+    if (s->T > kDecMaxT || (int64_t)s->T * (s->k + s->n_shared) > kDecMaxRoutes)
+        return fail(MOE_ERR_UNSUPPORTED, "decode: needs T <= %d and T * (k + n_shared) <= %d", kDecMaxT, kDecMaxRoutes);
+    return MOE_OK;
+}
+
+moe_status check_decode_ws(const moe_shape *s, void *ws, size_t ws_bytes, DecLayout *w)
+{
+    *w = dec_layout(*s);
+    if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (!aligned(ws, 256)) return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < w->total) return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu < %zu", ws_bytes, w->total);
+    return MOE_OK;
+}
+
+// The decode kernels, arguments checked and the slots' loads ordered before.
+moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, const float *W_r, const float *bias,
+                       const float *logits, float *Y, const moe_arena *a, const PhiArg &phi, const moe_routes &r,
+                       void *ws, hipStream_t st)
+{
+    const float *L = logits;
+    if (W_r) {
+        float *own = ws_at<float>(ws, w.logits);
+        HIP_TRY(TIMED(MOE_KERNEL_ROUTER, st, launch_router_logits(s, X, W_r, bias, own, st)), "router launch");
+        L = own;
+    }
+    HIP_TRY(TIMED(MOE_KERNEL_TOPK, st, launch_topk(s, 0, s.T, L, r.topk_idx, r.topk_w, nullptr, st)), "top-k launch");
+    int32_t *list = ws_at<int32_t>(ws, w.list);
+    DecArgs g{};
+    g.l = DecLists{list, list + 1, list + 1 + kMaxExp, list + 1 + 2 * kMaxExp, list + 1 + 3 * kMaxExp};
+    HIP_TRY(launch_dec_lists(s, r.topk_idx, phi, g.l, st), "route list launch");
+    g.kp = s.k + s.n_shared;
+    g.R = s.T * g.kp;
+    g.topk_w = r.topk_w;
+    DecArgs h = g;
+    g.X = X;
+    g.ldx = s.ldx;
+    g.W = a->plane_gu;
+    g.slot_bytes = a->stride_gu * a->esz;
+    g.scale_off = (int64_t)2 * s.f * s.d;
+    g.N = 2 * s.f;
+    g.K = s.d;
+    g.out = ws_at<char>(ws, w.H);
+    g.ldo = s.f;
+    HIP_TRY(TIMED(MOE_KERNEL_GATE_UP, st, launch_dec_proj(s, g, true, st)), "gate/up launch");
+    h.X = g.out;
+    h.ldx = s.f;
+    h.W = a->plane_d;
+    h.slot_bytes = a->stride_d * a->esz;
+    h.scale_off = (int64_t)s.d * s.f;
+    h.N = s.d;
+    h.K = s.f;
+    h.out = ws_at<char>(ws, w.Yr);
+    h.ldo = s.d;
+    HIP_TRY(TIMED(MOE_KERNEL_DOWN, st, launch_dec_proj(s, h, false, st)), "down launch");
+    HIP_TRY(TIMED(MOE_KERNEL_COMBINE, st, launch_dec_combine(s, Y, ws_at<float>(ws, w.Yr), st)), "combine launch");
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_decode_workspace_bytes(const moe_shape *shape)
+{
+    if (check_decode_shape(shape) != MOE_OK) return 0;
+    return dec_layout(*shape).total;
+}
+
+moe_status moe_decode_workspace_init(const moe_shape *shape, void *ws, size_t ws_bytes, moe_stream stream)
+{
+    MOE_TRY(check_decode_shape(shape));
+    DecLayout w;
+    MOE_TRY(check_decode_ws(shape, ws, ws_bytes, &w));
+    (void)stream;
+    return MOE_OK;
+}
+
+moe_status moe_layer_decode(const moe_shape *shape, const void *X, const float *W_r, const float *bias,
+                            const float *logits, float *Y, moe_arena *arena, const moe_routes *routes, void *ws,
+                            size_t ws_bytes, moe_stream stream)
+{
+    MOE_TRY(check_decode_shape(shape));
+    if (shape->T == 0) return MOE_OK;
+    const moe_shape &s = *shape;
+    hipStream_t st = S(stream);
+    DecLayout w;
+    MOE_TRY(check_decode_ws(shape, ws, ws_bytes, &w));
+    if (!routes || !routes->topk_idx || !routes->topk_w)
+        return fail(MOE_ERR_INVALID_ARG, "decode: topk_idx and topk_w are required");
+    if (!X || !Y || !arena) return fail(MOE_ERR_INVALID_ARG, "decode: X, Y and arena are required");
+    if (!W_r && !logits) return fail(MOE_ERR_INVALID_ARG, "decode: give W_r or logits");
+    if (W_r && !aligned(W_r, 16)) return fail(MOE_ERR_INVALID_ARG, "decode: W_r must be 16-byte aligned");
+    if (!aligned(X, 16) || !aligned(Y, 16))
+        return fail(MOE_ERR_INVALID_ARG, "decode: X and Y must be 16-byte aligned");
+    if (s.dtype == MOE_DT_F32 && (s.ldx % 4) != 0)
+        return fail(MOE_ERR_UNSUPPORTED, "decode: fp32 X needs ldx %% 4 == 0");
+    const moe_shape &as = arena->shape;
+    if (as.d != s.d || as.f != s.f || as.P != s.P || as.dtype != s.dtype || as.E != s.E || as.n_shared != s.n_shared)
+        return fail(MOE_ERR_INVALID_ARG, "arena was made for another shape");
+    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+    HIP_TRY(hipStreamIsCapturing(st, &cap), "hipStreamIsCapturing");
+    const int ne = s.E + s.n_shared;
+    int32_t phi[kMaxExp];
+    PhiArg pa;
+    std::lock_guard<std::mutex> lk(arena->mu);
+    arena->res.placement(phi, ne);
+    for (int e = 0; e < ne; ++e)
+        if (phi[e] < 0) return fail(MOE_ERR_SLOT_STATE, "expert %d is not resident", e);
+    MOE_TRY(check_phi(shape, phi, &pa));
+    if (cap != hipStreamCaptureStatusNone) {
+        MOE_TRY(R(arena, arena->res.acquire_captured(phi)));
+        return decode_impl(s, w, X, W_r, bias, logits, Y, arena, pa, *routes, ws, st);
+    }
+    MOE_TRY(arena_acquire(arena, phi, st));
+    MOE_TRY(decode_impl(s, w, X, W_r, bias, logits, Y, arena, pa, *routes, ws, st));
+    return arena_release_after(arena, phi, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,56 @@
+// Internal declarations of the few-token layer (moe_layer_decode).
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+constexpr int kDecMaxT = MOE_DECODE_MAX_T;             // a slot has at most this many rows
+constexpr int kDecMaxRoutes = MOE_DECODE_MAX_ROUTES;   // T * K'
+
+// Byte offsets of the decode workspace's regions.
+struct DecLayout {
+    size_t logits;   // float[T][E]
+    size_t list;     // int32: [0] slots with routes, then the DecLists arrays
+    size_t H;        // fp32 layers: float[R][f]; bf16 layers: uint16[3][R][f], H as a sum of three bf16 terms
+    size_t Yr;       // float[R][d], alpha times each route's output row
+    size_t total;
+};
+
+inline DecLayout dec_layout(const moe_shape &s)
+{
+    DecLayout w{};
+    const size_t R = (size_t)s.T * (s.k + s.n_shared);
+    size_t o = 0;
+    w.logits = o; o = align_up(o + (size_t)s.T * s.E * 4, 256);
+    w.list = o;   o = align_up(o + (size_t)(1 + 3 * kMaxExp + kDecMaxRoutes) * 4, 256);
+    w.H = o;      o = align_up(o + R * s.f * (act_bf16(s) ? 6 : 4), 256);
+    w.Yr = o;     o = align_up(o + R * s.d * 4, 256);
+    w.total = o;
+    return w;
+}
+
+// The routes sorted by slot: entry a < *n_act is a slot with routes, its
+// routes rec[off .. off + cnt) in ascending route order.
+struct DecLists {
+    int32_t *n_act, *slot, *off, *cnt, *rec;
+};
+
+struct DecArgs {
+    DecLists l;
+    const void *X;        // gate/up: activations; down: H
+    int64_t ldx;
+    const char *W;        // plane base
+    int64_t slot_bytes;   // bytes between slots
+    int64_t scale_off;    // fp8: bytes from a slice's start to its row scales
+    int N, K, kp, R, nchunk;
+    void *out;            // gate/up: H; down: Yr
+    int64_t ldo;
+    const float *topk_w;
+};
+
+hipError_t launch_dec_lists(const moe_shape &s, const int32_t *idx, const PhiArg &phi, const DecLists &l, hipStream_t st);
+hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a, bool gateup, hipStream_t st);
+hipError_t launch_dec_combine(const moe_shape &s, float *Y, const float *Yr, hipStream_t st);
+
+}  // namespace moe

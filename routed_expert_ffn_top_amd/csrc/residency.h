@@ -22,6 +22,7 @@
 //   typename Bk::Stream, typename Bk::Event
 //   int create(Event *), void destroy(Event), int record(Event, Stream),
 //   int wait(Stream, Event), int sync(Event)       (0 = success)
+//   bool done(Event)        (only for acquire_captured: the event's record has completed)
 // The library instantiates it with HIP streams and events; a host-only test
 // instantiates it with worker threads that play the streams.
 #pragma once
@@ -44,7 +45,7 @@ public:
 
     ResidencyTable(Bk &bk, int P, int n_exp)
         : bk_(bk), P_(P), ne_(n_exp), state_(P, MOE_SLOT_AVAILABLE), owner_(P, -1), ready_(P, Event()),
-          ready_gen_(P, 0), waited_stream_(P, Stream()), waited_gen_(P, 0), ring_(kRing, Event()),
+          ready_gen_(P, 0), loaded_gen_(P, 0), waited_stream_(P, Stream()), waited_gen_(P, 0), ring_(kRing, Event()),
           ring_set_(kRing, 0), last_use_(P, -1), has_ready_(P, 0)
     {
     }
@@ -160,6 +161,25 @@ public:
         return MOE_OK;
     }
 
+    // acquire for an invocation recorded into a graph, which can wait for no
+    // event of another stream: every slot phi names must be Ready or In-use
+    // with that expert and its load complete. No release is recorded; ordering
+    // a later load after the graph's replays is the caller's part.
+    moe_status acquire_captured(const int32_t *phi)
+    {
+        for (int e = 0; e < ne_; ++e) {
+            const int s = phi[e];
+            if (s < 0) continue;
+            if (s >= P_ || (state_[s] != MOE_SLOT_READY && state_[s] != MOE_SLOT_IN_USE) || owner_[s] != e)
+                return err(MOE_ERR_SLOT_STATE, "phi maps expert %d to slot %d, which is not Ready with it", e, s);
+            if (loaded_gen_[s] == ready_gen_[s]) continue;
+            if (!bk_.done(ready_[s]))
+                return err(MOE_ERR_SLOT_STATE, "slot %d is still being loaded: wait for it before capturing", s);
+            loaded_gen_[s] = ready_gen_[s];
+        }
+        return MOE_OK;
+    }
+
     // After an invocation's work on st: record a release event and mark the
     // slots phi names In-use with it as their last use. The ring's events are
     // created by the first load or publication, so an invocation (whose slots
@@ -254,6 +274,7 @@ private:
     std::vector<int> state_, owner_;
     std::vector<Event> ready_;
     std::vector<uint64_t> ready_gen_;
+    std::vector<uint64_t> loaded_gen_;   // the load last seen complete (acquire_captured)
     std::vector<Stream> waited_stream_;
     std::vector<uint64_t> waited_gen_;
     std::vector<Event> ring_;

@@ -44,6 +44,7 @@ class MoELayer:
         self.bias = None if inp.bias is None else inp.bias.to(self.device).contiguous()
         self.routes = B.alloc_routes(self.shape, self.device)
         self.ws = B.alloc_workspace(self.shape, self.device)
+        self._decode = {}   # by token count: shape, routes, workspace
         self.paged = paged
         self.arena = B.Arena(self.shape, G=(cfg.G if paged else None), device=self.device)
         Wg = inp.Wg.to(self.device)
@@ -85,6 +86,40 @@ class MoELayer:
         B.moe_layer_prefill(self.shape, self.X, Wr, bias, logits, Y, self.arena,
                             self.host_gu, self.host_d, self.routes, self.ws, compute, copy)
         return Y
+
+    def decode(self, X: torch.Tensor, Y: torch.Tensor, logits: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+        """The layer on a few new tokens X [T][d] (rows may be strided), with
+        the resident experts: Y [T][d] holds the residual on entry and the
+        layer output on return. Route ids and weights are in
+        ``decode_routes(T)``. One call at a time (one workspace a token count)."""
+        B.check_rows(X, self.X.dtype, self.cfg.d, "X")
+        B.check_rows(Y, torch.float32, self.cfg.d, "Y")
+        if X.shape[0] != Y.shape[0] or (logits is not None and tuple(logits.shape) != (X.shape[0], self.cfg.E)):
+            raise ValueError("X, Y and logits need as many rows")
+        shape, routes, ws = self._decode_buffers(X.shape[0])
+        shape.ldx, shape.ldy = B.row_stride(X), B.row_stride(Y)
+        if logits is not None:
+            B.check_rows(logits, torch.float32, self.cfg.E, "logits")
+            logits = logits.contiguous()
+        B.moe_layer_decode(shape, X, None if logits is not None else self.Wr, None if logits is not None else self.bias,
+                           logits, Y, self.arena, routes, ws, stream)
+        return Y
+
+    def decode_routes(self, T: int) -> dict:
+        """topk_idx and topk_w [T][K'] of the last decode call with T tokens."""
+        return self._decode_buffers(T)[1]
+
+    def _decode_buffers(self, T: int):
+        if T not in self._decode:
+            c = self.cfg
+            shape = B.make_shape(T, c.d, c.f, c.E, c.k, c.n_shared, P=self.shape.P, capacity=1, dtype=c.dtype,
+                                 renorm=c.renorm)
+            ws = B.alloc_decode_workspace(shape, self.device)
+            routes = dict(topk_idx=torch.zeros((T, c.kp), dtype=torch.int32, device=self.device),
+                          topk_w=torch.zeros((T, c.kp), dtype=torch.float32, device=self.device))
+            self._decode[T] = (shape, routes, ws)
+        return self._decode[T]
 
     def close(self):
         self.arena.close()

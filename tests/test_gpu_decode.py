@@ -1,0 +1,417 @@
+"""The layer for a few tokens (moe_layer_decode) against its formulas in 64
+bits.
+
+Bound on each output element. All sums are in fp32 with u = 2^-24 a rounding
+and gamma_n = n u / (1 - n u) for a sum of n terms in any order; weights and
+activations are exact inputs (bf16 products of 8 by 8 bits are exact in fp32,
+fp32 ones round once more). With a = |W_g||x|, b = |W_u||x|:
+  dg = gamma(d + 4) a, du = gamma(d + 4) b (4: row scale, products, joins)
+  dh = 1.1 |u| dg + |silu g| du + 1.1 dg du + 8u (|h| + ...)   (|silu'| < 1.1;
+       exp, 1 +, divide and multiply are within 2, 1, 1 and 1 ulp, counted as 8)
+  do = |W_d| dh + gamma(3 f + 4) |W_d| (|h| + dh)   (H enters as three terms)
+  dy = sum_j alpha (do + 2u (|o| + do)) + gamma(K' + 1) (|A| + sum_j alpha (|o| + do))
+Route ids and weights are taken from the call and checked on their own.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import OracleRun, check_routing_from_gpu_logits, gpu_inputs, say
+from routed_expert_ffn_top_amd import binding as B
+from routed_expert_ffn_top_amd.inputs import CONFIGS, MoEConfig, make_logits
+from routed_expert_ffn_top_amd.layer import MoELayer
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DTYPES = ["bf16", "f32", "bf16_fp8w", "bf16_fp4w"]
+
+
+def gamma(n):
+    return n * U / (1 - n * U)
+
+
+def plain_weights(inp):
+    """Expert weights as fp64 on the GPU, from the stored codes."""
+    cfg, o = inp.cfg, OracleRun.__new__(OracleRun)
+    if not cfg.quant_weights:
+        return tuple(w.double() for w in (inp.Wg, inp.Wu, inp.Wd))
+    from oracle import oracle as oracle_mod
+    orc = oracle_mod.get()
+    out = []
+    for q, s in ((inp.Wg, inp.Sg), (inp.Wu, inp.Su), (inp.Wd, inp.Sd)):
+        if cfg.fp8_weights:
+            w = torch.from_numpy(orc.fp8e4m3_decode(q.cpu().numpy())).cuda().double() * s.double()[..., None]
+        else:
+            w = torch.from_numpy(orc.mxfp4_decode(q.cpu().numpy(), s.cpu().numpy())).cuda().double()
+        out.append(w)
+    return tuple(out)
+
+
+def reference(inp, weights, X, A, idx, w):
+    """(y, bound) [T][d] in 64 bits for the given route ids and weights."""
+    cfg = inp.cfg
+    Wg, Wu, Wd = weights
+    x = X.double()
+    y, s, err = A.double(), A.double().abs(), torch.zeros_like(A, dtype=torch.float64)
+    for e in range(cfg.n_exp):
+        t, j = torch.nonzero(idx == e, as_tuple=True)
+        if not len(t):
+            continue
+        xe = x[t]
+        g, u = xe @ Wg[e].t(), xe @ Wu[e].t()
+        dg = gamma(cfg.d + 4) * (xe.abs() @ Wg[e].abs().t())
+        du = gamma(cfg.d + 4) * (xe.abs() @ Wu[e].abs().t())
+        silu = g * torch.sigmoid(g)
+        h = silu * u
+        dh = 1.1 * u.abs() * dg + silu.abs() * du + 1.1 * dg * du
+        dh = dh + 8 * U * (h.abs() + dh) + 2.0 ** -126
+        o = h @ Wd[e].t()
+        do = (dh + gamma(3 * cfg.f + 4) * (h.abs() + dh)) @ Wd[e].abs().t()
+        al = w[t, j].double()[:, None]
+        y[t] += al * o
+        s[t] += al * (o.abs() + do)
+        err[t] += al * (do + 2 * U * (o.abs() + do))
+    return y, err + gamma(cfg.kp + 1) * s + 2.0 ** -140
+
+
+def check(inp, weights, X, A, Y, routes, name=""):
+    torch.cuda.synchronize()
+    ref, bound = reference(inp, weights, X, A, routes["topk_idx"].long(), routes["topk_w"])
+    err = (Y.double() - ref).abs()
+    assert torch.isfinite(Y).all()
+    ffn = (ref - A.double()).norm()
+    say(f"  {name}: max err/bound {float((err / bound).max()):.3g}, expert sum rel {float(err.norm() / ffn):.3g}")
+    assert bool((err <= bound).all())
+
+
+def tokens(cfg, T, seed=1, pad=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    X = torch.empty((T, cfg.d + pad), device="cuda").normal_(generator=gen).to(cfg.torch_dtype)[:, : cfg.d]
+    return X, torch.empty((T, cfg.d), device="cuda").normal_(generator=gen)
+
+
+SMALL = MoEConfig(name="dec_small", index=71, T=4, d=256, f=192, E=8, k=2)
+SHARED = MoEConfig(name="dec_shared", index=72, T=4, d=320, f=128, E=5, k=3, n_shared=2, renorm=False)
+ONE = MoEConfig(name="dec_one", index=73, T=4, d=64, f=64, E=1, k=1)
+WIDE = MoEConfig(name="dec_wide", index=74, T=4, d=448, f=320, E=96, k=8)
+F32ODD = MoEConfig(name="dec_f32odd", index=75, T=4, d=100, f=96, E=6, k=2, dtype="f32")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cfg", [SMALL, SHARED, ONE, WIDE], ids=lambda c: c.name)
+def test_decode_token_counts(cfg, dtype):
+    cfg = cfg.with_(dtype=dtype)
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    for T in (1, 2, 15, 16, 17, 33, 64):
+        say(f"decode {cfg.name} {dtype} T={T}")
+        X, A = tokens(cfg, T, seed=T)
+        Y = A.clone()
+        layer.decode(X, Y)
+        check(inp, weights, X, A, Y, layer.decode_routes(T), f"T={T}")
+    assert B.moe_device_errors(layer.shape, layer.ws) == 0
+
+
+def test_decode_f32_odd_widths():
+    say("decode, fp32, d = 100 (a last K piece of 4 values), f = 96")
+    inp = gpu_inputs(F32ODD)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    for T in (1, 20):
+        X, A = tokens(F32ODD, T)
+        Y = A.clone()
+        layer.decode(X, Y)
+        check(inp, weights, X, A, Y, layer.decode_routes(T), f"T={T}")
+
+
+@pytest.mark.parametrize("name,T", [("olmoe_t1024", 1), ("olmoe_t1024_fp4w", 64), ("dsv2lite_t4096_fp8w", 8),
+                                    ("mixtral_t256_fp4w", 3)])
+def test_decode_model_shapes(name, T):
+    say(f"decode {name} T={T}")
+    cfg = CONFIGS[name].with_(T=1)
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    X, A = tokens(cfg, T)
+    Y = A.clone()
+    layer.decode(X, Y)
+    check(inp, weights, X, A, Y, layer.decode_routes(T), name)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_decode_routes_as_the_prompt_layer(dtype):
+    say(f"decode and prompt layer route alike, {dtype}")
+    cfg = WIDE.with_(T=40, dtype=dtype)
+    inp = gpu_inputs(cfg)
+    layer = MoELayer(inp)
+    Y = inp.A.clone()
+    layer.forward(Y)
+    Z = inp.A.clone()
+    layer.decode(inp.X, Z)
+    torch.cuda.synchronize()
+    r = layer.decode_routes(40)
+    assert torch.equal(r["topk_idx"], layer.routes["topk_idx"])
+    assert torch.equal(r["topk_w"], layer.routes["topk_w"])
+    # H is rounded there (bf16: half a step of 2^-8 each value) and not here
+    a, b = (Y - inp.A).double(), (Z - inp.A).double()
+    assert float((a - b).norm() / b.norm()) < (1e-5 if dtype == "f32" else 2.0 ** -8)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_decode_exact_on_integers(dtype):
+    """H of up to 22 bits and sums below 2^24: every step is exact in fp32, so
+    the outputs are the integers, in whatever order they are summed."""
+    say(f"decode on integers, {dtype}")
+    cfg = MoEConfig(name="dec_int", index=76, T=17, d=128, f=128, E=2, k=1, dtype=dtype, renorm=True)
+    inp = gpu_inputs(cfg)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    ints = lambda lo, hi, s: torch.randint(lo, hi + 1, s, generator=gen, device="cuda").float()
+    Wg, Wu = ints(1, 6, (2, 128, 128)), ints(-6, 6, (2, 128, 128))
+    Wg[Wg == 5] = 4.0
+    Wu[Wu.abs() == 5] = 4.0
+    # two units an output: |y| <= 2 * 6 * |h|
+    Wd = torch.zeros(2, 128, 128, device="cuda")
+    for n in range(128):
+        Wd[:, n, n], Wd[:, n, (n * 5 + 3) % 128] = 1.0, -1.0
+    X = ints(1, 4, (17, 128))
+    if cfg.fp4_weights:
+        code = {0: 0, 1: 2, 2: 4, 3: 5, 4: 6, 6: 7}
+        table = torch.zeros(7, dtype=torch.uint8, device="cuda")
+        for v, c in code.items():
+            table[v] = c
+        enc = lambda W: (table[W.abs().long()] | ((W < 0).to(torch.uint8) << 3))
+        pack = lambda W: (enc(W)[..., 0::2] | enc(W)[..., 1::2] << 4).contiguous()
+        inp.Wg, inp.Wu, inp.Wd = pack(Wg), pack(Wu), pack(Wd)
+        for s in (inp.Sg, inp.Su, inp.Sd):
+            s.fill_(127)
+    elif cfg.fp8_weights:
+        inp.Wg, inp.Wu, inp.Wd = (W.to(torch.float8_e4m3fn).view(torch.uint8) for W in (Wg, Wu, Wd))
+        for s in (inp.Sg, inp.Su, inp.Sd):
+            s.fill_(1.0)
+    else:
+        inp.Wg, inp.Wu, inp.Wd = (W.to(cfg.torch_dtype) for W in (Wg, Wu, Wd))
+    layer = MoELayer(inp)
+    logits = torch.zeros(17, 2, device="cuda")
+    logits[::2, 1] = 1.0
+    Y = torch.zeros(17, 128, device="cuda")
+    layer.decode(X.to(cfg.torch_dtype), Y, logits=logits)
+    torch.cuda.synchronize()
+    e = (torch.arange(17, device="cuda") % 2 == 0).long()
+    x = X.double()
+    g = torch.einsum("td,tfd->tf", x, Wg[e].double())
+    h = g * torch.einsum("td,tfd->tf", x, Wu[e].double())
+    assert float(g.min()) > 40 and 2 ** 18 < float(h.abs().max()) < 2 ** 22    # SiLU(g) = g in fp32, more than 16 bits
+    ref = torch.einsum("tf,tnf->tn", h, Wd[e].double())
+    assert float(ref.abs().max()) < 2 ** 24
+    assert torch.equal(Y.double(), ref)
+
+
+def test_decode_strides_and_untouched_columns():
+    say("decode with padded rows of X and Y")
+    inp = gpu_inputs(SMALL)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    for T in (1, 5):
+        X, A = tokens(SMALL, T, pad=40)
+        buf = torch.full((T + 1, SMALL.d + 12), 7.5, device="cuda")
+        Y = buf[:T, : SMALL.d]
+        Y.copy_(A)
+        layer.decode(X, Y)
+        check(inp, weights, X, A, Y, layer.decode_routes(T), f"T={T}")
+        assert bool((buf[:, SMALL.d:] == 7.5).all()) and bool((buf[T] == 7.5).all())
+        Y2 = A.clone()
+        layer.decode(X.contiguous(), Y2)
+        assert torch.equal(Y2, Y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "bf16_fp4w"])
+def test_decode_same_bits_for_any_placement(dtype):
+    say(f"decode: same bits for any phi and P, {dtype}")
+    cfg = WIDE.with_(dtype=dtype)
+    inp = gpu_inputs(cfg)
+    X, A = tokens(cfg, 9)
+    ys = []
+    gen = torch.Generator().manual_seed(3)
+    for phi in (None, torch.randperm(96, generator=gen).tolist(), (torch.randperm(200, generator=gen)[:96]).tolist()):
+        layer = MoELayer(inp, phi=phi)
+        Y = A.clone()
+        layer.decode(X, Y)
+        torch.cuda.synchronize()
+        ys.append(Y)
+        layer.close()
+    assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+
+
+def test_decode_bad_tokens_stay_alone():
+    say("decode: a NaN or infinite token leaves the others alone")
+    inp = gpu_inputs(SMALL)
+    layer = MoELayer(inp)
+    X, A = tokens(SMALL, 20)
+    L = make_logits(20, SMALL.E, 5, device="cuda")
+    Y = A.clone()
+    layer.decode(X, Y, logits=L)
+    X2, L2 = X.clone(), L.clone()
+    X2[3, 7], X2[11] = float("nan"), float("inf")
+    L2[17] = float("nan")
+    Z = A.clone()
+    layer.decode(X2, Z, logits=L2)
+    torch.cuda.synchronize()
+    keep = torch.ones(20, dtype=torch.bool)
+    keep[[3, 11, 17]] = False
+    assert torch.equal(Y[keep], Z[keep])
+    assert bool(torch.isnan(Z[3]).any()) and not bool(torch.isfinite(Z[11]).all())
+    # a row of NaN logits takes ids in order with weight 0
+    r = layer.decode_routes(20)
+    assert r["topk_idx"][17].tolist() == [0, 1] and r["topk_w"][17].tolist() == [0.0, 0.0]
+    assert torch.equal(Z[17], A[17])
+
+
+def test_decode_infinite_hidden_unit():
+    say("decode: an overflowing hidden unit is an infinity, not a NaN")
+    cfg = ONE.with_(dtype="bf16")
+    inp = gpu_inputs(cfg)
+    inp.Wg.fill_(0), inp.Wu.fill_(0), inp.Wd.fill_(0)
+    inp.Wg[0, 0, 0] = inp.Wu[0, 0, 0] = 2.0 ** 100
+    inp.Wd[0, 5, 0] = 1.0
+    layer = MoELayer(inp)
+    X = torch.zeros(1, 64, dtype=torch.bfloat16, device="cuda")
+    X[0, 0] = 1.0
+    Y = torch.zeros(1, 64, device="cuda")
+    layer.decode(X, Y, logits=torch.zeros(1, 1, device="cuda"))
+    torch.cuda.synchronize()
+    assert float(Y[0, 5]) == float("inf")
+
+
+def test_decode_after_prompt_and_between():
+    """As a server runs it: a prompt through the prompt layer, then tokens one
+    batch after another of changing size, all on one stream, unsynchronised."""
+    say("decode: prompt, then batches of changing size")
+    cfg = SHARED.with_(T=150)
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    alone = MoELayer(inp)
+    Yp = inp.A.clone()
+    layer.forward(Yp)
+    runs = []
+    for i, T in enumerate((1, 7, 64, 1, 33, 7)):
+        X, A = tokens(cfg, T, seed=40 + i)
+        Y = A.clone()
+        layer.decode(X, Y)
+        runs.append((X, A, Y))
+    layer.forward(Yp)
+    torch.cuda.synchronize()
+    for X, A, Y in runs:
+        Z = A.clone()
+        alone.decode(X, Z)
+        torch.cuda.synchronize()
+        assert torch.equal(Y, Z)
+    check(inp, weights, *runs[-1], layer.decode_routes(7), "last")
+    Ya = inp.A.clone()
+    alone.forward(Ya)
+    alone.forward(Ya)
+    torch.cuda.synchronize()
+    assert torch.equal(Ya, Yp)
+
+
+def test_decode_two_streams():
+    say("decode: two layers on two streams at once")
+    inps = [gpu_inputs(SMALL), gpu_inputs(WIDE)]
+    layers = [MoELayer(i) for i in inps]
+    ins = [tokens(i.cfg, 8, seed=3 + k) for k, i in enumerate(inps)]
+    want = []
+    for l, (X, A) in zip(layers, ins):
+        Y = A.clone()
+        l.decode(X, Y)
+        torch.cuda.synchronize()
+        want.append(Y)
+    streams = [torch.cuda.Stream() for _ in layers]
+    outs = [[] for _ in layers]
+    for rep in range(20):
+        for k, (l, (X, A)) in enumerate(zip(layers, ins)):
+            with torch.cuda.stream(streams[k]):
+                Y = A.clone()
+                l.decode(X, Y)
+                outs[k].append(Y)
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(y, want[k]) for y in outs[k])
+
+
+def test_decode_one_arena_on_two_streams():
+    say("decode: one arena, two workspaces, two streams")
+    inp = gpu_inputs(SMALL)
+    layer = MoELayer(inp)
+    X, A = tokens(SMALL, 8)
+    Y = A.clone()
+    layer.decode(X, Y)
+    torch.cuda.synchronize()
+    shape = B.make_shape(8, SMALL.d, SMALL.f, SMALL.E, SMALL.k, dtype=SMALL.dtype)
+    bufs = [(B.alloc_routes(shape), B.alloc_decode_workspace(shape), torch.cuda.Stream()) for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for rep in range(40):
+        for routes, ws, st in bufs:
+            with torch.cuda.stream(st):
+                Z = A.clone()
+                B.moe_layer_decode(shape, X, layer.Wr, None, None, Z, layer.arena, routes, ws)
+                outs.append(Z)
+    torch.cuda.synchronize()
+    assert all(torch.equal(Z, Y) for Z in outs)
+
+
+def test_decode_captured_and_replayed():
+    say("decode: captured into a graph, replayed between eager calls, and the arena loaded again")
+    inp = gpu_inputs(SMALL)
+    layer = MoELayer(inp)
+    X, A = tokens(SMALL, 6)
+    Xs, Ys = X.clone(), A.clone()
+    eager = MoELayer(inp)
+    g = torch.cuda.CUDAGraph()
+    layer.decode(Xs, Ys)       # buffers exist before the capture
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        layer.decode(Xs, Ys)
+    for i in range(6):
+        X, A = tokens(SMALL, 6, seed=60 + i)
+        Xs.copy_(X)
+        Ys.copy_(A)
+        g.replay()
+        Z = A.clone()
+        eager.decode(X, Z)
+        if i == 2:
+            W = A.clone()
+            layer2 = MoELayer(inp)
+            layer2.decode(X, W)
+        torch.cuda.synchronize()
+        assert torch.equal(Ys, Z), f"replay {i}"
+    # eager calls on the captured layer still run, and so does a load after the replays
+    for _ in range(40):
+        Z = A.clone()
+        layer.decode(X, Z)
+    torch.cuda.synchronize()
+    assert torch.equal(Z, Ys)
+    Wg, Wu, Wd = inp.Wg, inp.Wu, inp.Wd
+    B.arena_release_slot(layer.arena, 0)
+    B.moe_pack_gate_up(layer.shape, Wg[0], Wu[0], layer.arena.plane_gu[0], 1, 0, 0)
+    B.moe_pack_down(layer.shape, Wd[0], layer.arena.plane_d[0], 1, 0, 0)
+    B.arena_publish_slot(layer.arena, 0, 0)
+    Z = A.clone()
+    layer.decode(X, Z)
+    torch.cuda.synchronize()
+    assert torch.equal(Z, Ys)
+
+
+def test_decode_on_an_absent_expert_is_refused():
+    inp = gpu_inputs(SMALL)
+    layer = MoELayer(inp)
+    B.arena_release_slot(layer.arena, 3)
+    X, A = tokens(SMALL, 2)
+    with pytest.raises(B.MoEError) as e:
+        layer.decode(X, A.clone())
+    assert e.value.status == B.MOE_ERR_SLOT_STATE
+
+
+def test_decode_no_tokens():
+    inp = gpu_inputs(SMALL)
+    layer = MoELayer(inp)
+    X, A = tokens(SMALL, 0)
+    layer.decode(X, A)
+    torch.cuda.synchronize()

@@ -422,6 +422,65 @@ moe_status moe_pack_down_host(const moe_shape *shape, const void *W_d,
                               void *dst);
 
 /*
+ * MXFP4 blocks from values and back (the format of MOE_DT_BF16_FP4W); at
+ * most 2^34 values a call.
+ *   values   device [rows][ld] of val_dtype (MOE_DT_F32 or MOE_DT_BF16), K
+ *            of each row used, K a multiple of 32, rows >= 0, ld >= K; the
+ *            pointer and the row stride 16-byte aligned
+ *   codes    device [rows][K/2], two codes per byte, element 2i in the low
+ *            nibble; 16-byte aligned
+ *   scales   device [rows][K/32] E8M0 bytes
+ * Codes followed by their scales are a source slice of the packing calls.
+ * moe_quantize_mxfp4: a block's scale byte is max(e - 2, 0), e the biased
+ * exponent of its largest magnitude (0 for zeros and fp32 subnormals), so that
+ * magnitude / 2^(byte - 127) lies in [4, 8) wherever e >= 3; each value over
+ * 2^(byte - 127) is rounded to the nearest E2M1 value, ties to the even code,
+ * those beyond 6 to 6, with no negative zero. A block that holds an infinity
+ * or a NaN gets the byte 255 (NaN) and codes 0.
+ * moe_dequantize_mxfp4: value = code value * 2^(byte - 127), exact in both
+ * types unless it exceeds their largest value (infinity); byte 255 gives NaN.
+ */
+moe_status moe_quantize_mxfp4(const void *values, int32_t val_dtype,
+                              int64_t rows, int32_t K, int64_t ld, void *codes,
+                              void *scales, moe_stream stream);
+moe_status moe_dequantize_mxfp4(const void *codes, const void *scales,
+                                int64_t rows, int32_t K, void *values,
+                                int32_t val_dtype, int64_t ld,
+                                moe_stream stream);
+
+/*
+ * Product of MXFP4 matrices, one weight slice per group of rows, as the
+ * expert projections are grouped by the route map:
+ *   C[p][n] = sum_k A[row(p)][k] * B_s[n][k]   for the records p of slot s,
+ * both sides multiplied as they are stored (scaled matrix instructions),
+ * fp32 sums, C rounded once.
+ *   M            records, rows of C; M >= 0
+ *   N, K         multiples of 64
+ *   A_codes, A_scales   device [A_rows][K/2] and [A_rows][K/32], as
+ *                moe_quantize_mxfp4 writes them; A_codes 16-byte aligned,
+ *                A_scales 2-byte aligned
+ *   row_index    device [M] int32: row(p), in [0, A_rows) (rec_token of a
+ *                route build); NULL: row(p) = p, and A_rows >= M
+ *   slot_offset  device [P+1] int32 ascending from 0, at most M: slot s holds
+ *                records [slot_offset[s], slot_offset[s+1]) (slot_offset of a
+ *                route build); records from slot_offset[P] on are left as they
+ *                were. NULL: P = 1 and every record is in slot 0
+ *   B            device, P packed slices [N][K] (as moe_pack_down writes them
+ *                for MOE_DT_BF16_FP4W with d = N and f = K; a plane of an
+ *                arena), B_stride bytes apart; both multiples of 16 and
+ *                B_stride >= a slice when P > 1; P <= 512
+ *   C            device [M][ldc] of c_dtype (MOE_DT_F32 or MOE_DT_BF16), ldc >=
+ *                N; C and its row stride 16-byte aligned
+ * Rows and offsets out of range are brought into it on the device.
+ */
+moe_status moe_matmul_mxfp4(int32_t M, int32_t N, int32_t K,
+                            const void *A_codes, const void *A_scales,
+                            int32_t A_rows, const int32_t *row_index,
+                            const int32_t *slot_offset, int32_t P,
+                            const void *B, int64_t B_stride, void *C,
+                            int32_t c_dtype, int64_t ldc, moe_stream stream);
+
+/*
  * Slot arena (Eq. 3: the slice j of slot s starts at plane_j + s * S_j).
  *   plane_gu  device, P slots of packed gate/up slices (2f*d elements,
  *             tiled layout above), slot stride stride_gu

@@ -84,6 +84,9 @@ _SIGS = {
     "moe_expert_ffn": ([_VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SZ, _VP], _I32),
     "moe_layer_prefill": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _VP], _I32),
     "moe_layer_prefill_noalloc": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], _I32),
+    "moe_quantize_mxfp4": ([_VP, _I32, _I64, _I32, _I64, _VP, _VP, _VP], _I32),
+    "moe_dequantize_mxfp4": ([_VP, _VP, _I64, _I32, _VP, _I32, _I64, _VP], _I32),
+    "moe_matmul_mxfp4": ([_I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _I64, _VP, _I32, _I64, _VP], _I32),
     "moe_decode_workspace_bytes": ([_VP], _SZ),
     "moe_decode_workspace_init": ([_VP, _VP, _SZ, _VP], _I32),
     "moe_layer_decode": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP], _I32),
@@ -261,6 +264,64 @@ def moe_layer_decode(shape, X, W_r, bias, logits, Y, arena, routes: dict, ws, st
                                    _stream(stream)))
 
 
+_VAL_DTYPE = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
+
+
+def _mx_views(values, codes, scales):
+    """rows, K and row stride of [..., K] values and their blocks; leading
+    dimensions that one row stride covers count as rows."""
+    if values.dtype not in _VAL_DTYPE:
+        raise ValueError("values must be float32 or bfloat16")
+    K = values.shape[-1]
+    rows = values.numel() // K if K else 0
+    for t, cols, name in ((codes, K // 2, "codes"), (scales, K // 32, "scales")):
+        if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != rows * cols or K % 32:
+            raise ValueError(f"{name}: need contiguous uint8 [rows][{cols}], K a multiple of 32")
+    if values.dim() == 2:
+        if values.stride(1) != 1:
+            raise ValueError("values: rows must be contiguous")
+        ld = row_stride(values)
+    elif values.is_contiguous():
+        ld = K
+    else:
+        raise ValueError("values: only a matrix may have a row stride")
+    return rows, K, ld
+
+
+def moe_quantize_mxfp4(values, codes, scales, stream=None):
+    rows, K, ld = _mx_views(values, codes, scales)
+    _check(load().moe_quantize_mxfp4(_ptr(values), _VAL_DTYPE[values.dtype], rows, K, ld, _ptr(codes), _ptr(scales),
+                                     _stream(stream)))
+
+
+def moe_dequantize_mxfp4(codes, scales, values, stream=None):
+    rows, K, ld = _mx_views(values, codes, scales)
+    _check(load().moe_dequantize_mxfp4(_ptr(codes), _ptr(scales), rows, K, _ptr(values), _VAL_DTYPE[values.dtype], ld,
+                                       _stream(stream)))
+
+
+def moe_matmul_mxfp4(A_codes, A_scales, B, C, slot_offset=None, row_index=None, stream=None):
+    """C [M][N] = rows of A times the packed slices B [P][bytes] (or one slice
+    [bytes]); A_codes uint8 [A_rows][K/2], A_scales uint8 [A_rows][K/32]."""
+    A_rows, K = A_codes.shape[0], 2 * A_codes.shape[1]
+    M, N = C.shape
+    P = 1 if B.dim() == 1 else B.shape[0]
+    if A_codes.dtype != torch.uint8 or A_scales.dtype != torch.uint8 or B.dtype != torch.uint8:
+        raise ValueError("A_codes, A_scales and B must be uint8")
+    if not A_codes.is_contiguous() or not A_scales.is_contiguous() or tuple(A_scales.shape) != (A_rows, K // 32):
+        raise ValueError("A_codes [A_rows][K/2] and A_scales [A_rows][K/32] must be contiguous")
+    if C.dtype not in _VAL_DTYPE or C.stride(1) != 1 or (M > 1 and C.stride(0) < N):
+        raise ValueError("C must be float32 or bfloat16 with contiguous rows")
+    if B.shape[-1] < fp4_slice_bytes(N, K) or B.stride(-1) != 1:
+        raise ValueError("B: a slice is smaller than [N][K]")
+    for t, n, name in ((slot_offset, P + 1, "slot_offset"), (row_index, M, "row_index")):
+        if t is not None and (t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous()):
+            raise ValueError(f"{name}: need int32 [{n}]")
+    _check(load().moe_matmul_mxfp4(M, N, K, _ptr(A_codes), _ptr(A_scales), A_rows, _ptr(row_index), _ptr(slot_offset), P,
+                                   _ptr(B), B.stride(0) if B.dim() > 1 else B.numel(), _ptr(C), _VAL_DTYPE[C.dtype],
+                                   row_stride(C), _stream(stream)))
+
+
 def moe_pack_gate_up(shape, Wg, Wu, dst, n, src_stride, dst_stride, stream=None):
     _check(load().moe_pack_gate_up(ctypes.byref(shape), _ptr(Wg), _ptr(Wu), _ptr(dst), n,
                                    src_stride, dst_stride, _stream(stream)))
@@ -325,8 +386,8 @@ def moe_selftest_mfma_layout(out, stream=None):
 
 # ------------------------------------------------------- buffer helpers --
 def row_stride(t: torch.Tensor) -> int:
-    """Elements between rows; a single row's stride says nothing."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (t.shape[1] + 7) // 8 * 8)
+    """Elements between rows; a single row's stride says nothing, any aligned one does."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
 
 
 def check_rows(t: torch.Tensor, dtype, cols: int, name: str) -> None:
@@ -409,14 +470,29 @@ class Arena:
 
     def load_resident(self, Wg, Wu, Wd, phi: Sequence[int], stream=None, scales=None):
         """Pack and publish every expert e with phi[e] >= 0 into slot phi[e].
-        scales: (Sg, Su, Sd) row scales (fp8 codes) or block scales (MXFP4)."""
+        scales: (Sg, Su, Sd) row scales (fp8 codes) or block scales (MXFP4).
+        An MXFP4 arena takes fp32 or bf16 weights too, without scales: they
+        are quantised on the way (moe_quantize_mxfp4)."""
+        quantise = self.shape.dtype == MOE_DT_BF16_FP4W and scales is None and Wg.dtype in _VAL_DTYPE
         for e, s in enumerate(phi):
             if s < 0:
                 continue
-            g, u, dn = expert_slices(Wg, Wu, Wd, scales, e)
+            if quantise:
+                g, u, dn = (mxfp4_slice(W[e], stream) for W in (Wg, Wu, Wd))
+            else:
+                g, u, dn = expert_slices(Wg, Wu, Wd, scales, e)
             moe_pack_gate_up(self.shape, g, u, self.plane_gu[s], 1, 0, 0, stream)
             moe_pack_down(self.shape, dn, self.plane_d[s], 1, 0, 0, stream)
             arena_publish_slot(self, s, e, stream)
+
+
+def mxfp4_slice(W, stream=None) -> torch.Tensor:
+    """W [N][K] (fp32 or bf16) as a source slice of the packing calls: MXFP4
+    codes [N][K/2], then scale bytes [N][K/32]."""
+    N, K = W.shape
+    out = torch.empty(N * K // 2 + N * K // 32, dtype=torch.uint8, device=W.device)
+    moe_quantize_mxfp4(W, out[: N * K // 2], out[N * K // 2:], stream)
+    return out
 
 
 def expert_slices(Wg, Wu, Wd, scales, e):

@@ -22,6 +22,7 @@
 
 #include "common.h"
 #include "decode.h"
+#include "mxfp4.h"
 #include "residency.h"
 
 using namespace moe;
@@ -709,6 +710,93 @@ moe_status moe_selftest_mfma_layout(float *out, moe_stream stream)
 {
     if (!out) return fail(MOE_ERR_INVALID_ARG, "out is NULL");
     HIP_TRY(launch_selftest_mfma(out, S(stream)), "self-test launch");
+    return MOE_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// MXFP4 operators
+
+namespace {
+
+moe_status check_mx_values(const char *what, const void *v, int32_t dt, int64_t rows, int32_t K, int64_t ld,
+                           const void *codes, const void *scales)
+{
+    if (dt != MOE_DT_F32 && dt != MOE_DT_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "%s: val_dtype must be MOE_DT_F32 or MOE_DT_BF16", what);
+    if (rows < 0 || K <= 0 || ld < K) return fail(MOE_ERR_INVALID_ARG, "%s: bad sizes", what);
+    if (K % kWK != 0) return fail(MOE_ERR_UNSUPPORTED, "%s: K must be a multiple of 32", what);
+    // one thread per 8 values, at most 2^32 - 1 threads a launch
+    if (rows > ((int64_t)1 << 34) / K) return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^34 values", what);
+    if (rows > 0 && (!v || !codes || !scales)) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    const int esz = dt == MOE_DT_F32 ? 4 : 2;
+    if (!aligned(v, 16) || (ld * esz) % 16 != 0 || !aligned(codes, 16))
+        return fail(MOE_ERR_INVALID_ARG, "%s: values, their row stride and codes must be 16-byte aligned", what);
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_quantize_mxfp4(const void *values, int32_t val_dtype, int64_t rows, int32_t K, int64_t ld,
+                              void *codes, void *scales, moe_stream stream)
+{
+    MOE_TRY(check_mx_values("quantize", values, val_dtype, rows, K, ld, codes, scales));
+    HIP_TRY(launch_quantize_mxfp4(values, val_dtype == MOE_DT_BF16, rows, K, ld, (uint8_t *)codes, (uint8_t *)scales,
+                                  S(stream)),
+            "quantize launch");
+    return MOE_OK;
+}
+
+moe_status moe_dequantize_mxfp4(const void *codes, const void *scales, int64_t rows, int32_t K, void *values,
+                                int32_t val_dtype, int64_t ld, moe_stream stream)
+{
+    MOE_TRY(check_mx_values("dequantize", values, val_dtype, rows, K, ld, codes, scales));
+    HIP_TRY(launch_dequantize_mxfp4((const uint8_t *)codes, (const uint8_t *)scales, rows, K, values,
+                                    val_dtype == MOE_DT_BF16, ld, S(stream)),
+            "dequantize launch");
+    return MOE_OK;
+}
+
+moe_status moe_matmul_mxfp4(int32_t M, int32_t N, int32_t K, const void *A_codes, const void *A_scales,
+                            int32_t A_rows, const int32_t *row_index, const int32_t *slot_offset, int32_t P,
+                            const void *B, int64_t B_stride, void *C, int32_t c_dtype, int64_t ldc, moe_stream stream)
+{
+    if (M < 0 || N <= 0 || K <= 0 || A_rows < 0 || P < 1 || P > kMaxExp)
+        return fail(MOE_ERR_INVALID_ARG, "matmul: bad sizes M=%d N=%d K=%d A_rows=%d P=%d", M, N, K, A_rows, P);
+    if (N % 64 != 0 || K % 64 != 0) return fail(MOE_ERR_UNSUPPORTED, "matmul: N and K must be multiples of 64");
+    if (c_dtype != MOE_DT_F32 && c_dtype != MOE_DT_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "matmul: c_dtype must be MOE_DT_F32 or MOE_DT_BF16");
+    if (ldc < N) return fail(MOE_ERR_INVALID_ARG, "matmul: ldc below N");
+    if (!slot_offset && P != 1) return fail(MOE_ERR_INVALID_ARG, "matmul: slot_offset is required for P > 1");
+    if (M == 0) return MOE_OK;
+    if (A_rows < 1 || (!row_index && A_rows < M)) return fail(MOE_ERR_INVALID_ARG, "matmul: A has too few rows");
+    if (!A_codes || !A_scales || !B || !C) return fail(MOE_ERR_INVALID_ARG, "matmul: NULL pointer");
+    const int esz = c_dtype == MOE_DT_F32 ? 4 : 2;
+    if (!aligned(A_codes, 16) || !aligned(A_scales, 2) || !aligned(B, 16) || !aligned(C, 16) || (ldc * esz) % 16 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "matmul: A, B, C and C's row stride must be 16-byte aligned");
+    if (P > 1 && (B_stride < fp4_slice_bytes(N, K) || B_stride % 16 != 0))
+        return fail(MOE_ERR_INVALID_ARG, "matmul: B_stride must hold a slice and be a multiple of 16");
+    // 256 threads per 64 x 64 tile, at most 2^32 - 1 threads a launch
+    if (((int64_t)M / 64 + P + 1) * (N / 64) >= (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "matmul: too many tiles");
+    MxArgs a{};
+    a.A = (const uint8_t *)A_codes;
+    a.As = (const uint8_t *)A_scales;
+    a.A_rows = A_rows;
+    a.row_index = row_index;
+    a.slot_offset = slot_offset;
+    a.P = P;
+    a.B = (const uint8_t *)B;
+    a.B_stride = B_stride;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.C = C;
+    a.c_bf16 = c_dtype == MOE_DT_BF16;
+    a.ldc = ldc;
+    HIP_TRY(launch_matmul_mxfp4(a, S(stream)), "matmul launch");
     return MOE_OK;
 }
 

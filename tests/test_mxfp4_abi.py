@@ -1,0 +1,68 @@
+"""The MXFP4 operators' checks of their arguments, on the CPU: every call
+below ends in its checks, before any GPU work."""
+import pytest
+import torch
+
+from routed_expert_ffn_top_amd import binding as B
+
+INV, UN = B.MOE_ERR_INVALID_ARG, B.MOE_ERR_UNSUPPORTED
+L = B.load()
+
+
+@pytest.mark.parametrize("call", [L.moe_quantize_mxfp4, L.moe_dequantize_mxfp4], ids=["quantize", "dequantize"])
+def test_values_and_blocks(call):
+    def status(v=0x1000, dt=B.MOE_DT_BF16, rows=4, K=64, ld=64, codes=0x2000, scales=0x3000):
+        if call is L.moe_quantize_mxfp4:
+            return call(v, dt, rows, K, ld, codes, scales, None)
+        return call(codes, scales, rows, K, v, dt, ld, None)
+    assert status(rows=0, v=None, codes=None, scales=None) == B.MOE_OK     # nothing to do
+    assert status(dt=B.MOE_DT_BF16_FP4W) == INV
+    assert status(rows=-1) == INV
+    assert status(K=0) == INV and status(K=-32) == INV
+    assert status(ld=63) == INV
+    assert status(K=48) == UN
+    assert status(rows=1 << 30, K=32, ld=32) == UN                         # 2^35 values
+    for k in ("v", "codes", "scales"):
+        assert status(**{k: None}) == INV
+    assert status(v=0x1008) == INV and status(codes=0x2008) == INV
+    assert status(ld=68) == INV                                            # rows 136 bytes apart
+    assert status(dt=B.MOE_DT_F32, ld=66) == INV
+
+
+def test_matmul_refusals():
+    base = dict(M=4, N=64, K=64, A=0x1000, As=0x2000, rows=4, ri=None, off=None, P=1, W=0x4000, stride=0, C=0x8000,
+                dt=B.MOE_DT_F32, ldc=64)
+
+    def status(**kw):
+        a = dict(base, **kw)
+        return L.moe_matmul_mxfp4(a["M"], a["N"], a["K"], a["A"], a["As"], a["rows"], a["ri"], a["off"], a["P"], a["W"],
+                                  a["stride"], a["C"], a["dt"], a["ldc"], None)
+    assert status(M=0, A=None, As=None, W=None, C=None, rows=0) == B.MOE_OK
+    for kw in (dict(M=-1), dict(N=0), dict(K=0), dict(rows=-1), dict(P=0), dict(P=513, off=0x10), dict(dt=B.MOE_DT_BF16_FP4W),
+               dict(ldc=63), dict(P=2, stride=4096), dict(rows=3), dict(rows=0, ri=0x10), dict(A=None), dict(As=None),
+               dict(W=None), dict(C=None), dict(A=0x1008), dict(As=0x2001), dict(W=0x4008), dict(C=0x8004),
+               dict(ldc=66), dict(dt=B.MOE_DT_BF16, ldc=68), dict(P=2, off=0x10, stride=2175), dict(P=2, off=0x10, stride=2184)):
+        assert status(**kw) == INV, kw
+    for kw in (dict(N=96), dict(K=96), dict(M=1 << 30, rows=1 << 30)):
+        assert status(**kw) == UN, kw
+
+
+def test_binding_refuses_other_layouts():
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    x = torch.zeros(4, 64)
+    with pytest.raises(ValueError):
+        B.moe_quantize_mxfp4(x.half(), u8(4, 32), u8(4, 2))
+    with pytest.raises(ValueError):
+        B.moe_quantize_mxfp4(x, u8(4, 31), u8(4, 2))
+    with pytest.raises(ValueError):
+        B.moe_quantize_mxfp4(x, u8(4, 32), u8(4, 4)[:, :2])
+    with pytest.raises(ValueError):
+        B.moe_quantize_mxfp4(torch.zeros(64, 4).t(), u8(4, 32), u8(4, 2))
+    with pytest.raises(ValueError):
+        B.moe_quantize_mxfp4(torch.zeros(2, 2, 128)[..., :64], u8(4, 32), u8(4, 2))
+    ok = dict(A_codes=u8(4, 32), A_scales=u8(4, 2), B=u8(B.fp4_slice_bytes(64, 64)), C=torch.zeros(4, 64))
+    for kw in (dict(A_scales=u8(4, 3)), dict(B=u8(B.fp4_slice_bytes(64, 64) - 1)), dict(C=torch.zeros(64, 4).t()),
+               dict(C=torch.zeros(4, 64).half()), dict(row_index=torch.zeros(4, dtype=torch.int64)),
+               dict(row_index=torch.zeros(3, dtype=torch.int32)), dict(slot_offset=torch.zeros(1, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            B.moe_matmul_mxfp4(**dict(ok, **kw))

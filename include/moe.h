@@ -350,18 +350,19 @@ moe_status moe_layer_prefill_noalloc(const moe_shape *shape, const void *X,
  * in fp32: unlike the prompt layer's bf16 H, H is not rounded, so the outputs
  * of the two differ by that rounding. Each expert hit is read once. Y is
  * bitwise run-to-run identical and independent of phi and P.
- *   shape    T <= MOE_DECODE_MAX_T tokens, T * K' <= MOE_DECODE_MAX_ROUTES
+ *   shape    T <= MOE_DECODE_MAX_T tokens, T * K' <= MOE_DECODE_MAX_ROUTES,
+ *            d <= MOE_DECODE_MAX_D, a packed gate/up slice below 2 GiB
  *            (MOE_ERR_UNSUPPORTED otherwise); every dtype; `capacity` is not
  *            used. T, k, ldx and ldy may differ from the arena's shape.
  *   X        16-byte aligned; fp32 X needs ldx % 4 == 0
  *   W_r, bias, logits, Y: as in moe_layer_prefill
  *   routes   topk_idx and topk_w [T][K'] are written; the other descriptors
  *            are neither read nor written and may be NULL
- *   ws       at least moe_decode_workspace_bytes(shape) bytes, prepared once
- *            by moe_decode_workspace_init with any shape at least as large in
- *            T; 256-byte aligned. Its contents do not outlive a call, so one
- *            workspace may serve any number of layers and of shapes with no
- *            more bytes, one call at a time (calls on several streams, or
+ *   ws       at least moe_decode_workspace_bytes(shape) bytes, 256-byte
+ *            aligned, prepared once by moe_decode_workspace_init. Between
+ *            calls it holds nothing but cleared counters, so one workspace
+ *            may serve any number of layers, and of shapes that need no more
+ *            bytes, one call at a time (calls on several streams, or
  *            graphs replayed on several, need one each).
  * Into a stream that is being captured the call records its kernels only, no
  * event: every slot's load must have completed by then (MOE_ERR_SLOT_STATE
@@ -370,6 +371,7 @@ moe_status moe_layer_prefill_noalloc(const moe_shape *shape, const void *X,
  */
 #define MOE_DECODE_MAX_T 64
 #define MOE_DECODE_MAX_ROUTES 1024
+#define MOE_DECODE_MAX_D 131072
 size_t moe_decode_workspace_bytes(const moe_shape *shape);
 moe_status moe_decode_workspace_init(const moe_shape *shape, void *ws,
                                      size_t ws_bytes, moe_stream stream);

@@ -48,6 +48,7 @@ MOE_SLOT_AVAILABLE, MOE_SLOT_FILLING, MOE_SLOT_READY, MOE_SLOT_IN_USE = 0, 1, 2,
 MOE_MAX_EXPERTS = 512
 MOE_DECODE_MAX_T = 64
 MOE_DECODE_MAX_ROUTES = 1024
+MOE_DECODE_MAX_D = 131072
 
 
 class MoEError(RuntimeError):

@@ -812,6 +812,9 @@ moe_status check_decode_shape(const moe_shape *s)
     MOE_TRY(check_shape(s));
     if (s->T > kDecMaxT || (int64_t)s->T * (s->k + s->n_shared) > kDecMaxRoutes)
         return fail(MOE_ERR_UNSUPPORTED, "decode: needs T <= %d and T * (k + n_shared) <= %d", kDecMaxT, kDecMaxRoutes);
+    if (gu_slice_bytes(*s) >= (size_t)1 << 31)
+        return fail(MOE_ERR_UNSUPPORTED, "decode: an expert's gate/up slice must be below 2 GiB");
+    if (s->d > kDecMaxD) return fail(MOE_ERR_UNSUPPORTED, "decode: needs d <= %d", kDecMaxD);
     return MOE_OK;
 }
 
@@ -829,17 +832,33 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
                        const float *logits, float *Y, const moe_arena *a, const PhiArg &phi, const moe_routes &r,
                        void *ws, hipStream_t st)
 {
-    const float *L = logits;
-    if (W_r) {
-        float *own = ws_at<float>(ws, w.logits);
-        HIP_TRY(TIMED(MOE_KERNEL_ROUTER, st, launch_router_logits(s, X, W_r, bias, own, st)), "router launch");
-        L = own;
-    }
-    HIP_TRY(TIMED(MOE_KERNEL_TOPK, st, launch_topk(s, 0, s.T, L, r.topk_idx, r.topk_w, nullptr, st)), "top-k launch");
-    int32_t *list = ws_at<int32_t>(ws, w.list);
+    int32_t *list = ws_at<int32_t>(ws, w.list), *ctr = ws_at<int32_t>(ws, w.ctr);
+    const DecLists lists{list, list + 1, list + 1 + kMaxExp, list + 1 + 2 * kMaxExp, list + 1 + 3 * kMaxExp};
+    DecRouteArgs q{};
+    q.X = X;
+    q.ldx = s.ldx;
+    q.Wr = W_r;
+    q.bias = bias;
+    q.given = logits;
+    q.logits = ws_at<float>(ws, w.logits);
+    q.T = s.T;
+    q.d = s.d;
+    q.E = s.E;
+    q.k = s.k;
+    q.n_shared = s.n_shared;
+    q.renorm = s.renorm;
+    q.P = s.P;
+    q.idx = r.topk_idx;
+    q.w = r.topk_w;
+    q.ctr = ctr;
+    q.l = lists;
+    HIP_TRY(TIMED(MOE_KERNEL_ROUTER, st, launch_dec_route(s, q, phi, st)), "route launch");
     DecArgs g{};
-    g.l = DecLists{list, list + 1, list + 1 + kMaxExp, list + 1 + 2 * kMaxExp, list + 1 + 3 * kMaxExp};
-    HIP_TRY(launch_dec_lists(s, r.topk_idx, phi, g.l, st), "route list launch");
+    g.l = lists;
+    g.T = s.T;
+    g.Y = Y;
+    g.ldy = s.ldy;
+    g.ctr = ctr + 1 + kDecMaxT;
     g.kp = s.k + s.n_shared;
     g.R = s.T * g.kp;
     g.topk_w = r.topk_w;
@@ -849,6 +868,7 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
     g.W = a->plane_gu;
     g.slot_bytes = a->stride_gu * a->esz;
     g.scale_off = (int64_t)2 * s.f * s.d;
+    g.slice_bytes = (int64_t)gu_slice_bytes(s);
     g.N = 2 * s.f;
     g.K = s.d;
     g.out = ws_at<char>(ws, w.H);
@@ -859,12 +879,12 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
     h.W = a->plane_d;
     h.slot_bytes = a->stride_d * a->esz;
     h.scale_off = (int64_t)s.d * s.f;
+    h.slice_bytes = (int64_t)d_slice_bytes(s);
     h.N = s.d;
     h.K = s.f;
     h.out = ws_at<char>(ws, w.Yr);
     h.ldo = s.d;
     HIP_TRY(TIMED(MOE_KERNEL_DOWN, st, launch_dec_proj(s, h, false, st)), "down launch");
-    HIP_TRY(TIMED(MOE_KERNEL_COMBINE, st, launch_dec_combine(s, Y, ws_at<float>(ws, w.Yr), st)), "combine launch");
     return MOE_OK;
 }
 
@@ -883,7 +903,7 @@ moe_status moe_decode_workspace_init(const moe_shape *shape, void *ws, size_t ws
     MOE_TRY(check_decode_shape(shape));
     DecLayout w;
     MOE_TRY(check_decode_ws(shape, ws, ws_bytes, &w));
-    (void)stream;
+    HIP_TRY(launch_fill_i32(ws_at<int32_t>(ws, w.ctr), 0, 1 + kDecMaxT + kDecMaxD / kDecRows, S(stream)), "fill launch");
     return MOE_OK;
 }
 

@@ -8,8 +8,15 @@ namespace moe {
 constexpr int kDecMaxT = MOE_DECODE_MAX_T;             // a slot has at most this many rows
 constexpr int kDecMaxRoutes = MOE_DECODE_MAX_ROUTES;   // T * K'
 
-// Byte offsets of the decode workspace's regions.
+constexpr int kDecRows = 32;                           // fewest output columns per workgroup (one counter each)
+constexpr int kDecMaxD = MOE_DECODE_MAX_D;
+
+// Byte offsets of the decode workspace's regions. The counters stand first and
+// have one size, so that they stay where they are when the shape changes: they
+// are zero between calls (cleared once by moe_decode_workspace_init; the last
+// workgroup to arrive at a counter clears it).
 struct DecLayout {
+    size_t ctr;      // int32: [0] token blocks routed, then per token block, then per column chunk of the output
     size_t logits;   // float[T][E]
     size_t list;     // int32: [0] slots with routes, then the DecLists arrays
     size_t H;        // fp32 layers: float[R][f]; bf16 layers: uint16[3][R][f], H as a sum of three bf16 terms
@@ -22,6 +29,7 @@ inline DecLayout dec_layout(const moe_shape &s)
     DecLayout w{};
     const size_t R = (size_t)s.T * (s.k + s.n_shared);
     size_t o = 0;
+    w.ctr = o;    o = align_up(o + (size_t)(1 + kDecMaxT + kDecMaxD / kDecRows) * 4, 256);
     w.logits = o; o = align_up(o + (size_t)s.T * s.E * 4, 256);
     w.list = o;   o = align_up(o + (size_t)(1 + 3 * kMaxExp + kDecMaxRoutes) * 4, 256);
     w.H = o;      o = align_up(o + R * s.f * (act_bf16(s) ? 6 : 4), 256);
@@ -43,14 +51,31 @@ struct DecArgs {
     const char *W;        // plane base
     int64_t slot_bytes;   // bytes between slots
     int64_t scale_off;    // fp8: bytes from a slice's start to its row scales
-    int N, K, kp, R, nchunk;
+    int64_t slice_bytes;  // of one slice, below 2^31
+    int N, K, kp, R, nchunk, slots;
     void *out;            // gate/up: H; down: Yr
     int64_t ldo;
     const float *topk_w;
+    float *Y;             // down: the tokens' rows, their routes' sums added
+    int64_t ldy;
+    int T;
+    int32_t *ctr;         // down: arrivals per chunk
 };
 
-hipError_t launch_dec_lists(const moe_shape &s, const int32_t *idx, const PhiArg &phi, const DecLists &l, hipStream_t st);
+struct DecRouteArgs {
+    const void *X;
+    int64_t ldx;
+    const float *Wr, *bias;   // Wr null: logits holds the caller's
+    const float *given;
+    float *logits;
+    int T, d, E, k, n_shared, renorm, P;
+    int32_t *idx;
+    float *w;
+    int32_t *ctr;
+    DecLists l;
+};
+
+hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const PhiArg &phi, hipStream_t st);
 hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a, bool gateup, hipStream_t st);
-hipError_t launch_dec_combine(const moe_shape &s, float *Y, const float *Yr, hipStream_t st);
 
 }  // namespace moe

@@ -23,9 +23,13 @@
 // H is kept to full fp32 between the projections: it is written as three bf16
 // terms h = h1 + h2 + h3 of 8 bits each, cut (not rounded) from fp32, which
 // is exact, and the down projection multiplies each weight operand by all
-// three. Three instructions instead of one cost nothing beside the weights'
-// load. fp32 layers keep H as fp32 and use the fp32 matrix instruction.
+// three. A slot with at most 5 routes takes them as 15 of the 16 columns of one
+// operand (column 3 i + j: term j of route i); with more routes the three terms
+// are three instructions. Either way each term has its own sums, joined in one
+// order, so a token's bits hang on nothing but the token. fp32 layers keep H
+// as fp32 and use the fp32 matrix instruction.
 #include <algorithm>
+#include <type_traits>
 
 #include "decode.h"
 
@@ -39,47 +43,269 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 enum { W_F32 = 0, W_BF16 = 1, W_FP8 = 2, W_FP4 = 3 };
 
-// One workgroup: the routes sorted by slot. Thread s counts slot s's routes,
-// then places them; R <= 1024.
-__global__ __launch_bounds__(kMaxExp) void k_dec_lists(const int32_t *__restrict__ idx, int R, int P, PhiArg phi,
-                                                       DecLists l)
+// ---- values handed from workgroup to workgroup within a launch ----
+// The compute dies have an L2 each. A release or acquire at device scope
+// writes back or drops a whole L2, which costs every other workgroup there its
+// lines (measured: 2048 arrivals made the MXFP4 down projection 87 us instead
+// of 35). So what is handed over is stored and loaded past the L2, value by
+// value (relaxed atomics at device scope), and an arrival only has to wait for
+// its own stores.
+template <typename T>
+__device__ __forceinline__ void put(T *p, T v)
 {
-    __shared__ int32_t key[kDecMaxRoutes];
-    __shared__ int32_t wsum[2][kMaxExp / 64];
-    const int s = threadIdx.x, lane = s & 63, wave = s >> 6;
-    for (int i = s; i < R; i += kMaxExp) key[i] = phi.v[idx[i]];
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T>
+__device__ __forceinline__ T get(const T *p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Every wave's put()s are complete, then one thread adds 1 to the counter.
+// True for the workgroup whose arrival is the last of `all`, which may get()
+// what the others put; it clears the counter for the next call. Nobody waits.
+__device__ __forceinline__ bool last_to_arrive(int32_t *ctr, int all)
+{
+    __shared__ int32_t s_last;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0);   // the stores have reached memory
     __syncthreads();
-    int cnt = 0;
-    if (s < P)
-        for (int i = 0; i < R; ++i) cnt += key[i] == s;
-    // exclusive prefixes over slots of the route counts and of the slots in use
-    int off = cnt, pos = cnt > 0;
+    if (threadIdx.x == 0) {
+        const int n = __hip_atomic_fetch_add(ctr, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = n == all - 1;
+        if (s_last) put(ctr, 0);
+    }
+    __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    return s_last != 0;
+}
+
+__device__ __forceinline__ float wave_max(float v)
+{
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// Order-preserving 64-bit key of (logit, expert): larger logit first, equal
+// ones by lower id; NaN as -infinity, -0 as +0.
+__device__ __forceinline__ uint64_t topk_key(float x, int e)
+{
+    if (x != x) x = -__builtin_huge_valf();
+    if (x == 0.0f) x = 0.0f;
+    const uint32_t u = __float_as_uint(x);
+    return ((uint64_t)((u & 0x80000000u) ? ~u : (u | 0x80000000u)) << 32) | (uint32_t)~(uint32_t)e;
+}
+
+// Router, top-k and the routes by slot, in one launch. A workgroup takes 4
+// tokens x 16 experts (a wave 4 experts, 16 lanes each): lane p of an expert
+// holds the partial sum p of the router's fixed order (runs of 8 hidden
+// indices, run r to partial sum r mod 16, ascending, one fused multiply-add a
+// term), so a wave's loads are whole 512-byte stretches of W_r and the bits
+// are the prompt router's. The last workgroup of a token block does its top-k
+// (a wave a token, the prompt kernel's arithmetic), and the last block of all
+// sorts the routes by slot. The order of the routes within a slot is that of
+// LDS atomics and is not fixed: it only says which column of a matrix operand
+// a route takes, and columns do not mix. Bound by latency: W_r is 0.5 MB.
+template <typename TX, int C, int TB>
+__global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
+{
+    constexpr int XE = 16 / sizeof(TX), XV = 8 / XE;   // x values per 16 bytes, 16-byte pieces per run
+    __shared__ float part[4][TB][64];
+    __shared__ uint64_t keys[4][64 * C + 2];
+    __shared__ int32_t cnt[kMaxExp], off[kMaxExp], wsum[2][4], sphi[kMaxExp];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int t0 = blockIdx.x * TB, nt = min(TB, a.T - t0);
+    const int kp = a.k + a.n_shared;
+    if (a.Wr) {
+        const int e0 = blockIdx.y * 16 + wave * 4, p = lane & 15, d = a.d;
+        const int e = min(e0 + (lane >> 4), a.E - 1);
+        const float *w = a.Wr + (int64_t)e * d + p * 8;
+        const TX *x[TB];
+#pragma unroll
+        for (int t = 0; t < TB; ++t) x[t] = (const TX *)a.X + (int64_t)min(t0 + t, a.T - 1) * a.ldx + p * 8;
+        float acc[TB];
+#pragma unroll
+        for (int t = 0; t < TB; ++t) acc[t] = 0.0f;
+        constexpr int U = TB == 1 ? 64 / sizeof(TX) / 4 : 4;   // groups of 128 hidden indices in flight
+        const int ng = (d + 127) / 128;
+        for (int g = 0; g < ng; g += U) {
+            u32x4_t wv[U][2], xv[U][TB][XV];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                // pieces at or past d are read from the row start and not used
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int i = (g + u) * 128 + 4 * h;
+                    wv[u][h] = *(const u32x4_t *)(w + (i + p * 8 < d ? i : -p * 8));
+                }
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+#pragma unroll
+                    for (int h = 0; h < XV; ++h) {
+                        const int i = (g + u) * 128 + XE * h;
+                        if (t == 0 || t < nt) xv[u][t][h] = *(const u32x4_t *)(x[t] + (i + p * 8 < d ? i : -p * 8));
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    if ((g + u) * 128 + p * 8 + c >= d) continue;
+                    const float wc = __uint_as_float(wv[u][c >> 2][c & 3]);
+#pragma unroll
+                    for (int t = 0; t < TB; ++t) {
+                        if (t > 0 && t >= nt) continue;
+                        float xc;
+                        if constexpr (sizeof(TX) == 2) {
+                            const uint32_t w2 = xv[u][t][0][c >> 1];
+                            xc = __uint_as_float((c & 1) ? (w2 & 0xffff0000u) : (w2 << 16));
+                        } else {
+                            xc = __uint_as_float(xv[u][t][c >> 2][c & 3]);
+                        }
+                        acc[t] = __builtin_fmaf(xc, wc, acc[t]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < TB; ++t) part[wave][t][lane] = acc[t];
+        __builtin_amdgcn_wave_barrier();   // the reads below are of this wave's writes
+        // lane (t, expert): the 16 partial sums in ascending order
+        const int t = lane >> 2, es = lane & 3;
+        if (lane < 4 * nt && e0 + es < a.E) {
+            float s = part[wave][t][es * 16];
+#pragma unroll
+            for (int c = 1; c < 16; ++c) s = s + part[wave][t][es * 16 + c];
+            put(a.logits + (int64_t)(t0 + t) * a.E + e0 + es, a.bias ? s + a.bias[e0 + es] : s);
+        }
+        if (gridDim.y > 1 && !last_to_arrive(a.ctr + 1 + blockIdx.x, gridDim.y)) return;
+        __syncthreads();
+    }
+
+    // top-k of this block's tokens, a wave a token
+    if (wave < nt) {
+        const float *L = (a.Wr ? a.logits : a.given) + (int64_t)(t0 + wave) * a.E;
+        const float NEG_INF = -__builtin_huge_valf();
+        float v[C];
+        uint64_t key[C];
+        int rank[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = lane + 64 * c;
+            v[c] = e < a.E ? get(L + e) : NEG_INF;
+            if (v[c] != v[c]) v[c] = NEG_INF;
+            key[c] = topk_key(v[c], e);
+            keys[wave][e] = e < a.E ? key[c] : 0ull;
+            rank[c] = 0;
+        }
+        if (lane < 2) keys[wave][64 * C + lane] = 0ull;
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 8
+        for (int e2 = 0; e2 < ((a.E + 1) & ~1); e2 += 2) {
+            const uint64_t k0 = keys[wave][e2], k1 = keys[wave][e2 + 1];
+#pragma unroll
+            for (int c = 0; c < C; ++c) rank[c] += (int)(k0 > key[c]) + (int)(k1 > key[c]);
+        }
+        float m = NEG_INF;
+#pragma unroll
+        for (int c = 0; c < C; ++c) m = fmaxf(m, v[c]);
+        m = wave_max(m);
+        if (m == NEG_INF) m = 0.0f;
+        float z[C], s = 0.0f, ssel = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = lane + 64 * c;
+            z[c] = e < a.E ? expf(v[c] - m) : 0.0f;
+            s += z[c];
+            if (e < a.E && rank[c] < a.k) ssel += z[c];
+        }
+        s = wave_sum(s);
+        ssel = wave_sum(ssel);
+        const float den = a.renorm ? ssel : s;
+        const int64_t r0 = (int64_t)(t0 + wave) * kp;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int e = lane + 64 * c;
+            if (e < a.E && rank[c] < a.k) {
+                put(a.idx + r0 + rank[c], e);
+                a.w[r0 + rank[c]] = den > 0.0f ? z[c] / den : 0.0f;
+            }
+        }
+        if (lane < a.n_shared) {
+            put(a.idx + r0 + a.k + lane, a.E + lane);
+            a.w[r0 + a.k + lane] = 1.0f;
+        }
+    }
+    if (gridDim.x > 1) {
+        if (!last_to_arrive(a.ctr, gridDim.x)) return;
+    } else {
+        __builtin_amdgcn_s_waitcnt(0);   // this workgroup's ids, read below past the caches
+    }
+
+    // the routes by slot: counts, offsets, places
+    for (int s = tid; s < kMaxExp; s += 256) {
+        cnt[s] = 0;
+        sphi[s] = phi.v[s];
+    }
+    __syncthreads();
+    const int R = a.T * kp;
+    constexpr int RT = kDecMaxRoutes / 256;
+    int slot[RT], pos[RT];
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+        const int i = tid + 256 * q;
+        if (i < R) {
+            slot[q] = sphi[get(a.idx + i)];
+            pos[q] = atomicAdd(&cnt[slot[q]], 1);
+        }
+    }
+    __syncthreads();
+    // thread tid: slots 2 tid and 2 tid + 1
+    const int c0 = cnt[2 * tid], c1 = cnt[2 * tid + 1];
+    int so = c0 + c1, sn = (c0 > 0) + (c1 > 0);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(off, o, 64), v = __shfl_up(pos, o, 64);
+        const int u = __shfl_up(so, o, 64), n = __shfl_up(sn, o, 64);
         if (lane >= o) {
-            off += u;
-            pos += v;
+            so += u;
+            sn += n;
         }
     }
     if (lane == 63) {
-        wsum[0][wave] = off;
-        wsum[1][wave] = pos;
+        wsum[0][wave] = so;
+        wsum[1][wave] = sn;
     }
     __syncthreads();
     for (int w = 0; w < wave; ++w) {
-        off += wsum[0][w];
-        pos += wsum[1][w];
+        so += wsum[0][w];
+        sn += wsum[1][w];
     }
-    if (s == kMaxExp - 1) *l.n_act = pos;
-    off -= cnt;
-    if (cnt > 0) {
-        l.slot[pos - 1] = s;
-        l.off[pos - 1] = off;
-        l.cnt[pos - 1] = cnt;
-        for (int i = 0; i < R; ++i)
-            if (key[i] == s) l.rec[off++] = i;
+    if (tid == 255) *a.l.n_act = sn;
+    so -= c0 + c1;
+    sn -= (c0 > 0) + (c1 > 0);
+    off[2 * tid] = so;
+    off[2 * tid + 1] = so + c0;
+    if (c0) {
+        a.l.slot[sn] = 2 * tid;
+        a.l.off[sn] = so;
+        a.l.cnt[sn] = c0;
+        ++sn;
     }
+    if (c1) {
+        a.l.slot[sn] = 2 * tid + 1;
+        a.l.off[sn] = so + c0;
+        a.l.cnt[sn] = c1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < RT; ++q)
+        if (tid + 256 * q < R) a.l.rec[off[slot[q]] + pos[q]] = tid + 256 * q;
 }
 
 // E8M0 scale byte -> fp32 2^(s-127); 255 is NaN
@@ -110,259 +336,440 @@ __device__ __forceinline__ bf16x8_t fp4_operand(uint32_t w, float scale)
     return __builtin_bit_cast(bf16x8_t, u);
 }
 
-constexpr int kDecRows = 64;    // rows of the slice per workgroup
+#ifndef DEC_U
+#define DEC_U (MT == 1 || (MT == 2 && PL == 1 && WF == W_BF16) ? 2 : 1)
+#endif
+#ifndef DEC_PRE
+#define DEC_PRE 48
+#endif
+#ifndef DEC_GRID
+#define DEC_GRID 512
+#endif
 constexpr int kDecWaves = 8;
+constexpr uint32_t kNowhere = 0x80000000u;   // a buffer offset past every slice: such a load gives zeros and reads nothing
+
+// Workgroup barrier that waits for this wave's LDS traffic only: loads in
+// flight stay so (gfx9 s_waitcnt encoding: vmcnt[3:0] | expcnt[6:4] |
+// lgkmcnt[11:8] | vmcnt[5:4] at bits 15:14).
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // WF: weight format. MT: 16-row groups of routes a slot can have (T <= 16 MT).
-template <int WF, int MT, bool GATEUP>
+// NT: 16-row groups of the slice per tile.
+//
+// The workgroups are persistent: each walks its tiles (slot, 16 NT rows) and
+// requests the next stretch of weights, of the same tile or of the next,
+// before it multiplies the present one, so that the loads never stop, not even
+// over a tile's joining of sums and its stores. The operand of the tokens is
+// requested before that next stretch: loads return in order, and the wait for
+// it then leaves the weights in flight. Weights come through buffer loads, whose
+// bounds check makes a stretch that is not there zeros without a branch, so
+// that the number of loads in flight is the same on every path.
+template <int WF, int MT, int NT, bool GATEUP>
 __global__ __launch_bounds__(kDecWaves * 64) void k_dec_proj(DecArgs a)
 {
-    constexpr int NT = kDecRows / 16;                                  // weight row groups
     constexpr int LK = WF == W_F32 ? 4 : WF == W_BF16 ? 8 : WF == W_FP8 ? 16 : 32;   // k values per lane and step
     constexpr int KS = 4 * LK;                                         // k values per step
     constexpr int NI = LK > 8 ? LK / 8 : 1;                            // bf16 operands of 8 per lane and step
     constexpr int PL = !GATEUP && WF != W_F32 ? 3 : 1;                 // terms of the second operand
-    constexpr int U = WF == W_FP4 ? 2 : 4;                             // steps in flight
+    constexpr int U = DEC_U; // steps per stretch
+    constexpr int ROWB = WF == W_F32 ? 0 : WF == W_BF16 ? 64 : WF == W_FP8 ? 32 : 16;   // bytes of a row in a K piece
     __shared__ f32x4_t red[kDecWaves][MT * NT][64];
+    __shared__ int32_t s_slot[kMaxExp], s_off[kMaxExp], s_cnt[kMaxExp], s_rec[kDecMaxRoutes];
 
-    const int act = blockIdx.x / a.nchunk, chunk = blockIdx.x % a.nchunk;
-    if (act >= *a.l.n_act) return;
-    const int slot = a.l.slot[act], off = a.l.off[act], cnt = a.l.cnt[act];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4;
-    const int K = a.K, N = a.N, n0 = chunk * kDecRows;
-    const int nmt = MT == 1 ? 1 : (cnt + 15) / 16;
-
-    // second operand rows of this lane: tokens (gate/up) or routes (down)
-    int64_t xoff[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int i = a.l.rec[off + min(16 * m + r, cnt - 1)];
-        xoff[m] = (int64_t)(GATEUP ? i / a.kp : i) * a.ldx;
+    const int K = a.K, N = a.N, nchunk = a.nchunk;
+    // entries past the last slot with routes are there, and not used
+    const int n_act = *a.l.n_act;
+    for (int i = tid; i < a.slots; i += kDecWaves * 64) {
+        s_slot[i] = a.l.slot[i];
+        s_off[i] = a.l.off[i];
+        s_cnt[i] = a.l.cnt[i];
     }
-    // the chunk's 64 rows lie in one 256-row block of the tiled slice
-    const int nb = n0 / kWRows, rows = min(kWRows, N - nb * kWRows);
-    const char *W = a.W + (int64_t)slot * a.slot_bytes;
-    int rb[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) rb[t] = min(n0 + 16 * t + r, N - 1) - nb * kWRows;
+    for (int i = tid; i < a.R; i += kDecWaves * 64) s_rec[i] = a.l.rec[i];
+    __syncthreads();
 
-    f32x4_t acc[MT][NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[m][t] = f32x4_t{0, 0, 0, 0};
+    // Tiles of this workgroup. Gate/up: every gridDim-th of all. Down: one
+    // column chunk (every gridDim-th, where there are more chunks than
+    // workgroups) and every `groups`-th slot, so that it arrives at each of
+    // its chunks once.
+    const int groups = GATEUP ? 1 : max(1, (int)gridDim.x / nchunk);
+    int chunk = blockIdx.x % nchunk, act = blockIdx.x / nchunk;
+    const int act0 = act;
+    auto advance = [&](int &ac, int &ch) {
+        if (GATEUP) {
+            const int g = ac * nchunk + ch + (int)gridDim.x;
+            ac = g / nchunk;
+            ch = g % nchunk;
+        } else {
+            ac += groups;
+            if (ac >= n_act && groups == 1) {
+                ac = 0;
+                ch += gridDim.x;
+                if (ch >= nchunk) ac = n_act;
+            }
+        }
+    };
+    if (!GATEUP && act0 >= groups) return;
+    if (act >= n_act) return;   // down: fewer slots than groups; the others arrive alone
 
     const int steps = (K + KS - 1) / KS;
     const int s0 = (int)((int64_t)steps * wave / kDecWaves), s1 = (int)((int64_t)steps * (wave + 1) / kDecWaves);
-    for (int s = s0; s < s1; s += U) {
+
+    // Where a tile's weights are: the slot's slice as a buffer, this lane's
+    // offset of step 0, and bytes from step to step.
+    struct Src {
+        __amdgpu_buffer_rsrc_t buf;
+        uint32_t at, sc_at, stride;
+        int rows, nb;
+    };
+    auto source = [&](int ac, int ch) {
+        Src p;
+        const int slot = __builtin_amdgcn_readfirstlane(s_slot[ac]);
+        p.buf = __builtin_amdgcn_make_buffer_rsrc((void *)(a.W + (int64_t)slot * a.slot_bytes), 0, (int)a.slice_bytes,
+                                                  0x00027000);
+        const int n0 = ch * (16 * NT);
+        p.nb = n0 / kWRows;
+        p.rows = min(kWRows, N - p.nb * kWRows);
+        const uint32_t rb = n0 - p.nb * kWRows + r;
+        if constexpr (WF == W_FP4) {
+            const uint32_t pb = (uint32_t)fp4_piece_bytes(p.rows);
+            p.at = (uint32_t)p.nb * (K / kWK) * (uint32_t)fp4_piece_bytes(kWRows) + q * pb;
+            p.sc_at = p.at + p.rows * 16 + rb;
+            p.at += rb * 16;
+            p.stride = 4 * pb;
+        } else {
+            p.at = (uint32_t)p.nb * kWRows * K * (ROWB / kWK) + rb * ROWB;
+            if constexpr (WF == W_FP8) p.at += (q & 1) * 16 + (q >> 1) * p.rows * ROWB;
+            if constexpr (WF == W_BF16) p.at += q * 16;
+            p.sc_at = 0;
+            p.stride = (WF == W_FP8 ? 2 : 1) * p.rows * ROWB;
+        }
+        return p;
+    };
+    struct Stretch {
         u32x4_t w[U][NT];
-        uint32_t sc[U][NT];
-        u32x4_t x[U][MT][PL][NI];
+        uint32_t sc[U][WF == W_FP4 ? NT : 1];
+    };
+    auto request = [&](Stretch &d, const Src &p, int s, bool any) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = (s + u) * KS + q * LK;
-            const bool in = s + u < s1 && k < K;
-            const int kc = in ? k : 0;
-            const int64_t piece = kc / kWK;
+            const bool in = any && s + u < s1 && k < K;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const char *p;
+                uint32_t at;
                 if constexpr (WF == W_F32) {
-                    const int wd = min(kWK, K - (int)piece * kWK);
-                    p = W + ((int64_t)nb * kWRows * K + piece * rows * kWK + (int64_t)rb[t] * wd + kc % kWK) * 4;
-                } else if constexpr (WF == W_BF16) {
-                    p = W + ((int64_t)nb * kWRows * K + piece * rows * kWK + rb[t] * kWK + kc % kWK) * 2;
-                } else if constexpr (WF == W_FP8) {
-                    p = W + (int64_t)nb * kWRows * K + piece * rows * kWK + rb[t] * kWK + kc % kWK;
+                    // K pieces of the last columns are narrower, and N may end inside the tile
+                    const int piece = k / kWK, wd = min(kWK, K - piece * kWK);
+                    const int rb = min((int)p.at / 1 + 16 * t, p.rows - 1);
+                    at = (uint32_t)(p.nb * kWRows * K + piece * p.rows * kWK + rb * wd + k % kWK) * 4;
                 } else {
-                    p = W + (int64_t)nb * (K / kWK) * fp4_piece_bytes(kWRows) + piece * fp4_piece_bytes(rows);
-                    sc[u][t] = *(const uint8_t *)(p + rows * 16 + rb[t]);
-                    p += rb[t] * 16;
+                    at = p.at + (uint32_t)(s + u) * p.stride + t * 16 * ROWB;
                 }
-                w[u][t] = *(const u32x4_t *)p;
-                if (!in) w[u][t] = u32x4_t{0, 0, 0, 0};
-                if (WF == W_FP4 && !in) sc[u][t] = 127;
+                d.w[u][t] = __builtin_amdgcn_raw_buffer_load_b128(p.buf, (int)(in ? at : kNowhere), 0, 0);
+                if constexpr (WF == W_FP4)
+                    d.sc[u][t] = __builtin_amdgcn_raw_buffer_load_b8(
+                        p.buf, (int)(in ? p.sc_at + (uint32_t)(s + u) * p.stride + t * 16 : kNowhere), 0, 0);
             }
         }
+    };
+
+    Src src = source(act, chunk);
+    if constexpr (WF == W_F32) src.at = chunk * (16 * NT) - src.nb * kWRows + r;
+    Stretch cur, nxt;
+    request(cur, src, s0, true);
+    for (;;) {
+        const int off = __builtin_amdgcn_readfirstlane(s_off[act]), cnt = __builtin_amdgcn_readfirstlane(s_cnt[act]);
+        const int n0 = chunk * (16 * NT);
+        int nact = act, nch = chunk;
+        advance(nact, nch);
+        const bool more = nact < n_act;
+        Src nsrc = source(more ? nact : act, more ? nch : chunk);
+        if constexpr (WF == W_F32) nsrc.at = (more ? nch : chunk) * (16 * NT) - nsrc.nb * kWRows + r;
+
+        // second operand of this lane: tokens (gate/up), routes or a route's term (down)
+        const bool packed = PL == 3 && cnt <= 5;
+        const int nmt = MT == 1 ? 1 : (cnt + 15) / 16;
+        const char *xp[MT];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = (s + u) * KS + q * LK;
-            const bool in = s + u < s1 && k < K;
-            const int kc = in ? k : 0;
+        for (int m = 0; m < MT; ++m) {
+            const int col = packed ? min(r / 3, cnt - 1) : min(16 * m + r, cnt - 1);
+            const int i = s_rec[off + col];
+            xp[m] = (const char *)a.X + ((int64_t)(GATEUP ? i / a.kp : i) * a.ldx +
+                                         (packed ? (int64_t)(r % 3) * a.R * a.ldx : 0)) * (WF == W_F32 ? 4 : 2);
+        }
+        // what this thread needs for its result (one of 4 rows x 1 route), asked
+        // for now: at the end of the tile it would wait behind the weights
+        const int rl = tid & 63, rg = tid >> 6;
+        const int rm = GATEUP ? rg >> 1 : rg / NT, rt = GATEUP ? rg & 1 : rg % NT;
+        const int rrow = 16 * rm + (rl & 15), rn = 16 * rt + 4 * (rl >> 4);
+        const bool mine = rrow < cnt && (GATEUP || n0 + rn < N);   // N % 4 == 0
+        const int route = s_rec[off + min(rrow, cnt - 1)];
+        const float alpha = GATEUP ? 1.0f : a.topk_w[route];
+        f32x4_t rs0 = {1, 1, 1, 1}, rs1 = {1, 1, 1, 1};
+        if constexpr (WF == W_FP8) {
+            const char *S = a.W + (int64_t)__builtin_amdgcn_readfirstlane(s_slot[act]) * a.slot_bytes + a.scale_off;
+            rs0 = *(const f32x4_t *)(S + (int64_t)(n0 + min(rn, 16 * NT - 4)) * 4);
+            if (GATEUP) rs1 = *(const f32x4_t *)(S + (int64_t)(n0 + 32 + rn) * 4);
+        }
+        f32x4_t acc[PL][MT][NT];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (m >= nmt) continue;
+        for (int pl = 0; pl < PL; ++pl)
 #pragma unroll
-                for (int pl = 0; pl < PL; ++pl) {
-                    const char *p = (const char *)a.X + (xoff[m] + (int64_t)pl * a.R * a.ldx + kc) * (WF == W_F32 ? 4 : 2);
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) acc[pl][m][t] = f32x4_t{0, 0, 0, 0};
+
+        // terms: instructions per first operand and column group (1 or PL)
+        auto sweep = [&](auto terms) {
+            constexpr int TM = decltype(terms)::value;
+            constexpr bool PRE = U * MT * TM * NI * 4 <= DEC_PRE;   // the whole stretch's operand at once
+            constexpr int XI = PRE ? NI : 1;
+            int s = s0;
+            do {
+                u32x4_t x[U][MT][TM][XI];
+                auto load_x = [&](int u, int i0) {
+                    const int k = (s + u) * KS + q * LK;
+                    const bool in = s + u < s1 && k < K;
+                    const int kc = in ? k : 0;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int pl = 0; pl < TM; ++pl)
+#pragma unroll
+                            for (int i = 0; i < XI; ++i) {
+                                const char *p = xp[m] + ((int64_t)pl * a.R * a.ldx + kc + 8 * (i0 + i)) * (WF == W_F32 ? 4 : 2);
+                                x[u][m][pl][i] = *(const u32x4_t *)p;
+                                // a weight of zero times whatever stands there is to add nothing
+                                if (WF == W_FP4 || WF == W_F32)
+                                    if (!in) x[u][m][pl][i] = u32x4_t{0, 0, 0, 0};
+                            }
+                };
+                if constexpr (PRE)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) load_x(u, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                const bool last = s + U >= s1;
+                request(nxt, last ? nsrc : src, last ? s0 : s + U, !last || more);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (s + u >= s1) continue;
 #pragma unroll
                     for (int i = 0; i < NI; ++i) {
-                        x[u][m][pl][i] = *(const u32x4_t *)(p + 16 * i);
-                        if (!in) x[u][m][pl][i] = u32x4_t{0, 0, 0, 0};
-                    }
-                }
-            }
-        }
+                        if constexpr (!PRE) load_x(u, i);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+                        for (int t = 0; t < NT; ++t) {
+                            bf16x8_t wv;
+                            if constexpr (WF == W_BF16) wv = __builtin_bit_cast(bf16x8_t, cur.w[u][t]);
+                            if constexpr (WF == W_FP8) wv = fp8_operand(cur.w[u][t], i);
+                            if constexpr (WF == W_FP4) wv = fp4_operand(cur.w[u][t][i], e8m0(cur.sc[u][t]));
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+                            for (int m = 0; m < MT; ++m) {
+                                if (m >= nmt) continue;
+                                if constexpr (WF == W_F32) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    bf16x8_t wv;
-                    if constexpr (WF == W_BF16) wv = __builtin_bit_cast(bf16x8_t, w[u][t]);
-                    if constexpr (WF == W_FP8) wv = fp8_operand(w[u][t], i);
-                    if constexpr (WF == W_FP4) wv = fp4_operand(w[u][t][i], e8m0(sc[u][t]));
+                                    for (int c = 0; c < 4; ++c)
+                                        acc[0][m][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                            __uint_as_float(cur.w[u][t][c]), __uint_as_float(x[u][m][0][0][c]),
+                                            acc[0][m][t], 0, 0, 0);
+                                } else {
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (m >= nmt) continue;
-                        if constexpr (WF == W_F32) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                                    __uint_as_float(w[u][t][c]), __uint_as_float(x[u][m][0][0][c]), acc[m][t], 0, 0, 0);
-                        } else {
-#pragma unroll
-                            for (int pl = 0; pl < PL; ++pl)
-                                acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                    wv, __builtin_bit_cast(bf16x8_t, x[u][m][pl][i]), acc[m][t], 0, 0, 0);
+                                    for (int pl = 0; pl < TM; ++pl)
+                                        acc[pl][m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                            wv, __builtin_bit_cast(bf16x8_t, x[u][m][pl][PRE ? i : 0]), acc[pl][m][t],
+                                            0, 0, 0);
+                                }
+                            }
                         }
                     }
                 }
-    }
+                cur = nxt;
+                s += U;
+            } while (s < s1);
+        };
+        if constexpr (PL == 3) {
+            if (packed)
+                sweep(std::integral_constant<int, 1>());
+            else
+                sweep(std::integral_constant<int, PL>());
+        } else {
+            sweep(std::integral_constant<int, 1>());
+        }
 
+        // this wave's sums, terms joined in ascending order, to LDS
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) red[wave][m * NT + t][lane] = acc[m][t];
-    __syncthreads();
+            for (int t = 0; t < NT; ++t) {
+                f32x4_t v = acc[0][m][t];
+                if constexpr (PL == 3) {
+                    if (packed) {
+                        if (m > 0) continue;
+                        f32x4_t v1, v2;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            v1[c] = __shfl_down(v[c], 1, 64);
+                            v2[c] = __shfl_down(v[c], 2, 64);
+                        }
+                        v = (v + v1) + v2;
+                        if (r % 3 == 0) red[wave][t][(lane & 48) + r / 3] = v;   // r = 15 writes column 5, which is not read
+                        continue;
+                    }
+                    v = (v + acc[1][m][t]) + acc[2][m][t];
+                }
+                red[wave][m * NT + t][lane] = v;
+            }
+        lds_barrier();
 
-    // Result layout: element c of lane l is weight row 4 (l / 16) + c of its
-    // group, route l % 16. Sums of the waves in ascending order.
-    auto total = [&](int g, int l) {
-        f32x4_t v = red[0][g][l];
+        // Result layout: element c of lane l is weight row 4 (l / 16) + c of its
+        // group, route l % 16. Sums of the waves in ascending order.
+        auto total = [&](int g, int l) {
+            f32x4_t v = red[0][g][l];
 #pragma unroll
-        for (int w = 1; w < kDecWaves; ++w) v += red[w][g][l];
-        return v;
-    };
-    auto scale = [&](f32x4_t v, int n) {   // fp8: the rows' scales
-        if constexpr (WF == W_FP8)
+            for (int w = 1; w < kDecWaves; ++w) v += red[w][g][l];
+            return v;
+        };
+        static_assert(MT * (GATEUP ? 2 : NT) <= kDecWaves, "a thread has one result");
+        if constexpr (GATEUP) {
+            // groups 0, 1 are gate rows, 2, 3 the up rows of the same 32 units
+            static_assert(NT == 4, "a tile is 32 gate and 32 up rows");
+            if (mine) {
+                f32x4_t g = total(rm * NT + rt, rl), u = total(rm * NT + 2 + rt, rl);
+                if constexpr (WF == W_FP8) {
+                    g *= rs0;
+                    u *= rs1;
+                }
+                const int64_t at = (int64_t)route * a.ldo + chunk * 32 + rn;
+                float v[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] *= *(const float *)(W + a.scale_off + (int64_t)(n + c) * 4);
-        return v;
-    };
-    if constexpr (GATEUP) {
-        // groups 0, 1 are gate rows, 2, 3 the up rows of the same 32 units
-        for (int e = threadIdx.x; e < nmt * 2 * 64; e += kDecWaves * 64) {
-            const int l = e & 63, h = (e >> 6) & 1, m = e >> 7;
-            const int row = 16 * m + (l & 15), n = 16 * h + 4 * (l >> 4);
-            if (row >= cnt) continue;
-            const f32x4_t g = scale(total(m * NT + h, l), n0 + n), u = scale(total(m * NT + 2 + h, l), n0 + 32 + n);
-            const int64_t at = (int64_t)a.l.rec[off + row] * a.ldo + chunk * 32 + n;
-            float v[4];
+                for (int c = 0; c < 4; ++c) v[c] = g[c] / (1.0f + expf(-g[c])) * u[c];
+                if constexpr (WF == W_F32) {
+                    *(float4 *)((float *)a.out + at) = make_float4(v[0], v[1], v[2], v[3]);
+                } else {
+                    uint16_t t3[3][4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = g[c] / (1.0f + expf(-g[c])) * u[c];
-            if constexpr (WF == W_F32) {
-                *(float4 *)((float *)a.out + at) = make_float4(v[0], v[1], v[2], v[3]);
-            } else {
-                uint16_t t3[3][4];
+                    for (int c = 0; c < 4; ++c) {
+                        // cut 8 bits at a time: each difference is exact, and the
+                        // third has at most 8 bits left
+                        float rest = v[c];
+                        if (rest != rest) rest = __uint_as_float(0x7fc00000u);
+                        const bool inf = __builtin_isinf(rest);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    // cut 8 bits at a time: each difference is exact, and the
-                    // third has at most 8 bits left
-                    float rest = v[c];
-                    if (rest != rest) rest = __uint_as_float(0x7fc00000u);
-                    const bool inf = __builtin_isinf(rest);
+                        for (int pl = 0; pl < 3; ++pl) {
+                            const uint32_t b = __float_as_uint(rest) & 0xffff0000u;
+                            t3[pl][c] = (uint16_t)(b >> 16);
+                            rest = inf ? 0.0f : rest - __uint_as_float(b);
+                        }
+                    }
 #pragma unroll
-                    for (int pl = 0; pl < 3; ++pl) {
-                        const uint32_t b = __float_as_uint(rest) & 0xffff0000u;
-                        t3[pl][c] = (uint16_t)(b >> 16);
-                        rest = inf ? 0.0f : rest - __uint_as_float(b);
+                    for (int pl = 0; pl < 3; ++pl)
+                        *(uint2 *)((uint16_t *)a.out + (int64_t)pl * a.R * a.ldo + at) =
+                            make_uint2(t3[pl][0] | (uint32_t)t3[pl][1] << 16, t3[pl][2] | (uint32_t)t3[pl][3] << 16);
+                }
+            }
+        } else {
+            if (mine) {
+                f32x4_t v = total(rm * NT + rt, rl);
+                if constexpr (WF == W_FP8) v *= rs0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) put((float *)a.out + (int64_t)route * a.ldo + n0 + rn + c, alpha * v[c]);
+            }
+            if (!more || nch != chunk) {
+                // The last workgroup to finish these columns adds the tokens'
+                // rows: Y_t += the token's route rows in ascending j.
+                if (last_to_arrive(a.ctr + chunk, min(groups, n_act))) {
+                    const int n = n0 + 4 * (tid % (4 * NT));
+                    for (int t = tid / (4 * NT); t < a.T && n < N; t += kDecWaves * 16 / NT) {
+                        float4 y = *(const float4 *)(a.Y + (int64_t)t * a.ldy + n);
+                        const float *Yr = (const float *)a.out + (int64_t)t * a.kp * a.ldo + n;
+#pragma unroll 4
+                        for (int j = 0; j < a.kp; ++j) {
+                            const float *v = Yr + (int64_t)j * a.ldo;
+                            y.x += get(v);
+                            y.y += get(v + 1);
+                            y.z += get(v + 2);
+                            y.w += get(v + 3);
+                        }
+                        *(float4 *)(a.Y + (int64_t)t * a.ldy + n) = y;
                     }
                 }
-#pragma unroll
-                for (int pl = 0; pl < 3; ++pl)
-                    *(uint2 *)((uint16_t *)a.out + (int64_t)pl * a.R * a.ldo + at) =
-                        make_uint2(t3[pl][0] | (uint32_t)t3[pl][1] << 16, t3[pl][2] | (uint32_t)t3[pl][3] << 16);
             }
         }
-    } else {
-        for (int e = threadIdx.x; e < nmt * NT * 64; e += kDecWaves * 64) {
-            const int l = e & 63, t = (e >> 6) % NT, m = (e >> 6) / NT;
-            const int row = 16 * m + (l & 15), n = n0 + 16 * t + 4 * (l >> 4);
-            if (row >= cnt || n >= N) continue;   // N % 4 == 0
-            const int i = a.l.rec[off + row];
-            const f32x4_t v = scale(total(m * NT + t, l), n);
-            const float al = a.topk_w[i];
-            *(float4 *)((float *)a.out + (int64_t)i * a.ldo + n) =
-                make_float4(al * v[0], al * v[1], al * v[2], al * v[3]);
-        }
+        if (!more) break;
+        lds_barrier();   // the sums are read: the next tile's may be written
+        act = nact;
+        chunk = nch;
+        src = nsrc;
     }
 }
 
-// Y_t += the token's route rows in ascending j.
-__global__ __launch_bounds__(256) void k_dec_combine(float *__restrict__ Y, int64_t ldy, const float *__restrict__ Yr,
-                                                     int d, int kp, int cblocks)
+// Persistent workgroups: two per compute unit of the 256.
+constexpr int kDecGrid = DEC_GRID;
+
+template <int WF, int MT, int NT, bool GATEUP>
+hipError_t launch_proj_n(const moe_shape &s, DecArgs a, hipStream_t st)
 {
-    const int t = blockIdx.x / cblocks, c = ((int)(blockIdx.x % cblocks) * 256 + threadIdx.x) * 4;
-    if (c >= d) return;
-    float4 y = *(const float4 *)(Y + (int64_t)t * ldy + c);
-    for (int j = 0; j < kp; ++j) {
-        const float4 v = *(const float4 *)(Yr + ((int64_t)t * kp + j) * d + c);
-        y.x += v.x;
-        y.y += v.y;
-        y.z += v.z;
-        y.w += v.w;
-    }
-    *(float4 *)(Y + (int64_t)t * ldy + c) = y;
+    a.nchunk = (a.N + 16 * NT - 1) / (16 * NT);
+    // at most this many slots have routes
+    a.slots = (int)std::min<int64_t>(s.E + s.n_shared, a.R);
+    const int64_t most = kDecGrid, tiles = (int64_t)a.slots * a.nchunk;
+    int64_t grid = std::min(most, tiles);
+    if (!GATEUP && a.nchunk < grid) grid = grid / a.nchunk * a.nchunk;
+    hipLaunchKernelGGL((k_dec_proj<WF, MT, NT, GATEUP>), dim3((unsigned)grid), dim3(kDecWaves * 64), 0, st, a);
+    return hipGetLastError();
 }
 
 template <int WF, bool GATEUP>
-hipError_t launch_proj_t(const moe_shape &s, const DecArgs &a, unsigned grid, hipStream_t st)
+hipError_t launch_proj_t(const moe_shape &s, const DecArgs &a, hipStream_t st)
 {
-    if (s.T <= 16)
-        hipLaunchKernelGGL((k_dec_proj<WF, 1, GATEUP>), dim3(grid), dim3(kDecWaves * 64), 0, st, a);
-    else if (s.T <= 32)
-        hipLaunchKernelGGL((k_dec_proj<WF, 2, GATEUP>), dim3(grid), dim3(kDecWaves * 64), 0, st, a);
-    else
-        hipLaunchKernelGGL((k_dec_proj<WF, 4, GATEUP>), dim3(grid), dim3(kDecWaves * 64), 0, st, a);
-    return hipGetLastError();
+    if (s.T <= 16) return launch_proj_n<WF, 1, 4, GATEUP>(s, a, st);
+    if (s.T <= 32) return launch_proj_n<WF, 2, 4, GATEUP>(s, a, st);
+    // 64 routes in three terms each: 32 rows, or the sums do not fit the registers
+    return launch_proj_n<WF, 4, GATEUP ? 4 : 2, GATEUP>(s, a, st);
 }
 
 }  // namespace
 
-hipError_t launch_dec_lists(const moe_shape &s, const int32_t *idx, const PhiArg &phi, const DecLists &l, hipStream_t st)
+template <typename TX, int TB>
+static hipError_t launch_route_t(const DecRouteArgs &a, const PhiArg &phi, hipStream_t st)
 {
-    hipLaunchKernelGGL(k_dec_lists, dim3(1), dim3(kMaxExp), 0, st, idx, s.T * (s.k + s.n_shared), s.P, phi, l);
+    const dim3 grid((unsigned)((a.T + TB - 1) / TB), a.Wr ? (unsigned)((a.E + 15) / 16) : 1u);
+    if (a.E <= 64)
+        hipLaunchKernelGGL((k_dec_route<TX, 1, TB>), grid, dim3(256), 0, st, a, phi);
+    else if (a.E <= 128)
+        hipLaunchKernelGGL((k_dec_route<TX, 2, TB>), grid, dim3(256), 0, st, a, phi);
+    else
+        hipLaunchKernelGGL((k_dec_route<TX, 4, TB>), grid, dim3(256), 0, st, a, phi);
     return hipGetLastError();
 }
 
-hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a0, bool gateup, hipStream_t st)
+hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const PhiArg &phi, hipStream_t st)
 {
-    DecArgs a = a0;
-    a.nchunk = (a.N + kDecRows - 1) / kDecRows;
-    // at most this many slots have routes
-    const int64_t slots = std::min<int64_t>(s.E + s.n_shared, a.R);
-    const unsigned grid = (unsigned)(slots * a.nchunk);
+    if (act_bf16(s))
+        return a.T == 1 ? launch_route_t<uint16_t, 1>(a, phi, st) : launch_route_t<uint16_t, 4>(a, phi, st);
+    return a.T == 1 ? launch_route_t<float, 1>(a, phi, st) : launch_route_t<float, 4>(a, phi, st);
+}
+
+hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a, bool gateup, hipStream_t st)
+{
     if (gateup) {
-        if (s.dtype == MOE_DT_F32) return launch_proj_t<W_F32, true>(s, a, grid, st);
-        if (w_fp8(s)) return launch_proj_t<W_FP8, true>(s, a, grid, st);
-        if (w_fp4(s)) return launch_proj_t<W_FP4, true>(s, a, grid, st);
-        return launch_proj_t<W_BF16, true>(s, a, grid, st);
+        if (s.dtype == MOE_DT_F32) return launch_proj_t<W_F32, true>(s, a, st);
+        if (w_fp8(s)) return launch_proj_t<W_FP8, true>(s, a, st);
+        if (w_fp4(s)) return launch_proj_t<W_FP4, true>(s, a, st);
+        return launch_proj_t<W_BF16, true>(s, a, st);
     }
-    if (s.dtype == MOE_DT_F32) return launch_proj_t<W_F32, false>(s, a, grid, st);
-    if (w_fp8(s)) return launch_proj_t<W_FP8, false>(s, a, grid, st);
-    if (w_fp4(s)) return launch_proj_t<W_FP4, false>(s, a, grid, st);
-    return launch_proj_t<W_BF16, false>(s, a, grid, st);
-}
-
-hipError_t launch_dec_combine(const moe_shape &s, float *Y, const float *Yr, hipStream_t st)
-{
-    const int cblocks = (s.d / 4 + 255) / 256;
-    hipLaunchKernelGGL(k_dec_combine, dim3((unsigned)(s.T * cblocks)), dim3(256), 0, st, Y, s.ldy, Yr, s.d,
-                       s.k + s.n_shared, cblocks);
-    return hipGetLastError();
+    if (s.dtype == MOE_DT_F32) return launch_proj_t<W_F32, false>(s, a, st);
+    if (w_fp8(s)) return launch_proj_t<W_FP8, false>(s, a, st);
+    if (w_fp4(s)) return launch_proj_t<W_FP4, false>(s, a, st);
+    return launch_proj_t<W_BF16, false>(s, a, st);
 }
 
 }  // namespace moe

@@ -19,6 +19,8 @@ def _shape(**kw):
     (dict(T=64, E=64, k=15, n_shared=2), B.MOE_ERR_UNSUPPORTED),
     (dict(T=-1), B.MOE_ERR_INVALID_ARG),
     (dict(d=96), B.MOE_ERR_UNSUPPORTED),
+    (dict(d=131136), B.MOE_ERR_UNSUPPORTED),
+    (dict(d=65536, f=8192), B.MOE_ERR_UNSUPPORTED),        # a gate/up slice of 2 GiB
 ])
 def test_decode_shapes_refused(kw, status):
     assert B.moe_decode_workspace_bytes(_shape(**kw)) == 0

@@ -10,6 +10,7 @@ constexpr int kDecMaxRoutes = MOE_DECODE_MAX_ROUTES;   // T * K'
 
 constexpr int kDecRows = 32;                           // fewest output columns per workgroup (one counter each)
 constexpr int kDecMaxD = MOE_DECODE_MAX_D;
+constexpr int kDecTokBlock = 4;                        // tokens per route workgroup
 
 // Byte offsets of the decode workspace's regions. The counters stand first and
 // have one size, so that they stay where they are when the shape changes: they

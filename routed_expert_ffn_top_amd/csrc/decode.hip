@@ -104,7 +104,7 @@ __device__ __forceinline__ uint64_t topk_key(float x, int e)
 }
 
 // Router, top-k and the routes by slot, in one launch. A workgroup takes 4
-// tokens x 16 experts (a wave 4 experts, 16 lanes each): lane p of an expert
+// experts (16 lanes each) for 4 tokens, a wave a token: lane p of an expert
 // holds the partial sum p of the router's fixed order (runs of 8 hidden
 // indices, run r to partial sum r mod 16, ascending, one fused multiply-add a
 // term), so a wave's loads are whole 512-byte stretches of W_r and the bits
@@ -112,80 +112,80 @@ __device__ __forceinline__ uint64_t topk_key(float x, int e)
 // (a wave a token, the prompt kernel's arithmetic), and the last block of all
 // sorts the routes by slot. The order of the routes within a slot is that of
 // LDS atomics and is not fixed: it only says which column of a matrix operand
-// a route takes, and columns do not mix. Bound by latency: W_r is 0.5 MB.
-template <typename TX, int C, int TB>
+// a route takes, and columns do not mix. Bound by latency: a wave has 32 KB
+// of W_r to read for d = 2048, and takes 8 groups of 128 hidden indices at once
+// so that two round trips do. (16 experts a workgroup, a wave 4 of them for 4
+// tokens: 15 us for one token instead of ROUTE_US.)
+template <typename TX, int C>
 __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
 {
+    constexpr int TB = kDecTokBlock;
     constexpr int XE = 16 / sizeof(TX), XV = 8 / XE;   // x values per 16 bytes, 16-byte pieces per run
-    __shared__ float part[4][TB][64];
+    __shared__ float part[TB][64];
     __shared__ uint64_t keys[4][64 * C + 2];
     __shared__ int32_t cnt[kMaxExp], off[kMaxExp], wsum[2][4], sphi[kMaxExp];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int t0 = blockIdx.x * TB, nt = min(TB, a.T - t0);
     const int kp = a.k + a.n_shared;
     if (a.Wr) {
-        const int e0 = blockIdx.y * 16 + wave * 4, p = lane & 15, d = a.d;
-        const int e = min(e0 + (lane >> 4), a.E - 1);
-        const float *w = a.Wr + (int64_t)e * d + p * 8;
-        const TX *x[TB];
+        if (wave < nt) {
+            const int e0 = blockIdx.y * 4, p = lane & 15, d = a.d;
+            const float *w = a.Wr + (int64_t)min(e0 + (lane >> 4), a.E - 1) * d + p * 8;
+            const TX *x = (const TX *)a.X + (int64_t)(t0 + wave) * a.ldx + p * 8;
+            float acc = 0.0f;
+            constexpr int U = 8;   // groups of 128 hidden indices in flight
+            const int ng = (d + 127) / 128;
+            for (int g = 0; g < ng; g += U) {
+                u32x4_t wv[U][2], xv[U][XV];
 #pragma unroll
-        for (int t = 0; t < TB; ++t) x[t] = (const TX *)a.X + (int64_t)min(t0 + t, a.T - 1) * a.ldx + p * 8;
-        float acc[TB];
+                for (int u = 0; u < U; ++u) {
+                    // pieces at or past d are read from the row start and not used
 #pragma unroll
-        for (int t = 0; t < TB; ++t) acc[t] = 0.0f;
-        constexpr int U = TB == 1 ? 64 / sizeof(TX) / 4 : 4;   // groups of 128 hidden indices in flight
-        const int ng = (d + 127) / 128;
-        for (int g = 0; g < ng; g += U) {
-            u32x4_t wv[U][2], xv[U][TB][XV];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                // pieces at or past d are read from the row start and not used
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int i = (g + u) * 128 + 4 * h;
-                    wv[u][h] = *(const u32x4_t *)(w + (i + p * 8 < d ? i : -p * 8));
-                }
-#pragma unroll
-                for (int t = 0; t < TB; ++t)
+                    for (int h = 0; h < 2; ++h) {
+                        const int i = (g + u) * 128 + 4 * h;
+                        wv[u][h] = *(const u32x4_t *)(w + (i + p * 8 < d ? i : -p * 8));
+                    }
 #pragma unroll
                     for (int h = 0; h < XV; ++h) {
                         const int i = (g + u) * 128 + XE * h;
-                        if (t == 0 || t < nt) xv[u][t][h] = *(const u32x4_t *)(x[t] + (i + p * 8 < d ? i : -p * 8));
-                    }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    if ((g + u) * 128 + p * 8 + c >= d) continue;
-                    const float wc = __uint_as_float(wv[u][c >> 2][c & 3]);
-#pragma unroll
-                    for (int t = 0; t < TB; ++t) {
-                        if (t > 0 && t >= nt) continue;
-                        float xc;
-                        if constexpr (sizeof(TX) == 2) {
-                            const uint32_t w2 = xv[u][t][0][c >> 1];
-                            xc = __uint_as_float((c & 1) ? (w2 & 0xffff0000u) : (w2 << 16));
-                        } else {
-                            xc = __uint_as_float(xv[u][t][c >> 2][c & 3]);
-                        }
-                        acc[t] = __builtin_fmaf(xc, wc, acc[t]);
+                        xv[u][h] = *(const u32x4_t *)(x + (i + p * 8 < d ? i : -p * 8));
                     }
                 }
-        }
+                __builtin_amdgcn_sched_barrier(0);   // all requested before the first is used
 #pragma unroll
-        for (int t = 0; t < TB; ++t) part[wave][t][lane] = acc[t];
-        __builtin_amdgcn_wave_barrier();   // the reads below are of this wave's writes
-        // lane (t, expert): the 16 partial sums in ascending order
-        const int t = lane >> 2, es = lane & 3;
-        if (lane < 4 * nt && e0 + es < a.E) {
-            float s = part[wave][t][es * 16];
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int c = 1; c < 16; ++c) s = s + part[wave][t][es * 16 + c];
-            put(a.logits + (int64_t)(t0 + t) * a.E + e0 + es, a.bias ? s + a.bias[e0 + es] : s);
+                    for (int c = 0; c < 8; ++c) {
+                        const float wc = __uint_as_float(wv[u][c >> 2][c & 3]);
+                        float xc;
+                        if constexpr (sizeof(TX) == 2) {
+                            const uint32_t w2 = xv[u][0][c >> 1];
+                            xc = __uint_as_float((c & 1) ? (w2 & 0xffff0000u) : (w2 << 16));
+                        } else {
+                            xc = __uint_as_float(xv[u][c >> 2][c & 3]);
+                        }
+                        const float s = __builtin_fmaf(xc, wc, acc);
+                        acc = (g + u) * 128 + p * 8 + c < d ? s : acc;
+                    }
+            }
+            part[wave][lane] = acc;
+            __builtin_amdgcn_wave_barrier();   // the reads below are of this wave's writes
+            // lane < 4: the 16 partial sums of an expert in ascending order
+            if (lane < 4 && e0 + lane < a.E) {
+                float v[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) v[c] = part[wave][lane * 16 + c];
+                float s = v[0];
+#pragma unroll
+                for (int c = 1; c < 16; ++c) s = s + v[c];
+                put(a.logits + (int64_t)(t0 + wave) * a.E + e0 + lane, a.bias ? s + a.bias[e0 + lane] : s);
+            }
         }
-        if (gridDim.y > 1 && !last_to_arrive(a.ctr + 1 + blockIdx.x, gridDim.y)) return;
-        __syncthreads();
+        if (gridDim.y > 1) {
+            if (!last_to_arrive(a.ctr + 1 + blockIdx.x, gridDim.y)) return;
+        } else {
+            __builtin_amdgcn_s_waitcnt(0);   // this wave's logits, read below past the caches
+        }
     }
 
     // top-k of this block's tokens, a wave a token
@@ -738,24 +738,22 @@ hipError_t launch_proj_t(const moe_shape &s, const DecArgs &a, hipStream_t st)
 
 }  // namespace
 
-template <typename TX, int TB>
+template <typename TX>
 static hipError_t launch_route_t(const DecRouteArgs &a, const PhiArg &phi, hipStream_t st)
 {
-    const dim3 grid((unsigned)((a.T + TB - 1) / TB), a.Wr ? (unsigned)((a.E + 15) / 16) : 1u);
+    const dim3 grid((unsigned)((a.T + kDecTokBlock - 1) / kDecTokBlock), a.Wr ? (unsigned)((a.E + 3) / 4) : 1u);
     if (a.E <= 64)
-        hipLaunchKernelGGL((k_dec_route<TX, 1, TB>), grid, dim3(256), 0, st, a, phi);
+        hipLaunchKernelGGL((k_dec_route<TX, 1>), grid, dim3(256), 0, st, a, phi);
     else if (a.E <= 128)
-        hipLaunchKernelGGL((k_dec_route<TX, 2, TB>), grid, dim3(256), 0, st, a, phi);
+        hipLaunchKernelGGL((k_dec_route<TX, 2>), grid, dim3(256), 0, st, a, phi);
     else
-        hipLaunchKernelGGL((k_dec_route<TX, 4, TB>), grid, dim3(256), 0, st, a, phi);
+        hipLaunchKernelGGL((k_dec_route<TX, 4>), grid, dim3(256), 0, st, a, phi);
     return hipGetLastError();
 }
 
 hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const PhiArg &phi, hipStream_t st)
 {
-    if (act_bf16(s))
-        return a.T == 1 ? launch_route_t<uint16_t, 1>(a, phi, st) : launch_route_t<uint16_t, 4>(a, phi, st);
-    return a.T == 1 ? launch_route_t<float, 1>(a, phi, st) : launch_route_t<float, 4>(a, phi, st);
+    return act_bf16(s) ? launch_route_t<uint16_t>(a, phi, st) : launch_route_t<float>(a, phi, st);
 }
 
 hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a, bool gateup, hipStream_t st)

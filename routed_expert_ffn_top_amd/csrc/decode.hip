@@ -115,7 +115,7 @@ __device__ __forceinline__ uint64_t topk_key(float x, int e)
 // a route takes, and columns do not mix. Bound by latency: a wave has 32 KB
 // of W_r to read for d = 2048, and takes 8 groups of 128 hidden indices at once
 // so that two round trips do. (16 experts a workgroup, a wave 4 of them for 4
-// tokens: 15 us for one token instead of ROUTE_US.)
+// tokens: 15 us for one token instead of 8.7.)
 template <typename TX, int C>
 __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
 {

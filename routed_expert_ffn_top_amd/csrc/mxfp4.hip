@@ -7,6 +7,7 @@
 // nearest E2M1 value, ties to the even code, at most 6. A block that holds an
 // infinity or a NaN gets the byte 255 (NaN) and codes 0. A zero has no sign.
 #include <algorithm>
+#include <type_traits>
 
 #include "mxfp4.h"
 
@@ -128,13 +129,37 @@ __device__ __forceinline__ uint32_t bf16_bits(float x)
     return u >> 16;
 }
 
+// ---------------------------------------------------------------------------
 // Product of MXFP4 operands on the scaled matrix instructions
 // (v_mfma_scale_f32_32x32x64_f8f6f4: lane l supplies row l % 32 and the 32
 // consecutive k values 32 (l / 32) .. +31 of each operand, 16 bytes of codes,
 // with that block's scale byte): products and scales are exact, sums in fp32.
-// A tile of 64 records x 64 columns per workgroup, 32 x 32 per wave, operands
-// straight from global memory.
-__global__ __launch_bounds__(256) void k_matmul(MxArgs a)
+// Every element of C is one chain of these instructions in ascending k, in
+// both kernels below, so a record's bits hang neither on the size of its group
+// nor on which kernel runs.
+
+// Two floats rounded to bf16 (nearest even), lo in bits 15:0.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t));
+}
+
+// Slot s holds the records [lo, hi), brought into [0, M).
+__device__ __forceinline__ void slot_range(const MxArgs &a, int s, int *lo, int *hi)
+{
+    *lo = a.slot_offset ? min(max(a.slot_offset[s], 0), a.M) : 0;
+    *hi = a.slot_offset ? min(max(a.slot_offset[s + 1], *lo), a.M) : a.M;
+}
+__device__ __forceinline__ int row_of(const MxArgs &a, int rec)
+{
+    return min(max(a.row_index ? a.row_index[rec] : rec, 0), a.A_rows - 1);
+}
+
+// Few records a slot: 64 records x 64 columns per workgroup, 32 x 32 per wave,
+// operands straight from global memory, 8 steps of 64 k requested at a time.
+// Bound by latency and, with many slots, by reading the weights.
+__global__ __launch_bounds__(256) void k_matmul_small(MxArgs a)
 {
     __shared__ int32_t s_tile[4];   // slot, first record, records
     const int ntn = a.N / 64;
@@ -145,17 +170,14 @@ __global__ __launch_bounds__(256) void k_matmul(MxArgs a)
         int run = 0;
         for (int s0 = 0; s0 < a.P; s0 += 64) {
             const int s = s0 + lane;
-            int off = 0, end = 0;
-            if (s < a.P) {
-                off = a.slot_offset ? min(max(a.slot_offset[s], 0), a.M) : 0;
-                end = a.slot_offset ? min(a.slot_offset[s + 1], a.M) : a.M;
-            }
-            const int mt = max(end - off + 63, 0) / 64;
+            int lo = 0, hi = 0;
+            if (s < a.P) slot_range(a, s, &lo, &hi);
+            const int mt = (hi - lo + 63) / 64;
             const int inc = run + wave_incl_scan(mt, lane);
             if (bid < inc && bid >= inc - mt) {
                 s_tile[0] = s;
-                s_tile[1] = off + (bid - (inc - mt)) * 64;
-                s_tile[2] = min(64, end - s_tile[1]);
+                s_tile[1] = lo + (bid - (inc - mt)) * 64;
+                s_tile[2] = min(64, hi - s_tile[1]);
             }
             run = __shfl(inc, 63, 64);
         }
@@ -167,25 +189,39 @@ __global__ __launch_bounds__(256) void k_matmul(MxArgs a)
     const int m0 = (wave >> 1) * 32, c0 = n0 + (wave & 1) * 32;
     if (m0 >= cnt) return;
     const int half = lane >> 5;
-    int rec = row0 + min(m0 + (lane & 31), cnt - 1);
-    if (a.row_index) rec = a.row_index[rec];
-    rec = min(max(rec, 0), a.A_rows - 1);
+    const int rec = row_of(a, row0 + min(m0 + (lane & 31), cnt - 1));
     const uint8_t *ap = a.A + (int64_t)rec * (K / 2) + half * 16;
     const uint8_t *as = a.As + (int64_t)rec * (K / 32) + half;
     const int n = c0 + (lane & 31), nb = n / kWRows, rows = min(kWRows, N - nb * kWRows);
     const int64_t pb = fp4_piece_bytes(rows);
-    const uint8_t *bp = a.B + (int64_t)slot * a.B_stride + (int64_t)nb * (K / kWK) * fp4_piece_bytes(kWRows) + half * pb;
     const int rb = n - nb * kWRows;
+    const uint8_t *bp = a.B + (int64_t)slot * a.B_stride + (int64_t)nb * (K / kWK) * fp4_piece_bytes(kWRows) + half * pb +
+                        rb * 16;
+    const uint8_t *bs = bp - rb * 16 + rows * 16 + rb;
     f32x16_t acc;
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
-    for (int k = 0; k < K / 64; ++k) {
-        const u32x4_t av = *(const u32x4_t *)(ap + k * 32);
-        const u32x4_t bv = *(const u32x4_t *)(bp + 2 * k * pb + rb * 16);
-        const int sa = as[2 * k], sb = bp[2 * k * pb + rows * 16 + rb];
-        const i32x8_t A = {(int)av[0], (int)av[1], (int)av[2], (int)av[3], 0, 0, 0, 0};
-        const i32x8_t Bv = {(int)bv[0], (int)bv[1], (int)bv[2], (int)bv[3], 0, 0, 0, 0};
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, Bv, acc, 4, 4, 0, sa, 0, sb);
+    constexpr int U = 8;
+    const int nk = K / 64;
+    for (int k = 0; k < nk; k += U) {
+        u32x4_t av[U], bv[U];
+        int sa[U], sb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t kk = min(k + u, nk - 1);
+            bv[u] = *(const u32x4_t *)(bp + 2 * kk * pb);
+            sb[u] = bs[2 * kk * pb];
+            av[u] = *(const u32x4_t *)(ap + kk * 32);
+            sa[u] = as[2 * kk];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k + u >= nk) continue;
+            const i32x8_t A = {(int)av[u][0], (int)av[u][1], (int)av[u][2], (int)av[u][3], 0, 0, 0, 0};
+            const i32x8_t Bv = {(int)bv[u][0], (int)bv[u][1], (int)bv[u][2], (int)bv[u][3], 0, 0, 0, 0};
+            acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, Bv, acc, 4, 4, 0, sa[u], 0, sb[u]);
+        }
     }
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
@@ -196,6 +232,327 @@ __global__ __launch_bounds__(256) void k_matmul(MxArgs a)
             ((uint16_t *)a.C)[at] = (uint16_t)bf16_bits(acc[r]);
         else
             ((float *)a.C)[at] = acc[r];
+    }
+}
+
+#define LDS_AS __attribute__((address_space(3)))
+#define GLOBAL_AS __attribute__((address_space(1)))
+
+// s_waitcnt with only the vector-memory counter constrained (gfx9 encoding:
+// vmcnt[3:0] | expcnt[6:4] | lgkmcnt[11:8] | vmcnt[5:4] at bits 15:14).
+template <int N>
+__device__ __forceinline__ void wait_vmcnt()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+// At most n * STEP vector memory operations of this wave outstanding, n in [0, MAXN].
+template <int STEP, int MAXN>
+__device__ __forceinline__ void wait_vmcnt_stages(int n)
+{
+    if constexpr (MAXN > 0) {
+        if (n >= MAXN) {
+            wait_vmcnt<MAXN * STEP>();
+            return;
+        }
+        wait_vmcnt_stages<STEP, MAXN - 1>(n);
+    } else {
+        wait_vmcnt<0>();
+    }
+}
+
+constexpr int kXcd = 8;
+
+// Many records a slot: a persistent ring kernel. Tile BM records x 256 columns,
+// one stage = 128 k: BM rows of 64 code bytes, 4 K pieces of the packed slice
+// (256 rows of 16 code bytes each, one contiguous run) and both sides' scale
+// bytes, copied straight into LDS (16 bytes a lane), NS stages deep; 8 waves as
+// 2 x 4, MI x NI 32 x 32 blocks each, so that the B fragments, whose scales are
+// read byte by byte, are the fewer. A rows are stored with their 16-byte chunk
+// c at c ^ ((row >> 2) & 3), which keeps the fragment reads free of bank
+// conflicts; the pieces of B are so as they stand. A row's scale bytes of a
+// stage are one 32-bit word, aligned or not: SHIFT copies the two aligned words
+// that hold it and the lanes cut it out; without it (K % 128 == 0 and aligned
+// scales) one word is copied. The tiles of an XCD (workgroup id mod 8) are one
+// contiguous range, column block major, walked in step, so that tiles which
+// share weights or rows share that XCD's L2.
+template <int BM, int NS, bool SHIFT>
+__global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
+{
+    constexpr int BN = 256, WM = 2, WN = 4, TM = BM / WM, TN = BN / WN, MI = TM / 32, NI = TN / 32;
+    constexpr int ACODE = BM * 64, BCODE = BN * 64, ASC = BM * (SHIFT ? 8 : 4), BSC = BN * 4;
+    constexpr int STAGE = ACODE + BCODE + ASC + BSC;
+    constexpr int AI = BM / 128, BI = 2, SI = SHIFT ? 2 : 1;   // copies per wave and stage
+    constexpr int LOADS = AI + BI + SI;
+    static_assert(BM == 256 && NS >= 3, "the copies of the scales are laid out for 256 rows");
+    __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE];
+    __shared__ int32_t s_tpref[kMaxExp + 1], s_lo[kMaxExp], s_cnt[kMaxExp];
+    __shared__ int32_t s_shift[SHIFT ? BM : 1];   // bytes from the aligned word to a row's scales
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN, half = lane >> 5;
+    const int K = a.K, N = a.N, P = a.P;
+    const int ntn = (N + BN - 1) / BN;
+    if (tid < 64) {
+        int run = 0;
+        for (int s0 = 0; s0 < P; s0 += 64) {
+            const int s = s0 + lane;
+            int lo = 0, hi = 0;
+            if (s < P) slot_range(a, s, &lo, &hi);
+            const int w = (hi - lo + BM - 1) / BM * ntn;
+            const int inc = run + wave_incl_scan(w, lane);
+            if (s < P) {
+                s_tpref[s] = inc - w;
+                s_lo[s] = lo;
+                s_cnt[s] = hi - lo;
+            }
+            run = __shfl(inc, 63, 64);
+        }
+        if (lane == 0) s_tpref[P] = run;
+    }
+    __syncthreads();
+    const int total = s_tpref[P];
+    const int xcd = blockIdx.x % kXcd, li = blockIdx.x / kXcd;
+    const int nwg = ((int)gridDim.x - xcd + kXcd - 1) / kXcd;
+    const int qx = total / kXcd, rx = total % kXcd;
+    const int cnt_x = qx + (xcd < rx ? 1 : 0), start_x = xcd * qx + min(xcd, rx);
+    if (li >= cnt_x) return;
+
+    struct Tile {
+        int slot, row0, rows, n0;
+    };
+    auto decode = [&](int L) -> Tile {
+        int lo = 0, hi = P - 1;   // last slot whose first tile is <= L (skips empty slots)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_tpref[mid] <= L) lo = mid; else hi = mid - 1;
+        }
+        const int mt = (s_cnt[lo] + BM - 1) / BM, local = L - s_tpref[lo], ml = local % mt;
+        Tile t;
+        t.slot = lo;
+        t.row0 = s_lo[lo] + ml * BM;
+        t.rows = __builtin_amdgcn_readfirstlane(min(BM, s_cnt[lo] - ml * BM));
+        t.n0 = (local / mt) * BN;
+        return t;
+    };
+
+    // Copies of this wave: A codes rows 16 (wave AI + j) .. +15 (lane: row + l/4,
+    // chunk position l % 4), B codes 64 rows 64 ((2 wave + j) % 4) .. of piece
+    // (2 wave + j) / 4, and scales: waves 0-3 those of A rows 64 wave .. +63,
+    // waves 4-7 the 256 of B's piece wave - 4.
+    const char *asrc[AI], *bsrc[BI], *ssrc[SI];
+    int bstep = 0;
+    auto fetch_rows = [&](const Tile &t, int *rows) {
+#pragma unroll
+        for (int j = 0; j < AI; ++j) rows[j] = row_of(a, t.row0 + min((wave * AI + j) * 16 + (lane >> 2), t.rows - 1));
+        rows[AI] = row_of(a, t.row0 + min((wave & 3) * 64 + lane, t.rows - 1));
+    };
+    auto scales_at = [&](int row) { return (uintptr_t)a.As + (uintptr_t)((int64_t)row * (K / 32)); };
+    // the last aligned word that holds scale bytes
+    const uintptr_t last_word = (scales_at(a.A_rows) - 1) & ~(uintptr_t)3;
+    auto set_sources = [&](const Tile &t, const int *rows) {
+#pragma unroll
+        for (int j = 0; j < AI; ++j) {
+            const int r = (wave * AI + j) * 16 + (lane >> 2);
+            asrc[j] = (const char *)a.A + (int64_t)rows[j] * (K / 2) + ((lane & 3) ^ ((r >> 2) & 3)) * 16;
+        }
+        const int nb = t.n0 / kWRows, rows_nb = min(kWRows, N - nb * kWRows);
+        const int64_t pb = fp4_piece_bytes(rows_nb);
+        const char *Bblk = (const char *)a.B + (int64_t)t.slot * a.B_stride + (int64_t)nb * (K / kWK) * fp4_piece_bytes(kWRows);
+        bstep = (int)(4 * pb);
+#pragma unroll
+        for (int j = 0; j < BI; ++j) {
+            const int c = wave * BI + j;
+            bsrc[j] = Bblk + (c >> 2) * pb + min((c & 3) * 64 + lane, rows_nb - 1) * 16;
+        }
+        if (wave < 4) {
+            const uintptr_t p = scales_at(rows[AI]) & ~(uintptr_t)3;
+            ssrc[0] = (const char *)p;
+            if constexpr (SHIFT) {
+                ssrc[1] = (const char *)p;
+                s_shift[wave * 64 + lane] = (int)(scales_at(rows[AI]) & 3);   // read after the tile's first barrier
+            }
+        } else {
+            ssrc[0] = Bblk + (wave - 4) * pb + rows_nb * 16 + ((lane & 15) * 16 < rows_nb ? (lane & 15) * 16 : 0);
+            if constexpr (SHIFT) ssrc[1] = ssrc[0];
+        }
+    };
+    const int nk = (K + 127) / 128;
+    const bool odd = (K & 64) != 0;   // the last stage has 64 k
+    auto issue = [&](int kt) {
+        char *st = lds + (kt % NS) * STAGE;
+        // the pieces past K of a last half stage are those of its first half again, and not used
+        const bool tail = odd && kt == nk - 1;
+#pragma unroll
+        for (int j = 0; j < AI; ++j) {
+            const int c = (lane & 3) ^ ((((wave * AI + j) * 16 + (lane >> 2)) >> 2) & 3);
+            __builtin_amdgcn_global_load_lds((const GLOBAL_AS void *)(asrc[j] + (int64_t)kt * 64 - (tail && c >= 2 ? 32 : 0)),
+                                             (LDS_AS void *)(st + (wave * AI + j) * 1024), 16, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < BI; ++j) {
+            const int c = wave * BI + j;
+            __builtin_amdgcn_global_load_lds(
+                (const GLOBAL_AS void *)(bsrc[j] + (int64_t)kt * bstep - (tail && (c >> 2) >= 2 ? bstep / 2 : 0)),
+                (LDS_AS void *)(st + ACODE + c * 1024), 16, 0, 0);
+        }
+        if (wave < 4) {
+#pragma unroll
+            for (int q = 0; q < SI; ++q) {
+                const uintptr_t p = (uintptr_t)ssrc[q] + (uintptr_t)kt * 4 + 4 * q;
+                __builtin_amdgcn_global_load_lds((const GLOBAL_AS void *)(p < last_word ? p : last_word),
+                                                 (LDS_AS void *)(st + ACODE + BCODE + q * BM * 4 + wave * 256), 4, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < SI; ++q)
+                if (lane < 16)
+                    __builtin_amdgcn_global_load_lds(
+                        (const GLOBAL_AS void *)(ssrc[q] + (int64_t)kt * bstep - (tail && wave >= 6 ? bstep / 2 : 0)),
+                        (LDS_AS void *)(st + ACODE + BCODE + ASC + (wave - 4) * 256), 16, 0, 0);
+        }
+    };
+
+    const int sw = ((lane & 31) >> 2) & 3;
+    const int foff[2] = {(lane & 31) * 64 + ((0 + half) ^ sw) * 16, (lane & 31) * 64 + ((2 + half) ^ sw) * 16};
+    f32x16_t acc[MI][NI];
+    u32x4_t af[2][MI], bf[2][NI];
+    int as[MI], bs[2][NI];   // A: this lane's scale bytes at bytes 0 (step 0) and 2 (step 1)
+    int asn[MI];
+    auto read_frags = [&](int stage, int ks, int set) {
+        const char *st = lds + stage * STAGE;
+        const char *As = st + wm * TM * 64 + foff[ks];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) af[set][i] = *(const u32x4_t *)(As + i * 32 * 64);
+        const char *Bs = st + ACODE + (2 * ks + half) * (BN * 16) + (wn * TN + (lane & 31)) * 16;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) bf[set][j] = *(const u32x4_t *)(Bs + j * 32 * 16);
+        const char *Bc = st + ACODE + BCODE + ASC + (2 * ks + half) * BN + wn * TN + (lane & 31);
+#pragma unroll
+        for (int j = 0; j < NI; ++j) bs[set][j] = *(const uint8_t *)(Bc + j * 32);
+        if (ks == 0) {
+            const char *Ac = st + ACODE + BCODE + (wm * TM + (lane & 31)) * 4;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                uint32_t w = *(const uint32_t *)(Ac + i * 128);
+                if constexpr (SHIFT) w = __builtin_amdgcn_alignbyte(*(const uint32_t *)(Ac + BM * 4 + i * 128), w,
+                                                                  s_shift[wm * TM + i * 32 + (lane & 31)]);
+                asn[i] = (int)(w >> (8 * half));
+            }
+        }
+    };
+    auto mfmas = [&](auto ks_t) {
+        constexpr int ks = decltype(ks_t)::value;
+        if (ks == 0)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) as[i] = asn[i];
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const i32x8_t A = {(int)af[ks][i][0], (int)af[ks][i][1], (int)af[ks][i][2], (int)af[ks][i][3], 0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                const i32x8_t Bv = {(int)bf[ks][j][0], (int)bf[ks][j][1], (int)bf[ks][j][2], (int)bf[ks][j][3], 0, 0, 0, 0};
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, Bv, acc[i][j], 4, 4, 2 * ks, as[i], 0,
+                                                                            bs[ks][j]);
+            }
+        }
+    };
+
+    int tl = li;
+    Tile cur = decode(start_x + tl);
+    int rows[AI + 1];
+    fetch_rows(cur, rows);
+    set_sources(cur, rows);
+#pragma unroll
+    for (int p = 0; p < NS - 1; ++p)
+        if (p < nk) issue(p);
+    for (;;) {
+        const bool wave_active = wm * TM < cur.rows;
+        const int tn = tl + nwg;
+        const bool has_next = tn < cnt_x;
+        const Tile nxt = has_next ? decode(start_x + tn) : cur;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        // Loads return in order: stage 0 is there once no more than the copies
+        // of the min(NS - 2, nk - 1) stages requested after it are outstanding.
+        wait_vmcnt_stages<LOADS, NS - 2>(min(NS - 2, nk - 1));
+        __syncthreads();
+        if (wave_active) read_frags(0, 0, 0);
+        // At the top of step kt stage kt is visible to every wave, and this wave
+        // holds its step-0 fragments. Stage kt + 1 is made visible (own copies
+        // waited for, then a barrier) and stage kt + NS - 1 requested into the
+        // slot of stage kt - 1, which every wave finished before that barrier.
+        for (int kt = 0; kt < nk; ++kt) {
+            const int stage = kt % NS;
+            const bool more = kt + 1 < nk;
+            if (more) {
+                wait_vmcnt_stages<LOADS, NS - 3>(min(NS - 3, nk - 2 - kt));
+                __builtin_amdgcn_s_barrier();
+            }
+            if (has_next && kt == 0) fetch_rows(nxt, rows);
+            if (more && kt + NS - 1 < nk) issue(kt + NS - 1);
+            if (wave_active) {
+                read_frags(stage, 1, 1);
+                mfmas(std::integral_constant<int, 0>());
+                if (more) read_frags((kt + 1) % NS, 0, 0);
+                if (!(odd && !more)) mfmas(std::integral_constant<int, 1>());
+            }
+        }
+        const Tile done = cur;
+        if (has_next) {
+            __syncthreads();   // nothing reads the ring any more
+            set_sources(nxt, rows);
+#pragma unroll
+            for (int p = 0; p < NS - 1; ++p)
+                if (p < nk) issue(p);
+        }
+        // Register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4 and column
+        // l % 32 of its block. bf16: adjacent lanes swap a value of rows R, R + 1,
+        // so that each stores two columns of one row.
+        if (wave_active) {
+            const int nlim = N - done.n0 - wn * TN;   // a multiple of 64
+            // opaque here, or the 64 row offsets are computed before the tile
+            // loop and held (211 registers spilled)
+            int64_t ldc = a.ldc;
+            asm volatile("" : "+s"(ldc));
+            if (a.c_bf16) {
+                const bool even = (lane & 1) == 0;
+                uint16_t *C = (uint16_t *)a.C + (int64_t)done.row0 * ldc + done.n0 + wn * TN + (lane & 30);
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 2) {
+                        const int m = wm * TM + i * 32 + 8 * (r / 4) + 4 * half + (r & 3) + (even ? 0 : 1);
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) {
+                            const float s0 = acc[i][j][r], s1 = acc[i][j][r + 1];
+                            const float y = __int_as_float(
+                                __builtin_amdgcn_mov_dpp(__float_as_int(even ? s1 : s0), 0xB1, 0xF, 0xF, false));
+                            const uint32_t v = even ? bf16_pair(s0, y) : bf16_pair(y, s1);
+                            if (m < done.rows && j * 32 < nlim) *(uint32_t *)(C + m * ldc + j * 32) = v;
+                        }
+                    }
+            } else {
+                float *C = (float *)a.C + (int64_t)done.row0 * ldc + done.n0 + wn * TN + (lane & 31);
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int m = wm * TM + i * 32 + 8 * (r / 4) + 4 * half + (r & 3);
+#pragma unroll
+                        for (int j = 0; j < NI; ++j)
+                            if (m < done.rows && j * 32 < nlim) C[m * ldc + j * 32] = acc[i][j][r];
+                    }
+            }
+        }
+        if (!has_next) break;
+        cur = nxt;
+        tl = tn;
     }
 }
 
@@ -229,12 +586,30 @@ hipError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, 
     return hipGetLastError();
 }
 
+template <bool SHIFT>
+static void launch_ring(const MxArgs &a, unsigned grid, hipStream_t st)
+{
+    hipLaunchKernelGGL((k_matmul_ring<256, 4, SHIFT>), dim3(grid), dim3(512), 0, st, a);
+}
+
 hipError_t launch_matmul_mxfp4(const MxArgs &a, hipStream_t st)
 {
     if (a.M == 0) return hipSuccess;
+#ifndef MX_RING_ROWS
+#define MX_RING_ROWS 96
+#endif
+    if (a.M >= (int64_t)MX_RING_ROWS * a.P) {
+        const int64_t tiles = ((int64_t)(a.M + 255) / 256 + std::min(a.P, a.M) - 1) * ((a.N + 255) / 256);
+        const unsigned grid = (unsigned)std::min<int64_t>(tiles, 256);   // one workgroup per compute unit
+        if (a.K % 128 == 0 && ((uintptr_t)a.As & 3) == 0)
+            launch_ring<false>(a, grid, st);
+        else
+            launch_ring<true>(a, grid, st);
+        return hipGetLastError();
+    }
     // at most this many row tiles: one partial tile per slot with records
     const int64_t mt = (int64_t)(a.M + 63) / 64 + std::min(a.P, a.M) - 1;
-    hipLaunchKernelGGL(k_matmul, dim3((unsigned)(mt * (a.N / 64))), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(k_matmul_small, dim3((unsigned)(mt * (a.N / 64))), dim3(256), 0, st, a);
     return hipGetLastError();
 }
 

@@ -471,8 +471,8 @@ moe_status moe_dequantize_mxfp4(const void *codes, const void *scales,
  *                for MOE_DT_BF16_FP4W with d = N and f = K; a plane of an
  *                arena), B_stride bytes apart; both multiples of 16 and
  *                B_stride >= a slice when P > 1; P <= 512
- *   C            device [M][ldc] of c_dtype (MOE_DT_F32 or MOE_DT_BF16), ldc >=
- *                N; C and its row stride 16-byte aligned
+ *   C            device [M][ldc] of c_dtype (MOE_DT_F32 or MOE_DT_BF16), N <=
+ *                ldc < 2^21; C and its row stride 16-byte aligned
  * Rows and offsets out of range are brought into it on the device.
  */
 moe_status moe_matmul_mxfp4(int32_t M, int32_t N, int32_t K,

@@ -779,6 +779,8 @@ moe_status moe_matmul_mxfp4(int32_t M, int32_t N, int32_t K, const void *A_codes
         return fail(MOE_ERR_INVALID_ARG, "matmul: A, B, C and C's row stride must be 16-byte aligned");
     if (P > 1 && (B_stride < fp4_slice_bytes(N, K) || B_stride % 16 != 0))
         return fail(MOE_ERR_INVALID_ARG, "matmul: B_stride must hold a slice and be a multiple of 16");
+    // 256 rows of C are one buffer of the ring kernel
+    if (ldc > ((int64_t)1 << 31) / 256 / 4 - 1) return fail(MOE_ERR_UNSUPPORTED, "matmul: ldc too large");
     // 256 threads per 64 x 64 tile, at most 2^32 - 1 threads a launch
     if (((int64_t)M / 64 + P + 1) * (N / 64) >= (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "matmul: too many tiles");
     MxArgs a{};

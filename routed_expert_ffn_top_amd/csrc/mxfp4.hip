@@ -379,7 +379,7 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
         }
     };
     const int nk = (K + 127) / 128;
-    const bool odd = (K & 64) != 0;   // the last stage has 64 k
+    const bool odd = SHIFT && (K & 64) != 0;   // the last stage has 64 k
     auto issue = [&](int kt) {
         char *st = lds + (kt % NS) * STAGE;
         // the pieces past K of a last half stage are those of its first half again, and not used
@@ -459,6 +459,15 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
         }
     };
 
+    // the next step's LDS reads are spread over this step's multiplies
+    auto interleave = [&]() {
+#pragma unroll
+        for (int q = 0; q < MI * NI; ++q) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // two LDS reads
+        }
+    };
+
     int tl = li;
     Tile cur = decode(start_x + tl);
     int rows[AI + 1];
@@ -499,8 +508,11 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
             if (wave_active) {
                 read_frags(stage, 1, 1);
                 mfmas(std::integral_constant<int, 0>());
-                if (more) read_frags((kt + 1) % NS, 0, 0);
+                interleave();
+                // on the last step this reads a resident stage again; the values are not used
+                read_frags((kt + 1) % NS, 0, 0);
                 if (!(odd && !more)) mfmas(std::integral_constant<int, 1>());
+                interleave();
             }
         }
         const Tile done = cur;
@@ -513,40 +525,46 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
         }
         // Register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4 and column
         // l % 32 of its block. bf16: adjacent lanes swap a value of rows R, R + 1,
-        // so that each stores two columns of one row.
-        if (wave_active) {
-            const int nlim = N - done.n0 - wn * TN;   // a multiple of 64
-            // opaque here, or the 64 row offsets are computed before the tile
-            // loop and held (211 registers spilled)
-            int64_t ldc = a.ldc;
-            asm volatile("" : "+s"(ldc));
+        // so that each stores two columns of one row. The tile's rows of C are a
+        // buffer: stores to rows past its last one are dropped by its bounds
+        // check, so no store has a branch. A wave's 64 columns are all in N or
+        // all past it.
+        if (wave_active && done.n0 + wn * TN < N) {
+            const int esz = a.c_bf16 ? 2 : 4;
+            char *base = (char *)a.C + ((int64_t)done.row0 * a.ldc + done.n0 + wn * TN) * esz;
+            // opaque, or the rows' offsets are computed before the tile loop and
+            // held through it (211 registers spilled)
+            uint32_t ld = (uint32_t)a.ldc * esz;
+            asm volatile("" : "+s"(ld));
+            const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(base, 0, (int)(done.rows * ld), 0x00027000);
+            const uint32_t row = wm * TM + 4 * half;
             if (a.c_bf16) {
                 const bool even = (lane & 1) == 0;
-                uint16_t *C = (uint16_t *)a.C + (int64_t)done.row0 * ldc + done.n0 + wn * TN + (lane & 30);
+                const uint32_t at = (row + (even ? 0 : 1)) * ld + (lane & 30) * 2;
 #pragma unroll
                 for (int i = 0; i < MI; ++i)
 #pragma unroll
                     for (int r = 0; r < 16; r += 2) {
-                        const int m = wm * TM + i * 32 + 8 * (r / 4) + 4 * half + (r & 3) + (even ? 0 : 1);
+                        const uint32_t o = at + (uint32_t)(i * 32 + 8 * (r / 4) + (r & 3)) * ld;
 #pragma unroll
                         for (int j = 0; j < NI; ++j) {
                             const float s0 = acc[i][j][r], s1 = acc[i][j][r + 1];
                             const float y = __int_as_float(
                                 __builtin_amdgcn_mov_dpp(__float_as_int(even ? s1 : s0), 0xB1, 0xF, 0xF, false));
-                            const uint32_t v = even ? bf16_pair(s0, y) : bf16_pair(y, s1);
-                            if (m < done.rows && j * 32 < nlim) *(uint32_t *)(C + m * ldc + j * 32) = v;
+                            __builtin_amdgcn_raw_buffer_store_b32(even ? bf16_pair(s0, y) : bf16_pair(y, s1), buf,
+                                                                  (int)(o + j * 64), 0, 0);
                         }
                     }
             } else {
-                float *C = (float *)a.C + (int64_t)done.row0 * ldc + done.n0 + wn * TN + (lane & 31);
+                const uint32_t at = row * ld + (lane & 31) * 4;
 #pragma unroll
                 for (int i = 0; i < MI; ++i)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const int m = wm * TM + i * 32 + 8 * (r / 4) + 4 * half + (r & 3);
+                        const uint32_t o = at + (uint32_t)(i * 32 + 8 * (r / 4) + (r & 3)) * ld;
 #pragma unroll
                         for (int j = 0; j < NI; ++j)
-                            if (m < done.rows && j * 32 < nlim) C[m * ldc + j * 32] = acc[i][j][r];
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][r]), buf, (int)(o + j * 128), 0, 0);
                     }
             }
         }

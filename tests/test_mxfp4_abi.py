@@ -43,7 +43,7 @@ def test_matmul_refusals():
                dict(W=None), dict(C=None), dict(A=0x1008), dict(As=0x2001), dict(W=0x4008), dict(C=0x8004),
                dict(ldc=66), dict(dt=B.MOE_DT_BF16, ldc=68), dict(P=2, off=0x10, stride=2175), dict(P=2, off=0x10, stride=2184)):
         assert status(**kw) == INV, kw
-    for kw in (dict(N=96), dict(K=96), dict(M=1 << 30, rows=1 << 30)):
+    for kw in (dict(N=96), dict(K=96), dict(M=1 << 30, rows=1 << 30), dict(ldc=1 << 21)):
         assert status(**kw) == UN, kw
 
 

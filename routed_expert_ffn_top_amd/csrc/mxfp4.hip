@@ -19,6 +19,14 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
+// Element offset of group i of 8 values (i < 2^31), rows of K8 groups ld elements apart.
+__device__ __forceinline__ int64_t place(int64_t i, int K8, int64_t ld)
+{
+    if (ld == (int64_t)K8 * 8) return i * 8;
+    const uint32_t row = (uint32_t)i / (uint32_t)K8;
+    return row * ld + (int64_t)((uint32_t)i - row * (uint32_t)K8) * 8;
+}
+
 // 8 values per lane, 4 lanes per block. Bound by HBM: 4 or 2 bytes read and
 // 17/32 written a value.
 template <bool BF16>
@@ -27,8 +35,7 @@ __global__ __launch_bounds__(256) void k_quantize(const void *__restrict__ src, 
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n8) return;   // whole blocks of 4 lanes: n8 % 4 == 0
-    const int64_t row = i / K8;
-    const int64_t at = row * ld + (i - row * K8) * 8;
+    const int64_t at = place(i, K8, ld);
     uint32_t v[8];
     if constexpr (BF16) {
         const u32x4_t w = *(const u32x4_t *)((const uint16_t *)src + at);
@@ -89,8 +96,7 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint32_t *__restrict__
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n8) return;
-    const int64_t row = i / K8;
-    const int64_t at = row * ld + (i - row * K8) * 8;
+    const int64_t at = place(i, K8, ld);
     const uint32_t q = codes[i];
     const float s = e8m0(scales[i >> 2]);
     const f32x2_t p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0),
@@ -262,6 +268,7 @@ __device__ __forceinline__ void wait_vmcnt_stages(int n)
 }
 
 constexpr int kXcd = 8;
+constexpr int kStream = 2;   // buffer stores of C, which is not read here: non-temporal (fp32 C 141 -> 132 us)
 
 // Many records a slot: a persistent ring kernel. Tile BM records x 256 columns,
 // one stage = 128 k: BM rows of 64 code bytes, 4 K pieces of the packed slice
@@ -552,7 +559,7 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
                             const float y = __int_as_float(
                                 __builtin_amdgcn_mov_dpp(__float_as_int(even ? s1 : s0), 0xB1, 0xF, 0xF, false));
                             __builtin_amdgcn_raw_buffer_store_b32(even ? bf16_pair(s0, y) : bf16_pair(y, s1), buf,
-                                                                  (int)(o + j * 64), 0, 0);
+                                                                  (int)(o + j * 64), 0, kStream);
                         }
                     }
             } else {
@@ -564,7 +571,7 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
                         const uint32_t o = at + (uint32_t)(i * 32 + 8 * (r / 4) + (r & 3)) * ld;
 #pragma unroll
                         for (int j = 0; j < NI; ++j)
-                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][r]), buf, (int)(o + j * 128), 0, 0);
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][r]), buf, (int)(o + j * 128), 0, kStream);
                     }
             }
         }

@@ -345,7 +345,9 @@ __device__ __forceinline__ bf16x8_t fp4_operand(uint32_t w, float scale)
 #ifndef DEC_GRID
 #define DEC_GRID 512
 #endif
-constexpr int kDecWaves = 8;
+#ifndef DEC_NW1
+#define DEC_NW1 4
+#endif
 constexpr uint32_t kNowhere = 0x80000000u;   // a buffer offset past every slice: such a load gives zeros and reads nothing
 
 // Workgroup barrier that waits for this wave's LDS traffic only: loads in
@@ -370,8 +372,8 @@ __device__ __forceinline__ void lds_barrier()
 // it then leaves the weights in flight. Weights come through buffer loads, whose
 // bounds check makes a stretch that is not there zeros without a branch, so
 // that the number of loads in flight is the same on every path.
-template <int WF, int MT, int NT, bool GATEUP>
-__global__ __launch_bounds__(kDecWaves * 64) void k_dec_proj(DecArgs a)
+template <int WF, int MT, int NT, int NW, bool GATEUP>
+__global__ __launch_bounds__(NW * 64) void k_dec_proj(DecArgs a)
 {
     constexpr int LK = WF == W_F32 ? 4 : WF == W_BF16 ? 8 : WF == W_FP8 ? 16 : 32;   // k values per lane and step
     constexpr int KS = 4 * LK;                                         // k values per step
@@ -379,7 +381,7 @@ __global__ __launch_bounds__(kDecWaves * 64) void k_dec_proj(DecArgs a)
     constexpr int PL = !GATEUP && WF != W_F32 ? 3 : 1;                 // terms of the second operand
     constexpr int U = DEC_U; // steps per stretch
     constexpr int ROWB = WF == W_F32 ? 0 : WF == W_BF16 ? 64 : WF == W_FP8 ? 32 : 16;   // bytes of a row in a K piece
-    __shared__ f32x4_t red[kDecWaves][MT * NT][64];
+    __shared__ f32x4_t red[NW][MT * NT][64];
     __shared__ int32_t s_slot[kMaxExp], s_off[kMaxExp], s_cnt[kMaxExp], s_rec[kDecMaxRoutes];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -387,12 +389,12 @@ __global__ __launch_bounds__(kDecWaves * 64) void k_dec_proj(DecArgs a)
     const int K = a.K, N = a.N, nchunk = a.nchunk;
     // entries past the last slot with routes are there, and not used
     const int n_act = *a.l.n_act;
-    for (int i = tid; i < a.slots; i += kDecWaves * 64) {
+    for (int i = tid; i < a.slots; i += NW * 64) {
         s_slot[i] = a.l.slot[i];
         s_off[i] = a.l.off[i];
         s_cnt[i] = a.l.cnt[i];
     }
-    for (int i = tid; i < a.R; i += kDecWaves * 64) s_rec[i] = a.l.rec[i];
+    for (int i = tid; i < a.R; i += NW * 64) s_rec[i] = a.l.rec[i];
     __syncthreads();
 
     // Tiles of this workgroup. Gate/up: every gridDim-th of all. Down: one
@@ -420,7 +422,7 @@ __global__ __launch_bounds__(kDecWaves * 64) void k_dec_proj(DecArgs a)
     if (act >= n_act) return;   // down: fewer slots than groups; the others arrive alone
 
     const int steps = (K + KS - 1) / KS;
-    const int s0 = (int)((int64_t)steps * wave / kDecWaves), s1 = (int)((int64_t)steps * (wave + 1) / kDecWaves);
+    const int s0 = (int)((int64_t)steps * wave / NW), s1 = (int)((int64_t)steps * (wave + 1) / NW);
 
     // Where a tile's weights are: the slot's slice as a buffer, this lane's
     // offset of step 0, and bytes from step to step.
@@ -634,10 +636,10 @@ __global__ __launch_bounds__(kDecWaves * 64) void k_dec_proj(DecArgs a)
         auto total = [&](int g, int l) {
             f32x4_t v = red[0][g][l];
 #pragma unroll
-            for (int w = 1; w < kDecWaves; ++w) v += red[w][g][l];
+            for (int w = 1; w < NW; ++w) v += red[w][g][l];
             return v;
         };
-        static_assert(MT * (GATEUP ? 2 : NT) <= kDecWaves, "a thread has one result");
+        static_assert(MT * (GATEUP ? 2 : NT) <= NW, "a thread has one result");
         if constexpr (GATEUP) {
             // groups 0, 1 are gate rows, 2, 3 the up rows of the same 32 units
             static_assert(NT == 4, "a tile is 32 gate and 32 up rows");
@@ -687,7 +689,7 @@ __global__ __launch_bounds__(kDecWaves * 64) void k_dec_proj(DecArgs a)
                 // rows: Y_t += the token's route rows in ascending j.
                 if (last_to_arrive(a.ctr + chunk, min(groups, n_act))) {
                     const int n = n0 + 4 * (tid % (4 * NT));
-                    for (int t = tid / (4 * NT); t < a.T && n < N; t += kDecWaves * 16 / NT) {
+                    for (int t = tid / (4 * NT); t < a.T && n < N; t += NW * 16 / NT) {
                         float4 y = *(const float4 *)(a.Y + (int64_t)t * a.ldy + n);
                         const float *Yr = (const float *)a.out + (int64_t)t * a.kp * a.ldo + n;
 #pragma unroll 4
@@ -714,26 +716,26 @@ __global__ __launch_bounds__(kDecWaves * 64) void k_dec_proj(DecArgs a)
 // Persistent workgroups: two per compute unit of the 256.
 constexpr int kDecGrid = DEC_GRID;
 
-template <int WF, int MT, int NT, bool GATEUP>
+template <int WF, int MT, int NT, int NW, bool GATEUP>
 hipError_t launch_proj_n(const moe_shape &s, DecArgs a, hipStream_t st)
 {
     a.nchunk = (a.N + 16 * NT - 1) / (16 * NT);
     // at most this many slots have routes
     a.slots = (int)std::min<int64_t>(s.E + s.n_shared, a.R);
-    const int64_t most = kDecGrid, tiles = (int64_t)a.slots * a.nchunk;
+    const int64_t most = kDecGrid * 8 / NW, tiles = (int64_t)a.slots * a.nchunk;
     int64_t grid = std::min(most, tiles);
     if (!GATEUP && a.nchunk < grid) grid = grid / a.nchunk * a.nchunk;
-    hipLaunchKernelGGL((k_dec_proj<WF, MT, NT, GATEUP>), dim3((unsigned)grid), dim3(kDecWaves * 64), 0, st, a);
+    hipLaunchKernelGGL((k_dec_proj<WF, MT, NT, NW, GATEUP>), dim3((unsigned)grid), dim3(NW * 64), 0, st, a);
     return hipGetLastError();
 }
 
 template <int WF, bool GATEUP>
 hipError_t launch_proj_t(const moe_shape &s, const DecArgs &a, hipStream_t st)
 {
-    if (s.T <= 16) return launch_proj_n<WF, 1, 4, GATEUP>(s, a, st);
-    if (s.T <= 32) return launch_proj_n<WF, 2, 4, GATEUP>(s, a, st);
+    if (s.T <= 16) return launch_proj_n<WF, 1, 4, DEC_NW1, GATEUP>(s, a, st);
+    if (s.T <= 32) return launch_proj_n<WF, 2, 4, 8, GATEUP>(s, a, st);
     // 64 routes in three terms each: 32 rows, or the sums do not fit the registers
-    return launch_proj_n<WF, 4, GATEUP ? 4 : 2, GATEUP>(s, a, st);
+    return launch_proj_n<WF, 4, GATEUP ? 4 : 2, 8, GATEUP>(s, a, st);
 }
 
 }  // namespace

@@ -835,7 +835,8 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
                        void *ws, hipStream_t st)
 {
     int32_t *list = ws_at<int32_t>(ws, w.list), *ctr = ws_at<int32_t>(ws, w.ctr);
-    const DecLists lists{list, list + 1, list + 1 + kMaxExp, list + 1 + 2 * kMaxExp, list + 1 + 3 * kMaxExp};
+    const DecLists lists{list, list + 1, list + 1 + kDecMaxEntries, list + 1 + 2 * kDecMaxEntries,
+                         list + 1 + 3 * kDecMaxEntries};
     DecRouteArgs q{};
     q.X = X;
     q.ldx = s.ldx;
@@ -850,6 +851,7 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
     q.n_shared = s.n_shared;
     q.renorm = s.renorm;
     q.P = s.P;
+    q.rpe = dec_rpe(s);
     q.idx = r.topk_idx;
     q.w = r.topk_w;
     q.ctr = ctr;
@@ -857,6 +859,8 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
     HIP_TRY(TIMED(MOE_KERNEL_ROUTER, st, launch_dec_route(s, q, phi, st)), "route launch");
     DecArgs g{};
     g.l = lists;
+    g.rpe = q.rpe;
+    g.entries = dec_entries(s);
     g.T = s.T;
     g.Y = Y;
     g.ldy = s.ldy;

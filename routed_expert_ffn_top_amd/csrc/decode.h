@@ -12,6 +12,17 @@ constexpr int kDecRows = 32;                           // fewest output columns 
 constexpr int kDecMaxD = MOE_DECODE_MAX_D;
 constexpr int kDecTokBlock = 4;                        // tokens per route workgroup
 
+// The routes sorted by slot, at most rpe to an entry: entry a < *n_act is a slot
+// and up to rpe of its routes, rec[off .. off + cnt).
+constexpr int kDecMaxEntries = kMaxExp + kDecMaxRoutes / 5;
+int dec_rpe(const moe_shape &s);   // 5, 16, 32 or 64
+inline int dec_entries(const moe_shape &s)   // at most this many
+{
+    const int R = s.T * (s.k + s.n_shared), ne = s.E + s.n_shared;
+    const int e = ne + R / dec_rpe(s);
+    return e < R ? e : R;
+}
+
 // Byte offsets of the decode workspace's regions. The counters stand first and
 // have one size, so that they stay where they are when the shape changes: they
 // are zero between calls (cleared once by moe_decode_workspace_init; the last
@@ -32,15 +43,13 @@ inline DecLayout dec_layout(const moe_shape &s)
     size_t o = 0;
     w.ctr = o;    o = align_up(o + (size_t)(1 + kDecMaxT + kDecMaxD / kDecRows) * 4, 256);
     w.logits = o; o = align_up(o + (size_t)s.T * s.E * 4, 256);
-    w.list = o;   o = align_up(o + (size_t)(1 + 3 * kMaxExp + kDecMaxRoutes) * 4, 256);
+    w.list = o;   o = align_up(o + (size_t)(1 + 3 * kDecMaxEntries + kDecMaxRoutes) * 4, 256);
     w.H = o;      o = align_up(o + R * s.f * (act_bf16(s) ? 6 : 4), 256);
     w.Yr = o;     o = align_up(o + R * s.d * 4, 256);
     w.total = o;
     return w;
 }
 
-// The routes sorted by slot: entry a < *n_act is a slot with routes, its
-// routes rec[off .. off + cnt) in ascending route order.
 struct DecLists {
     int32_t *n_act, *slot, *off, *cnt, *rec;
 };
@@ -53,7 +62,7 @@ struct DecArgs {
     int64_t slot_bytes;   // bytes between slots
     int64_t scale_off;    // fp8: bytes from a slice's start to its row scales
     int64_t slice_bytes;  // of one slice, below 2^31
-    int N, K, kp, R, nchunk, slots;
+    int N, K, kp, R, nchunk, entries, rpe;
     void *out;            // gate/up: H; down: Yr
     int64_t ldo;
     const float *topk_w;
@@ -69,7 +78,7 @@ struct DecRouteArgs {
     const float *Wr, *bias;   // Wr null: logits holds the caller's
     const float *given;
     float *logits;
-    int T, d, E, k, n_shared, renorm, P;
+    int T, d, E, k, n_shared, renorm, P, rpe;
     int32_t *idx;
     float *w;
     int32_t *ctr;

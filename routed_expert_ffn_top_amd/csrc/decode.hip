@@ -23,11 +23,9 @@
 // H is kept to full fp32 between the projections: it is written as three bf16
 // terms h = h1 + h2 + h3 of 8 bits each, cut (not rounded) from fp32, which
 // is exact, and the down projection multiplies each weight operand by all
-// three. A slot with at most 5 routes takes them as 15 of the 16 columns of one
-// operand (column 3 i + j: term j of route i); with more routes the three terms
-// are three instructions. Either way each term has its own sums, joined in one
-// order, so a token's bits hang on nothing but the token. fp32 layers keep H
-// as fp32 and use the fp32 matrix instruction.
+// three: 5 routes are 15 of the 16 columns of one operand (column 3 i + j: term
+// j of route i), joined at the end. So up to 5 routes of a slot cost what one
+// does. fp32 layers keep H as fp32 and use the fp32 matrix instruction.
 #include <algorithm>
 #include <type_traits>
 
@@ -268,7 +266,8 @@ __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
     __syncthreads();
     // thread tid: slots 2 tid and 2 tid + 1
     const int c0 = cnt[2 * tid], c1 = cnt[2 * tid + 1];
-    int so = c0 + c1, sn = (c0 > 0) + (c1 > 0);
+    const int e0 = (c0 + a.rpe - 1) / a.rpe, e1 = (c1 + a.rpe - 1) / a.rpe;
+    int so = c0 + c1, sn = e0 + e1;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         const int u = __shfl_up(so, o, 64), n = __shfl_up(sn, o, 64);
@@ -288,19 +287,18 @@ __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
     }
     if (tid == 255) *a.l.n_act = sn;
     so -= c0 + c1;
-    sn -= (c0 > 0) + (c1 > 0);
+    sn -= e0 + e1;
     off[2 * tid] = so;
     off[2 * tid + 1] = so + c0;
-    if (c0) {
-        a.l.slot[sn] = 2 * tid;
-        a.l.off[sn] = so;
-        a.l.cnt[sn] = c0;
-        ++sn;
-    }
-    if (c1) {
-        a.l.slot[sn] = 2 * tid + 1;
-        a.l.off[sn] = so + c0;
-        a.l.cnt[sn] = c1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int c = h ? c1 : c0, o = h ? so + c0 : so;
+        for (int q = 0; q < c; q += a.rpe) {
+            a.l.slot[sn] = 2 * tid + h;
+            a.l.off[sn] = o + q;
+            a.l.cnt[sn] = min(a.rpe, c - q);
+            ++sn;
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -337,16 +335,13 @@ __device__ __forceinline__ bf16x8_t fp4_operand(uint32_t w, float scale)
 }
 
 #ifndef DEC_U
-#define DEC_U (MT == 1 || (MT == 2 && PL == 1 && WF == W_BF16) ? 2 : 1)
+#define DEC_U ((WF == W_BF16 || WF == W_F32) && (RPE <= 16 || (RPE == 32 && PL == 1)) ? 2 : 1)
 #endif
 #ifndef DEC_PRE
 #define DEC_PRE 48
 #endif
 #ifndef DEC_GRID
 #define DEC_GRID 512
-#endif
-#ifndef DEC_NW1
-#define DEC_NW1 4
 #endif
 constexpr uint32_t kNowhere = 0x80000000u;   // a buffer offset past every slice: such a load gives zeros and reads nothing
 
@@ -361,7 +356,7 @@ __device__ __forceinline__ void lds_barrier()
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// WF: weight format. MT: 16-row groups of routes a slot can have (T <= 16 MT).
+// WF: weight format. RPE: an entry of the lists has at most this many routes.
 // NT: 16-row groups of the slice per tile.
 //
 // The workgroups are persistent: each walks its tiles (slot, 16 NT rows) and
@@ -372,24 +367,28 @@ __device__ __forceinline__ void lds_barrier()
 // it then leaves the weights in flight. Weights come through buffer loads, whose
 // bounds check makes a stretch that is not there zeros without a branch, so
 // that the number of loads in flight is the same on every path.
-template <int WF, int MT, int NT, int NW, bool GATEUP>
-__global__ __launch_bounds__(NW * 64) void k_dec_proj(DecArgs a)
+template <int WF, int RPE, int NT, int NW, bool GATEUP>
+__global__ __launch_bounds__(NW * 64, 2) void k_dec_proj(DecArgs a)
 {
     constexpr int LK = WF == W_F32 ? 4 : WF == W_BF16 ? 8 : WF == W_FP8 ? 16 : 32;   // k values per lane and step
     constexpr int KS = 4 * LK;                                         // k values per step
     constexpr int NI = LK > 8 ? LK / 8 : 1;                            // bf16 operands of 8 per lane and step
-    constexpr int PL = !GATEUP && WF != W_F32 ? 3 : 1;                 // terms of the second operand
+    constexpr int PL = !GATEUP && WF != W_F32 ? 3 : 1;                 // terms (columns) per route
+    constexpr int RG = 16 / PL, G = (RPE + RG - 1) / RG;               // routes per operand, operands
+    constexpr int MT = (RPE + 15) / 16;                                // 16-route groups of the joined sums
     constexpr int U = DEC_U; // steps per stretch
+    constexpr int GP = G < DEC_PRE / (U * NI * 4) ? G : (DEC_PRE / (U * NI * 4) > 1 ? DEC_PRE / (U * NI * 4) : 1);
+                                                                       // operands requested ahead of the weights
     constexpr int ROWB = WF == W_F32 ? 0 : WF == W_BF16 ? 64 : WF == W_FP8 ? 32 : 16;   // bytes of a row in a K piece
     __shared__ f32x4_t red[NW][MT * NT][64];
-    __shared__ int32_t s_slot[kMaxExp], s_off[kMaxExp], s_cnt[kMaxExp], s_rec[kDecMaxRoutes];
+    __shared__ int32_t s_slot[kDecMaxEntries], s_off[kDecMaxEntries], s_cnt[kDecMaxEntries], s_rec[kDecMaxRoutes];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int K = a.K, N = a.N, nchunk = a.nchunk;
-    // entries past the last slot with routes are there, and not used
+    // entries past the last are there, and not used
     const int n_act = *a.l.n_act;
-    for (int i = tid; i < a.slots; i += NW * 64) {
+    for (int i = tid; i < a.entries; i += NW * 64) {
         s_slot[i] = a.l.slot[i];
         s_off[i] = a.l.off[i];
         s_cnt[i] = a.l.cnt[i];
@@ -496,16 +495,14 @@ __global__ __launch_bounds__(NW * 64) void k_dec_proj(DecArgs a)
         Src nsrc = source(more ? nact : act, more ? nch : chunk);
         if constexpr (WF == W_F32) nsrc.at = (more ? nch : chunk) * (16 * NT) - nsrc.nb * kWRows + r;
 
-        // second operand of this lane: tokens (gate/up), routes or a route's term (down)
-        const bool packed = PL == 3 && cnt <= 5;
-        const int nmt = MT == 1 ? 1 : (cnt + 15) / 16;
-        const char *xp[MT];
+        // second operands of this lane: tokens (gate/up) or terms of routes (down)
+        const int ng = G == 1 ? 1 : (cnt + RG - 1) / RG;
+        const char *xp[G];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int col = packed ? min(r / 3, cnt - 1) : min(16 * m + r, cnt - 1);
-            const int i = s_rec[off + col];
-            xp[m] = (const char *)a.X + ((int64_t)(GATEUP ? i / a.kp : i) * a.ldx +
-                                         (packed ? (int64_t)(r % 3) * a.R * a.ldx : 0)) * (WF == W_F32 ? 4 : 2);
+        for (int g = 0; g < G; ++g) {
+            const int i = s_rec[off + min(g * RG + min(r / PL, RG - 1), cnt - 1)];
+            xp[g] = (const char *)a.X + ((int64_t)(GATEUP ? i / a.kp : i) * a.ldx +
+                                         (PL == 3 ? (int64_t)(r % 3) * a.R * a.ldx : 0)) * (WF == W_F32 ? 4 : 2);
         }
         // what this thread needs for its result (one of 4 rows x 1 route), asked
         // for now: at the end of the tile it would wait behind the weights
@@ -521,114 +518,96 @@ __global__ __launch_bounds__(NW * 64) void k_dec_proj(DecArgs a)
             rs0 = *(const f32x4_t *)(S + (int64_t)(n0 + min(rn, 16 * NT - 4)) * 4);
             if (GATEUP) rs1 = *(const f32x4_t *)(S + (int64_t)(n0 + 32 + rn) * 4);
         }
-        f32x4_t acc[PL][MT][NT];
+        f32x4_t acc[G][NT];
 #pragma unroll
-        for (int pl = 0; pl < PL; ++pl)
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) acc[pl][m][t] = f32x4_t{0, 0, 0, 0};
+            for (int t = 0; t < NT; ++t) acc[g][t] = f32x4_t{0, 0, 0, 0};
 
-        // terms: instructions per first operand and column group (1 or PL)
-        auto sweep = [&](auto terms) {
-            constexpr int TM = decltype(terms)::value;
-            constexpr bool PRE = U * MT * TM * NI * 4 <= DEC_PRE;   // the whole stretch's operand at once
-            constexpr int XI = PRE ? NI : 1;
-            int s = s0;
-            do {
-                u32x4_t x[U][MT][TM][XI];
-                auto load_x = [&](int u, int i0) {
-                    const int k = (s + u) * KS + q * LK;
-                    const bool in = s + u < s1 && k < K;
-                    const int kc = in ? k : 0;
+        int s = s0;
+        do {
+            u32x4_t x[GP][U][NI];
+            auto load_x = [&](u32x4_t &d, int g, int u, int i) {
+                const int k = (s + u) * KS + q * LK;
+                const bool in = s + u < s1 && k < K;
+                d = *(const u32x4_t *)(xp[g] + ((in ? k : 0) + 8 * i) * (WF == W_F32 ? 4 : 2));
+                // a weight of zero times whatever stands there is to add nothing
+                if (WF == W_FP4 || WF == W_F32)
+                    if (!in) d = u32x4_t{0, 0, 0, 0};
+            };
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+            for (int g = 0; g < GP; ++g) {
+                if (g > 0 && g >= ng) continue;
 #pragma unroll
-                        for (int pl = 0; pl < TM; ++pl)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                            for (int i = 0; i < XI; ++i) {
-                                const char *p = xp[m] + ((int64_t)pl * a.R * a.ldx + kc + 8 * (i0 + i)) * (WF == W_F32 ? 4 : 2);
-                                x[u][m][pl][i] = *(const u32x4_t *)p;
-                                // a weight of zero times whatever stands there is to add nothing
-                                if (WF == W_FP4 || WF == W_F32)
-                                    if (!in) x[u][m][pl][i] = u32x4_t{0, 0, 0, 0};
-                            }
-                };
-                if constexpr (PRE)
+                    for (int i = 0; i < NI; ++i) load_x(x[g][u][i], g, u, i);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const bool last = s + U >= s1;
+            request(nxt, last ? nsrc : src, last ? s0 : s + U, !last || more);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int u = 0; u < U; ++u) load_x(u, 0);
-                __builtin_amdgcn_sched_barrier(0);
-                const bool last = s + U >= s1;
-                request(nxt, last ? nsrc : src, last ? s0 : s + U, !last || more);
-                __builtin_amdgcn_sched_barrier(0);
+            for (int u = 0; u < U; ++u) {
+                if (s + u >= s1) continue;
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (s + u >= s1) continue;
+                for (int i = 0; i < NI; ++i) {
+                    bf16x8_t wv[NT];
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        if constexpr (!PRE) load_x(u, i);
+                    for (int t = 0; t < NT; ++t) {
+                        if constexpr (WF == W_BF16) wv[t] = __builtin_bit_cast(bf16x8_t, cur.w[u][t]);
+                        if constexpr (WF == W_FP8) wv[t] = fp8_operand(cur.w[u][t], i);
+                        if constexpr (WF == W_FP4) wv[t] = fp4_operand(cur.w[u][t][i], e8m0(cur.sc[u][t]));
+                    }
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        if (g > 0 && g >= ng) continue;
+                        u32x4_t xv;
+                        if (g < GP)
+                            xv = x[g < GP ? g : 0][u][i];
+                        else
+                            load_x(xv, g, u, i);
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            bf16x8_t wv;
-                            if constexpr (WF == W_BF16) wv = __builtin_bit_cast(bf16x8_t, cur.w[u][t]);
-                            if constexpr (WF == W_FP8) wv = fp8_operand(cur.w[u][t], i);
-                            if constexpr (WF == W_FP4) wv = fp4_operand(cur.w[u][t][i], e8m0(cur.sc[u][t]));
+                            if constexpr (WF == W_F32) {
 #pragma unroll
-                            for (int m = 0; m < MT; ++m) {
-                                if (m >= nmt) continue;
-                                if constexpr (WF == W_F32) {
-#pragma unroll
-                                    for (int c = 0; c < 4; ++c)
-                                        acc[0][m][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                                            __uint_as_float(cur.w[u][t][c]), __uint_as_float(x[u][m][0][0][c]),
-                                            acc[0][m][t], 0, 0, 0);
-                                } else {
-#pragma unroll
-                                    for (int pl = 0; pl < TM; ++pl)
-                                        acc[pl][m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                            wv, __builtin_bit_cast(bf16x8_t, x[u][m][pl][PRE ? i : 0]), acc[pl][m][t],
-                                            0, 0, 0);
-                                }
+                                for (int c = 0; c < 4; ++c)
+                                    acc[g][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                                        __uint_as_float(cur.w[u][t][c]), __uint_as_float(xv[c]), acc[g][t], 0, 0, 0);
+                            } else {
+                                acc[g][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                    wv[t], __builtin_bit_cast(bf16x8_t, xv), acc[g][t], 0, 0, 0);
                             }
                         }
                     }
                 }
-                cur = nxt;
-                s += U;
-            } while (s < s1);
-        };
-        if constexpr (PL == 3) {
-            if (packed)
-                sweep(std::integral_constant<int, 1>());
-            else
-                sweep(std::integral_constant<int, PL>());
-        } else {
-            sweep(std::integral_constant<int, 1>());
-        }
+            }
+            cur = nxt;
+            s += U;
+        } while (s < s1);
 
-        // this wave's sums, terms joined in ascending order, to LDS
+        // this wave's sums, a route's terms joined in ascending order, to LDS
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int g = 0; g < G; ++g) {
+            if (g > 0 && g >= ng) continue;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                f32x4_t v = acc[0][m][t];
+                f32x4_t v = acc[g][t];
                 if constexpr (PL == 3) {
-                    if (packed) {
-                        if (m > 0) continue;
-                        f32x4_t v1, v2;
+                    f32x4_t v1, v2;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            v1[c] = __shfl_down(v[c], 1, 64);
-                            v2[c] = __shfl_down(v[c], 2, 64);
-                        }
-                        v = (v + v1) + v2;
-                        if (r % 3 == 0) red[wave][t][(lane & 48) + r / 3] = v;   // r = 15 writes column 5, which is not read
-                        continue;
+                    for (int c = 0; c < 4; ++c) {
+                        v1[c] = __shfl_down(v[c], 1, 64);
+                        v2[c] = __shfl_down(v[c], 2, 64);
                     }
-                    v = (v + acc[1][m][t]) + acc[2][m][t];
+                    v = (v + v1) + v2;
+                    const int row = g * RG + r / 3;
+                    if (r % 3 == 0 && r < 15 && row < 16 * MT) red[wave][(row >> 4) * NT + t][(lane & 48) + (row & 15)] = v;
+                } else {
+                    red[wave][g * NT + t][lane] = v;
                 }
-                red[wave][m * NT + t][lane] = v;
             }
+        }
         lds_barrier();
 
         // Result layout: element c of lane l is weight row 4 (l / 16) + c of its
@@ -716,26 +695,27 @@ __global__ __launch_bounds__(NW * 64) void k_dec_proj(DecArgs a)
 // Persistent workgroups: two per compute unit of the 256.
 constexpr int kDecGrid = DEC_GRID;
 
-template <int WF, int MT, int NT, int NW, bool GATEUP>
+template <int WF, int RPE, int NT, int NW, bool GATEUP>
 hipError_t launch_proj_n(const moe_shape &s, DecArgs a, hipStream_t st)
 {
     a.nchunk = (a.N + 16 * NT - 1) / (16 * NT);
-    // at most this many slots have routes
-    a.slots = (int)std::min<int64_t>(s.E + s.n_shared, a.R);
-    const int64_t most = kDecGrid * 8 / NW, tiles = (int64_t)a.slots * a.nchunk;
+    const int64_t most = kDecGrid * 8 / NW, tiles = (int64_t)a.entries * a.nchunk;
     int64_t grid = std::min(most, tiles);
     if (!GATEUP && a.nchunk < grid) grid = grid / a.nchunk * a.nchunk;
-    hipLaunchKernelGGL((k_dec_proj<WF, MT, NT, NW, GATEUP>), dim3((unsigned)grid), dim3(NW * 64), 0, st, a);
+    hipLaunchKernelGGL((k_dec_proj<WF, RPE, NT, NW, GATEUP>), dim3((unsigned)grid), dim3(NW * 64), 0, st, a);
     return hipGetLastError();
 }
 
 template <int WF, bool GATEUP>
 hipError_t launch_proj_t(const moe_shape &s, const DecArgs &a, hipStream_t st)
 {
-    if (s.T <= 16) return launch_proj_n<WF, 1, 4, DEC_NW1, GATEUP>(s, a, st);
-    if (s.T <= 32) return launch_proj_n<WF, 2, 4, 8, GATEUP>(s, a, st);
+    switch (a.rpe) {
+    case 5: return launch_proj_n<WF, 5, 4, 4, GATEUP>(s, a, st);
+    case 16: return launch_proj_n<WF, 16, 4, 4, GATEUP>(s, a, st);
+    case 32: return launch_proj_n<WF, 32, 4, 8, GATEUP>(s, a, st);
     // 64 routes in three terms each: 32 rows, or the sums do not fit the registers
-    return launch_proj_n<WF, 4, GATEUP ? 4 : 2, 8, GATEUP>(s, a, st);
+    default: return launch_proj_n<WF, 64, GATEUP ? 4 : 2, 8, GATEUP>(s, a, st);
+    }
 }
 
 }  // namespace
@@ -756,6 +736,23 @@ static hipError_t launch_route_t(const DecRouteArgs &a, const PhiArg &phi, hipSt
 hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const PhiArg &phi, hipStream_t st)
 {
     return act_bf16(s) ? launch_route_t<uint16_t>(a, phi, st) : launch_route_t<float>(a, phi, st);
+}
+
+// Routes per entry of the lists: the fewest of what the kernels are built for
+// that hold most slots' routes whole (7/4 of the mean of the experts hit). A
+// slot with more has several entries and its weights are read again for each;
+// a kernel for more routes has more sums, and with them fewer waves a compute
+// unit. (16 tokens of 8 routes on 64 experts, MXFP4: RPE_A us for 5, RPE_B for 16.)
+int dec_rpe(const moe_shape &s)
+{
+    double miss = 1.0;   // that a routed expert is hit by none of the tokens
+    for (int t = 0; t < s.T; ++t) miss *= 1.0 - (double)s.k / s.E;
+    const double mean = (double)s.T * s.k / (s.E * (1.0 - miss));
+    const double want = std::min<double>(s.T, 1.75 * mean);
+#ifdef DEC_RPE
+    return DEC_RPE;
+#endif
+    return want <= 5 ? 5 : want <= 16 ? 16 : want <= 32 ? 32 : 64;
 }
 
 hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a, bool gateup, hipStream_t st)

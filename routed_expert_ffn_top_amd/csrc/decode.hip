@@ -121,17 +121,19 @@ __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
     constexpr int XE = 16 / sizeof(TX), XV = 8 / XE;   // x values per 16 bytes, 16-byte pieces per run
     __shared__ float part[TB][64];
     __shared__ uint64_t keys[4][64 * C + 2];
-    __shared__ int32_t cnt[kMaxExp], off[kMaxExp], wsum[2][4], sphi[kMaxExp];
+    __shared__ int32_t cnt[kMaxExp], off[kMaxExp], wsum[2][4], sphi[kMaxExp], s_idx[TB * 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int t0 = blockIdx.x * TB, nt = min(TB, a.T - t0);
     const int kp = a.k + a.n_shared;
+    // asked for before anything waits: kernel arguments come from far away
+    const int32_t phi0 = phi.v[tid], phi1 = phi.v[tid + 256];
     if (a.Wr) {
         if (wave < nt) {
             const int e0 = blockIdx.y * 4, p = lane & 15, d = a.d;
             const float *w = a.Wr + (int64_t)min(e0 + (lane >> 4), a.E - 1) * d + p * 8;
             const TX *x = (const TX *)a.X + (int64_t)(t0 + wave) * a.ldx + p * 8;
             float acc = 0.0f;
-            constexpr int U = 8;   // groups of 128 hidden indices in flight
+            constexpr int U = sizeof(TX) == 2 ? 16 : 8;   // groups of 128 hidden indices in flight
             const int ng = (d + 127) / 128;
             for (int g = 0; g < ng; g += U) {
                 u32x4_t wv[U][2], xv[U][XV];
@@ -232,25 +234,23 @@ __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
             const int e = lane + 64 * c;
             if (e < a.E && rank[c] < a.k) {
                 put(a.idx + r0 + rank[c], e);
+                s_idx[wave * kp + rank[c]] = e;
                 a.w[r0 + rank[c]] = den > 0.0f ? z[c] / den : 0.0f;
             }
         }
         if (lane < a.n_shared) {
             put(a.idx + r0 + a.k + lane, a.E + lane);
+            s_idx[wave * kp + a.k + lane] = a.E + lane;
             a.w[r0 + a.k + lane] = 1.0f;
         }
     }
-    if (gridDim.x > 1) {
-        if (!last_to_arrive(a.ctr, gridDim.x)) return;
-    } else {
-        __builtin_amdgcn_s_waitcnt(0);   // this workgroup's ids, read below past the caches
-    }
+    const bool alone = gridDim.x == 1;   // every token's ids are this workgroup's own
+    if (!alone && !last_to_arrive(a.ctr, gridDim.x)) return;
 
     // the routes by slot: counts, offsets, places
-    for (int s = tid; s < kMaxExp; s += 256) {
-        cnt[s] = 0;
-        sphi[s] = phi.v[s];
-    }
+    cnt[tid] = cnt[tid + 256] = 0;
+    sphi[tid] = phi0;
+    sphi[tid + 256] = phi1;
     __syncthreads();
     const int R = a.T * kp;
     constexpr int RT = kDecMaxRoutes / 256;
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
     for (int q = 0; q < RT; ++q) {
         const int i = tid + 256 * q;
         if (i < R) {
-            slot[q] = sphi[get(a.idx + i)];
+            slot[q] = sphi[alone ? s_idx[i] : get(a.idx + i)];
             pos[q] = atomicAdd(&cnt[slot[q]], 1);
         }
     }

@@ -611,25 +611,32 @@ hipError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, 
     return hipGetLastError();
 }
 
-template <bool SHIFT>
-static void launch_ring(const MxArgs &a, unsigned grid, hipStream_t st)
+// The ring kernel's time is that of whole tiles: 13 us for one round of tiles of
+// up to 128 rows and 19 us above (K = 2048), whatever they hold. The small
+// kernel's grows with its 32 x 64 pieces, 2.5 us for each 64 of them, and with
+// less than 16 rows a slot it is ahead at any size (64 slots of N = K = 2048: 1
+// row each 18 against 27 us, 16 rows 32 against 31, 64 rows 84 against 31; one
+// slot of 512 rows 13 against 19, of 2048 rows 38 against 20).
+static bool ring_pays(const MxArgs &a)
 {
-    hipLaunchKernelGGL((k_matmul_ring<256, 4, SHIFT>), dim3(grid), dim3(512), 0, st, a);
+#ifdef MX_RING_ROWS
+    return a.M >= (int64_t)MX_RING_ROWS * a.P;
+#endif
+    const int64_t slots = std::min(a.P, a.M), rows = a.M / slots;
+    const int64_t pieces = slots * ((rows + 31) / 32) * (a.N / 64);
+    return rows >= 16 && pieces >= (rows <= 128 ? 512 : 768);
 }
 
 hipError_t launch_matmul_mxfp4(const MxArgs &a, hipStream_t st)
 {
     if (a.M == 0) return hipSuccess;
-#ifndef MX_RING_ROWS
-#define MX_RING_ROWS 96
-#endif
-    if (a.M >= (int64_t)MX_RING_ROWS * a.P) {
+    if (ring_pays(a)) {
         const int64_t tiles = ((int64_t)(a.M + 255) / 256 + std::min(a.P, a.M) - 1) * ((a.N + 255) / 256);
         const unsigned grid = (unsigned)std::min<int64_t>(tiles, 256);   // one workgroup per compute unit
         if (a.K % 128 == 0 && ((uintptr_t)a.As & 3) == 0)
-            launch_ring<false>(a, grid, st);
+            hipLaunchKernelGGL((k_matmul_ring<256, 4, false>), dim3(grid), dim3(512), 0, st, a);
         else
-            launch_ring<true>(a, grid, st);
+            hipLaunchKernelGGL((k_matmul_ring<256, 4, true>), dim3(grid), dim3(512), 0, st, a);
         return hipGetLastError();
     }
     // at most this many row tiles: one partial tile per slot with records

@@ -421,3 +421,97 @@ def test_mxfp4_captured_and_on_another_stream():
         torch.cuda.current_stream().wait_stream(st)
         torch.cuda.synchronize()
         assert torch.equal(got[0], C) and torch.equal(got[1], V)
+
+
+# ---- sizes that the ring kernel takes (whole tiles of 256 x 256, stages of 128 k) ----
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(769, 2176, 128), (1100, 1408, 576), (2049, 832, 64), (1025, 1600, 640), (513, 4160, 1408),
+                                   (1024, 2048, 512)])
+def test_matmul_large_one_slice(M, N, K, dtype):
+    say(f"matmul, large, {M} x {N} x {K} {dtype}")
+    run_matmul(M, N, K, 1, [M], False, dtype)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("sizes,tail,N,K", [([257, 0, 255, 513, 1, 600], 31, 1088, 320), ([0] * 100 + [3000] + [0] * 50 + [129], 2, 256, 256),
+                                            ([40] * 66, 0, 512, 384), ([128, 129, 0, 256, 700], 5, 1152, 1024)])
+def test_matmul_large_groups(sizes, tail, N, K, gather):
+    say(f"matmul, large groups of {len(sizes)}, N={N} K={K}, {tail} rows behind, gather {gather}")
+    run_matmul(sum(sizes) + tail, N, K, len(sizes), sizes, gather, torch.float32, tail=tail, scale_spread=6)
+
+
+@pytest.mark.parametrize("off", [0, 2, 4, 6])
+def test_matmul_large_unaligned_scales(off):
+    """Scale bytes that start at any even address, at the end of their allocation."""
+    say(f"matmul, large, scales {off} bytes from a 16-byte address")
+    M, N, K = 900, 2048, 256
+    gen = torch.Generator(device="cuda").manual_seed(off)
+    x = torch.empty((M, K), device="cuda").normal_(generator=gen)
+    packed, W = pack(torch.empty((1, N, K), device="cuda").normal_(generator=gen))
+    c, s = quantise(x)
+    buf = torch.full((off + s.numel(),), 255, dtype=torch.uint8, device="cuda")
+    t = buf[off:].view(s.shape)
+    t.copy_(s)
+    C = torch.empty(M, N, device="cuda")
+    B.moe_matmul_mxfp4(c, t, packed[0], C)
+    torch.cuda.synchronize()
+    ref, mag = product(values(c, s).cuda(), W, [0, M], torch.arange(M, device="cuda"))
+    assert bool(((C.double() - ref).abs() <= gamma(2 * K) * mag).all())
+
+
+def test_matmul_large_same_bits_as_small():
+    say("matmul: a record's bits are the same in large and in small calls")
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    for K in (448, 512):
+        x = torch.empty((1300, K), device="cuda").normal_(generator=gen)
+        w = torch.empty((2, 1600, K), device="cuda").normal_(generator=gen)
+        packed, _ = pack(w)
+        c, s = quantise(x)
+        C = torch.empty(1300, 1600, device="cuda")
+        B.moe_matmul_mxfp4(c, s, packed, C, slot_offset=torch.tensor([0, 1290, 1300], dtype=torch.int32, device="cuda"))
+        D = torch.empty(1300, 1600, device="cuda")
+        for lo, hi, p in ((0, 1, 0), (1, 40, 0), (40, 160, 0), (1250, 1290, 0), (1290, 1300, 1)):
+            B.moe_matmul_mxfp4(c[lo:hi].clone(), s[lo:hi].clone(), packed[p], D[lo:hi])
+        torch.cuda.synchronize()
+        assert torch.equal(C[:160], D[:160]) and torch.equal(C[1250:], D[1250:])
+
+
+def test_matmul_large_nan_blocks_and_ranges():
+    say("matmul, large: NaN blocks stay in their rows and columns; rows and offsets out of range")
+    M, N, K = 800, 2048, 256
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.empty((M, K), device="cuda").normal_(generator=gen)
+    w = torch.empty((1, N, K), device="cuda").normal_(generator=gen)
+    packed, _ = pack(w)
+    c, s = quantise(x)
+    C = torch.empty(M, N, device="cuda")
+    B.moe_matmul_mxfp4(c, s, packed[0], C)
+    c2, s2, bad = c.clone(), s.clone(), [5, 255, 256, 799]
+    for i, r in enumerate(bad):
+        s2[r, i * 2] = 255
+    w2 = packed.clone()
+    B.moe_pack_down(B.make_shape(1, N, K, 1, 1, dtype="bf16_fp4w"), with_nan(w[0], 1500, 130), w2[0], 1, 0, 0)
+    D, E = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    B.moe_matmul_mxfp4(c2, s2, packed[0], D)
+    B.moe_matmul_mxfp4(c, s, w2[0], E)
+    rec = torch.arange(M, dtype=torch.int32, device="cuda")
+    rec[3], rec[700] = -9, M + 70
+    F = torch.zeros(M + 40, N, device="cuda")
+    far = torch.tensor([-7, M + 1000], dtype=torch.int32, device="cuda")
+    B.moe_matmul_mxfp4(c, s, packed, F[:M], slot_offset=far, row_index=rec)
+    torch.cuda.synchronize()
+    keep = torch.ones(M, dtype=torch.bool)
+    keep[bad] = False
+    assert torch.equal(C[keep], D[keep]) and bool(torch.isnan(D[~keep]).all())
+    cols = torch.arange(N) != 1500
+    assert torch.equal(C[:, cols], E[:, cols]) and bool(torch.isnan(E[:, 1500]).all())
+    want = C.clone()
+    want[3], want[700] = C[0], C[M - 1]
+    assert torch.equal(F[:M], want) and bool((F[M:] == 0).all())
+
+
+def with_nan(w, n, k):
+    w = w.clone()
+    w[n, k] = float("nan")
+    return B.mxfp4_slice(w)

@@ -856,7 +856,8 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
     q.w = r.topk_w;
     q.ctr = ctr;
     q.l = lists;
-    HIP_TRY(TIMED(MOE_KERNEL_ROUTER, st, launch_dec_route(s, q, phi, st)), "route launch");
+    const bool self = dec_self_routes(s, W_r != nullptr);
+    if (!self) HIP_TRY(TIMED(MOE_KERNEL_ROUTER, st, launch_dec_route(s, q, phi, st)), "route launch");
     DecArgs g{};
     g.l = lists;
     g.rpe = q.rpe;
@@ -879,7 +880,10 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
     g.K = s.d;
     g.out = ws_at<char>(ws, w.H);
     g.ldo = s.f;
-    HIP_TRY(TIMED(MOE_KERNEL_GATE_UP, st, launch_dec_proj(s, g, true, st)), "gate/up launch");
+    if (self)
+        HIP_TRY(TIMED(MOE_KERNEL_GATE_UP, st, launch_dec_route_proj(s, g, q, phi, st)), "gate/up launch");
+    else
+        HIP_TRY(TIMED(MOE_KERNEL_GATE_UP, st, launch_dec_proj(s, g, true, st)), "gate/up launch");
     h.X = g.out;
     h.ldx = s.f;
     h.W = a->plane_d;

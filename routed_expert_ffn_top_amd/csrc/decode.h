@@ -11,6 +11,7 @@ constexpr int kDecMaxRoutes = MOE_DECODE_MAX_ROUTES;   // T * K'
 constexpr int kDecRows = 32;                           // fewest output columns per workgroup (one counter each)
 constexpr int kDecMaxD = MOE_DECODE_MAX_D;
 constexpr int kDecTokBlock = 4;                        // tokens per route workgroup
+constexpr int kDecSelfRoutes = 256;                    // at most, where gate/up routes for itself
 
 // The routes sorted by slot, at most rpe to an entry: entry a < *n_act is a slot
 // and up to rpe of its routes, rec[off .. off + cnt).
@@ -85,6 +86,11 @@ struct DecRouteArgs {
     DecLists l;
 };
 
+// Whether gate/up does the routing itself (launch_dec_route_proj instead of
+// launch_dec_route and launch_dec_proj).
+bool dec_self_routes(const moe_shape &s, bool router);
+hipError_t launch_dec_route_proj(const moe_shape &s, const DecArgs &a, const DecRouteArgs &q, const PhiArg &phi,
+                                 hipStream_t st);
 hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const PhiArg &phi, hipStream_t st);
 hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a, bool gateup, hipStream_t st);
 

@@ -101,172 +101,146 @@ __device__ __forceinline__ uint64_t topk_key(float x, int e)
     return ((uint64_t)((u & 0x80000000u) ? ~u : (u | 0x80000000u)) << 32) | (uint32_t)~(uint32_t)e;
 }
 
-// Router, top-k and the routes by slot, in one launch. A workgroup takes 4
-// experts (16 lanes each) for 4 tokens, a wave a token: lane p of an expert
-// holds the partial sum p of the router's fixed order (runs of 8 hidden
-// indices, run r to partial sum r mod 16, ascending, one fused multiply-add a
-// term), so a wave's loads are whole 512-byte stretches of W_r and the bits
-// are the prompt router's. The last workgroup of a token block does its top-k
-// (a wave a token, the prompt kernel's arithmetic), and the last block of all
-// sorts the routes by slot. The order of the routes within a slot is that of
-// LDS atomics and is not fixed: it only says which column of a matrix operand
-// a route takes, and columns do not mix. Bound by latency: a wave has 32 KB
-// of W_r to read for d = 2048, and takes 8 groups of 128 hidden indices at once
-// so that two round trips do. (16 experts a workgroup, a wave 4 of them for 4
-// tokens: 15 us for one token instead of 8.7.)
-template <typename TX, int C>
-__global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
+// ---- routing ----
+// Router logits of one token for experts e0 .. e0+3, by one wave (16 lanes an
+// expert): lane p holds the partial sum p of the router's fixed order (runs of
+// 8 hidden indices, run r to partial sum r mod 16, ascending, one fused
+// multiply-add a term), so the loads are whole 512-byte stretches of W_r and
+// the bits are the prompt router's. U groups of 128 hidden indices are asked
+// for at once. part: 64 floats of this wave. out(e, logit) in lanes 0 .. 3.
+template <typename TX, int U, typename F>
+__device__ __forceinline__ void wave_logits(const DecRouteArgs &a, int t, int e0, float *part, F out)
 {
-    constexpr int TB = kDecTokBlock;
     constexpr int XE = 16 / sizeof(TX), XV = 8 / XE;   // x values per 16 bytes, 16-byte pieces per run
-    __shared__ float part[TB][64];
-    __shared__ uint64_t keys[4][64 * C + 2];
-    __shared__ int32_t cnt[kMaxExp], off[kMaxExp], wsum[2][4], sphi[kMaxExp], s_idx[TB * 64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int t0 = blockIdx.x * TB, nt = min(TB, a.T - t0);
-    const int kp = a.k + a.n_shared;
-    // asked for before anything waits: kernel arguments come from far away
-    const int32_t phi0 = phi.v[tid], phi1 = phi.v[tid + 256];
-    if (a.Wr) {
-        if (wave < nt) {
-            const int e0 = blockIdx.y * 4, p = lane & 15, d = a.d;
-            const float *w = a.Wr + (int64_t)min(e0 + (lane >> 4), a.E - 1) * d + p * 8;
-            const TX *x = (const TX *)a.X + (int64_t)(t0 + wave) * a.ldx + p * 8;
-            float acc = 0.0f;
-            constexpr int U = sizeof(TX) == 2 ? 16 : 8;   // groups of 128 hidden indices in flight
-            const int ng = (d + 127) / 128;
-            for (int g = 0; g < ng; g += U) {
-                u32x4_t wv[U][2], xv[U][XV];
+    const int lane = threadIdx.x & 63, p = lane & 15, d = a.d, ng = (d + 127) / 128;
+    const float *w = a.Wr + (int64_t)min(e0 + (lane >> 4), a.E - 1) * d + p * 8;
+    const TX *x = (const TX *)a.X + (int64_t)t * a.ldx + p * 8;
+    float acc = 0.0f;
+    for (int g = 0; g < ng; g += U) {
+        u32x4_t wv[U][2], xv[U][XV];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    // pieces at or past d are read from the row start and not used
+        for (int u = 0; u < U; ++u) {
+            // pieces at or past d are read from the row start and not used
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int i = (g + u) * 128 + 4 * h;
-                        wv[u][h] = *(const u32x4_t *)(w + (i + p * 8 < d ? i : -p * 8));
-                    }
+            for (int h = 0; h < 2; ++h) {
+                const int i = (g + u) * 128 + 4 * h;
+                wv[u][h] = *(const u32x4_t *)(w + (i + p * 8 < d ? i : -p * 8));
+            }
 #pragma unroll
-                    for (int h = 0; h < XV; ++h) {
-                        const int i = (g + u) * 128 + XE * h;
-                        xv[u][h] = *(const u32x4_t *)(x + (i + p * 8 < d ? i : -p * 8));
-                    }
+            for (int h = 0; h < XV; ++h) {
+                const int i = (g + u) * 128 + XE * h;
+                xv[u][h] = *(const u32x4_t *)(x + (i + p * 8 < d ? i : -p * 8));
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);   // all requested before the first is used
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float wc = __uint_as_float(wv[u][c >> 2][c & 3]);
+                float xc;
+                if constexpr (sizeof(TX) == 2) {
+                    const uint32_t w2 = xv[u][0][c >> 1];
+                    xc = __uint_as_float((c & 1) ? (w2 & 0xffff0000u) : (w2 << 16));
+                } else {
+                    xc = __uint_as_float(xv[u][c >> 2][c & 3]);
                 }
-                __builtin_amdgcn_sched_barrier(0);   // all requested before the first is used
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const float wc = __uint_as_float(wv[u][c >> 2][c & 3]);
-                        float xc;
-                        if constexpr (sizeof(TX) == 2) {
-                            const uint32_t w2 = xv[u][0][c >> 1];
-                            xc = __uint_as_float((c & 1) ? (w2 & 0xffff0000u) : (w2 << 16));
-                        } else {
-                            xc = __uint_as_float(xv[u][c >> 2][c & 3]);
-                        }
-                        const float s = __builtin_fmaf(xc, wc, acc);
-                        acc = (g + u) * 128 + p * 8 + c < d ? s : acc;
-                    }
+                const float s = __builtin_fmaf(xc, wc, acc);
+                acc = (g + u) * 128 + p * 8 + c < d ? s : acc;
             }
-            part[wave][lane] = acc;
-            __builtin_amdgcn_wave_barrier();   // the reads below are of this wave's writes
-            // lane < 4: the 16 partial sums of an expert in ascending order
-            if (lane < 4 && e0 + lane < a.E) {
-                float v[16];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) v[c] = part[wave][lane * 16 + c];
-                float s = v[0];
-#pragma unroll
-                for (int c = 1; c < 16; ++c) s = s + v[c];
-                put(a.logits + (int64_t)(t0 + wave) * a.E + e0 + lane, a.bias ? s + a.bias[e0 + lane] : s);
-            }
-        }
-        if (gridDim.y > 1) {
-            if (!last_to_arrive(a.ctr + 1 + blockIdx.x, gridDim.y)) return;
-        } else {
-            __builtin_amdgcn_s_waitcnt(0);   // this wave's logits, read below past the caches
-        }
     }
-
-    // top-k of this block's tokens, a wave a token
-    if (wave < nt) {
-        const float *L = (a.Wr ? a.logits : a.given) + (int64_t)(t0 + wave) * a.E;
-        const float NEG_INF = -__builtin_huge_valf();
-        float v[C];
-        uint64_t key[C];
-        int rank[C];
+    __builtin_amdgcn_wave_barrier();   // this wave's own writes and reads, in order
+    part[lane] = acc;
+    __builtin_amdgcn_wave_barrier();
+    if (lane < 4 && e0 + lane < a.E) {   // the 16 partial sums of an expert in ascending order
+        float v[16];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int e = lane + 64 * c;
-            v[c] = e < a.E ? get(L + e) : NEG_INF;
-            if (v[c] != v[c]) v[c] = NEG_INF;
-            key[c] = topk_key(v[c], e);
-            keys[wave][e] = e < a.E ? key[c] : 0ull;
-            rank[c] = 0;
-        }
-        if (lane < 2) keys[wave][64 * C + lane] = 0ull;
-        __builtin_amdgcn_wave_barrier();
+        for (int c = 0; c < 16; ++c) v[c] = part[lane * 16 + c];
+        float s = v[0];
+#pragma unroll
+        for (int c = 1; c < 16; ++c) s = s + v[c];
+        out(e0 + lane, a.bias ? s + a.bias[e0 + lane] : s);
+    }
+}
+
+// Top-k of one token by one wave, in the prompt kernel's arithmetic (lane l
+// holds experts l, l + 64, ..). logit(e); keys: 64 C + 2 words of this wave;
+// out(rank, expert, weight), shared experts included.
+template <int C, typename V, typename F>
+__device__ __forceinline__ void wave_topk(const DecRouteArgs &a, uint64_t *keys, V logit, F out)
+{
+    const int lane = threadIdx.x & 63;
+    const float NEG_INF = -__builtin_huge_valf();
+    float v[C];
+    uint64_t key[C];
+    int rank[C];
+    __builtin_amdgcn_wave_barrier();   // this wave's own writes and reads, in order
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = lane + 64 * c;
+        v[c] = e < a.E ? logit(e) : NEG_INF;
+        if (v[c] != v[c]) v[c] = NEG_INF;
+        key[c] = topk_key(v[c], e);
+        keys[e] = e < a.E ? key[c] : 0ull;
+        rank[c] = 0;
+    }
+    if (lane < 2) keys[64 * C + lane] = 0ull;
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll 8
-        for (int e2 = 0; e2 < ((a.E + 1) & ~1); e2 += 2) {
-            const uint64_t k0 = keys[wave][e2], k1 = keys[wave][e2 + 1];
+    for (int e2 = 0; e2 < ((a.E + 1) & ~1); e2 += 2) {
+        const uint64_t k0 = keys[e2], k1 = keys[e2 + 1];
 #pragma unroll
-            for (int c = 0; c < C; ++c) rank[c] += (int)(k0 > key[c]) + (int)(k1 > key[c]);
-        }
-        float m = NEG_INF;
-#pragma unroll
-        for (int c = 0; c < C; ++c) m = fmaxf(m, v[c]);
-        m = wave_max(m);
-        if (m == NEG_INF) m = 0.0f;
-        float z[C], s = 0.0f, ssel = 0.0f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int e = lane + 64 * c;
-            z[c] = e < a.E ? expf(v[c] - m) : 0.0f;
-            s += z[c];
-            if (e < a.E && rank[c] < a.k) ssel += z[c];
-        }
-        s = wave_sum(s);
-        ssel = wave_sum(ssel);
-        const float den = a.renorm ? ssel : s;
-        const int64_t r0 = (int64_t)(t0 + wave) * kp;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int e = lane + 64 * c;
-            if (e < a.E && rank[c] < a.k) {
-                put(a.idx + r0 + rank[c], e);
-                s_idx[wave * kp + rank[c]] = e;
-                a.w[r0 + rank[c]] = den > 0.0f ? z[c] / den : 0.0f;
-            }
-        }
-        if (lane < a.n_shared) {
-            put(a.idx + r0 + a.k + lane, a.E + lane);
-            s_idx[wave * kp + a.k + lane] = a.E + lane;
-            a.w[r0 + a.k + lane] = 1.0f;
-        }
+        for (int c = 0; c < C; ++c) rank[c] += (int)(k0 > key[c]) + (int)(k1 > key[c]);
     }
-    const bool alone = gridDim.x == 1;   // every token's ids are this workgroup's own
-    if (!alone && !last_to_arrive(a.ctr, gridDim.x)) return;
+    float m = NEG_INF;
+#pragma unroll
+    for (int c = 0; c < C; ++c) m = fmaxf(m, v[c]);
+    m = wave_max(m);
+    if (m == NEG_INF) m = 0.0f;
+    float z[C], s = 0.0f, ssel = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = lane + 64 * c;
+        z[c] = e < a.E ? expf(v[c] - m) : 0.0f;
+        s += z[c];
+        if (e < a.E && rank[c] < a.k) ssel += z[c];
+    }
+    s = wave_sum(s);
+    ssel = wave_sum(ssel);
+    const float den = a.renorm ? ssel : s;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = lane + 64 * c;
+        if (e < a.E && rank[c] < a.k) out(rank[c], e, den > 0.0f ? z[c] / den : 0.0f);
+    }
+    if (lane < a.n_shared) out(a.k + lane, a.E + lane, 1.0f);
+}
 
-    // the routes by slot: counts, offsets, places
+// The routes by slot, by a workgroup of 256: counts, offsets, places; at most
+// rpe routes to an entry. slot_of(i) of route i < R; put_entry(n, slot, off, cnt),
+// put_rec(place, i); returns the number of entries. The order of the routes
+// within a slot is that of LDS atomics and is not fixed: it only says which
+// column of a matrix operand a route takes, and columns do not mix.
+template <int RT, typename S, typename PE, typename PR>
+__device__ __forceinline__ int build_lists(int R, int rpe, int32_t *cnt, int32_t *off, int32_t *wsum, S slot_of,
+                                           PE put_entry, PR put_rec)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     cnt[tid] = cnt[tid + 256] = 0;
-    sphi[tid] = phi0;
-    sphi[tid + 256] = phi1;
     __syncthreads();
-    const int R = a.T * kp;
-    constexpr int RT = kDecMaxRoutes / 256;
     int slot[RT], pos[RT];
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
         const int i = tid + 256 * q;
         if (i < R) {
-            slot[q] = sphi[alone ? s_idx[i] : get(a.idx + i)];
+            slot[q] = slot_of(i);
             pos[q] = atomicAdd(&cnt[slot[q]], 1);
         }
     }
     __syncthreads();
     // thread tid: slots 2 tid and 2 tid + 1
     const int c0 = cnt[2 * tid], c1 = cnt[2 * tid + 1];
-    const int e0 = (c0 + a.rpe - 1) / a.rpe, e1 = (c1 + a.rpe - 1) / a.rpe;
+    const int e0 = (c0 + rpe - 1) / rpe, e1 = (c1 + rpe - 1) / rpe;
     int so = c0 + c1, sn = e0 + e1;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -277,15 +251,15 @@ __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
         }
     }
     if (lane == 63) {
-        wsum[0][wave] = so;
-        wsum[1][wave] = sn;
+        wsum[wave] = so;
+        wsum[4 + wave] = sn;
     }
     __syncthreads();
     for (int w = 0; w < wave; ++w) {
-        so += wsum[0][w];
-        sn += wsum[1][w];
+        so += wsum[w];
+        sn += wsum[4 + w];
     }
-    if (tid == 255) *a.l.n_act = sn;
+    const int all = wsum[4] + wsum[5] + wsum[6] + wsum[7];
     so -= c0 + c1;
     sn -= e0 + e1;
     off[2 * tid] = so;
@@ -293,17 +267,66 @@ __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int c = h ? c1 : c0, o = h ? so + c0 : so;
-        for (int q = 0; q < c; q += a.rpe) {
-            a.l.slot[sn] = 2 * tid + h;
-            a.l.off[sn] = o + q;
-            a.l.cnt[sn] = min(a.rpe, c - q);
-            ++sn;
-        }
+        for (int q = 0; q < c; q += rpe) put_entry(sn++, 2 * tid + h, o + q, min(rpe, c - q));
     }
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < RT; ++q)
-        if (tid + 256 * q < R) a.l.rec[off[slot[q]] + pos[q]] = tid + 256 * q;
+        if (tid + 256 * q < R) put_rec(off[slot[q]] + pos[q], tid + 256 * q);
+    return all;
+}
+
+// Router, top-k and the routes by slot, in one launch. A workgroup takes 4
+// experts for 4 tokens, a wave a token; the last workgroup of a token block
+// does its top-k, and the last block of all sorts the routes by slot. Bound by
+// latency: a wave has 32 KB of W_r to read for d = 2048, asked for at once (16
+// experts a workgroup, a wave 4 of them for 4 tokens: 15 us for one token
+// instead of 7.7).
+template <typename TX, int C>
+__global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
+{
+    constexpr int TB = kDecTokBlock;
+    __shared__ float part[TB][64];
+    __shared__ uint64_t keys[4][64 * C + 2];
+    __shared__ int32_t cnt[kMaxExp], off[kMaxExp], wsum[8], sphi[kMaxExp], s_idx[TB * 64];
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const int t0 = blockIdx.x * TB, nt = min(TB, a.T - t0);
+    const int kp = a.k + a.n_shared;
+    // asked for before anything waits: kernel arguments come from far away
+    const int32_t phi0 = phi.v[tid], phi1 = phi.v[tid + 256];
+    if (a.Wr) {
+        if (wave < nt)
+            wave_logits<TX, sizeof(TX) == 2 ? 16 : 8>(a, t0 + wave, blockIdx.y * 4, part[wave], [&](int e, float l) {
+                put(a.logits + (int64_t)(t0 + wave) * a.E + e, l);
+            });
+        if (gridDim.y > 1) {
+            if (!last_to_arrive(a.ctr + 1 + blockIdx.x, gridDim.y)) return;
+        } else {
+            __builtin_amdgcn_s_waitcnt(0);   // this wave's logits, read below past the caches
+        }
+    }
+    if (wave < nt) {
+        const float *L = (a.Wr ? a.logits : a.given) + (int64_t)(t0 + wave) * a.E;
+        const int64_t r0 = (int64_t)(t0 + wave) * kp;
+        wave_topk<C>(a, keys[wave], [&](int e) { return get(L + e); }, [&](int rank, int e, float w) {
+            put(a.idx + r0 + rank, e);
+            s_idx[wave * kp + rank] = e;
+            a.w[r0 + rank] = w;
+        });
+    }
+    const bool alone = gridDim.x == 1;   // every token's ids are this workgroup's own
+    if (!alone && !last_to_arrive(a.ctr, gridDim.x)) return;
+    sphi[tid] = phi0;
+    sphi[tid + 256] = phi1;
+    const int n = build_lists<kDecMaxRoutes / 256>(
+        a.T * kp, a.rpe, cnt, off, wsum, [&](int i) { return sphi[alone ? s_idx[i] : get(a.idx + i)]; },
+        [&](int n, int slot, int o, int c) {
+            a.l.slot[n] = slot;
+            a.l.off[n] = o;
+            a.l.cnt[n] = c;
+        },
+        [&](int place, int i) { a.l.rec[place] = i; });
+    if (tid == 0) *a.l.n_act = n;
 }
 
 // E8M0 scale byte -> fp32 2^(s-127); 255 is NaN
@@ -367,8 +390,14 @@ __device__ __forceinline__ void lds_barrier()
 // it then leaves the weights in flight. Weights come through buffer loads, whose
 // bounds check makes a stretch that is not there zeros without a branch, so
 // that the number of loads in flight is the same on every path.
+template <int WF, int RPE, int NT, int NW>
+struct ProjShared {
+    f32x4_t red[NW][(RPE + 15) / 16 * NT][64];
+    int32_t slot[kDecMaxEntries], off[kDecMaxEntries], cnt[kDecMaxEntries], rec[kDecMaxRoutes];
+};
+
 template <int WF, int RPE, int NT, int NW, bool GATEUP>
-__global__ __launch_bounds__(NW * 64, 2) void k_dec_proj(DecArgs a)
+__device__ __forceinline__ void proj_tiles(const DecArgs &a, const int n_act, ProjShared<WF, RPE, NT, NW> &sh)
 {
     constexpr int LK = WF == W_F32 ? 4 : WF == W_BF16 ? 8 : WF == W_FP8 ? 16 : 32;   // k values per lane and step
     constexpr int KS = 4 * LK;                                         // k values per step
@@ -380,21 +409,12 @@ __global__ __launch_bounds__(NW * 64, 2) void k_dec_proj(DecArgs a)
     constexpr int GP = G < DEC_PRE / (U * NI * 4) ? G : (DEC_PRE / (U * NI * 4) > 1 ? DEC_PRE / (U * NI * 4) : 1);
                                                                        // operands requested ahead of the weights
     constexpr int ROWB = WF == W_F32 ? 0 : WF == W_BF16 ? 64 : WF == W_FP8 ? 32 : 16;   // bytes of a row in a K piece
-    __shared__ f32x4_t red[NW][MT * NT][64];
-    __shared__ int32_t s_slot[kDecMaxEntries], s_off[kDecMaxEntries], s_cnt[kDecMaxEntries], s_rec[kDecMaxRoutes];
+    auto &red = sh.red;
+    const int32_t *s_slot = sh.slot, *s_off = sh.off, *s_cnt = sh.cnt, *s_rec = sh.rec;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, q = lane >> 4;
     const int K = a.K, N = a.N, nchunk = a.nchunk;
-    // entries past the last are there, and not used
-    const int n_act = *a.l.n_act;
-    for (int i = tid; i < a.entries; i += NW * 64) {
-        s_slot[i] = a.l.slot[i];
-        s_off[i] = a.l.off[i];
-        s_cnt[i] = a.l.cnt[i];
-    }
-    for (int i = tid; i < a.R; i += NW * 64) s_rec[i] = a.l.rec[i];
-    __syncthreads();
 
     // Tiles of this workgroup. Gate/up: every gridDim-th of all. Down: one
     // column chunk (every gridDim-th, where there are more chunks than
@@ -692,6 +712,77 @@ __global__ __launch_bounds__(NW * 64, 2) void k_dec_proj(DecArgs a)
     }
 }
 
+template <int WF, int RPE, int NT, int NW, bool GATEUP>
+__global__ __launch_bounds__(NW * 64, 2) void k_dec_proj(DecArgs a)
+{
+    __shared__ ProjShared<WF, RPE, NT, NW> sh;
+    const int tid = threadIdx.x;
+    // entries past the last are there, and not used
+    const int n_act = *a.l.n_act;
+    for (int i = tid; i < a.entries; i += NW * 64) {
+        sh.slot[i] = a.l.slot[i];
+        sh.off[i] = a.l.off[i];
+        sh.cnt[i] = a.l.cnt[i];
+    }
+    for (int i = tid; i < a.R; i += NW * 64) sh.rec[i] = a.l.rec[i];
+    __syncthreads();
+    proj_tiles<WF, RPE, NT, NW, GATEUP>(a, n_act, sh);
+}
+
+// Gate/up that routes for itself: every workgroup does the whole routing, and
+// the first writes it down. For few tokens and experts, where that takes less
+// than a launch of its own (dec_self_routes).
+template <int WF, int RPE>
+__global__ __launch_bounds__(256, 2) void k_dec_route_proj(DecArgs a, DecRouteArgs q, PhiArg phi)
+{
+    constexpr int NT = 4, NW = 4;
+    using TX = typename std::conditional<WF == W_F32, float, uint16_t>::type;
+    struct Scratch {   // in the place of the sums, which come later
+        float part[4][64], logit[4][64];
+        uint64_t keys[4][66];
+        int32_t cnt[kMaxExp], off[kMaxExp], wsum[8], idx[kDecSelfRoutes];
+    };
+    __shared__ ProjShared<WF, RPE, NT, NW> sh;
+    static_assert(sizeof(Scratch) <= sizeof(sh.red), "scratch");
+    Scratch &c = *(Scratch *)&sh.red;
+    const int tid = threadIdx.x, wave = tid >> 6, kp = a.kp;
+    const bool writes = blockIdx.x == 0;
+    for (int t = wave; t < a.T; t += NW) {
+        if (q.Wr)
+            for (int e0 = 0; e0 < q.E; e0 += 4)
+                wave_logits<TX, 8>(q, t, e0, c.part[wave], [&](int e, float l) { c.logit[wave][e] = l; });
+        wave_topk<1>(q, c.keys[wave], [&](int e) { return q.Wr ? c.logit[wave][e] : q.given[(int64_t)t * q.E + e]; },
+                     [&](int rank, int e, float w) {
+                         c.idx[t * kp + rank] = e;
+                         if (writes) {
+                             q.idx[t * kp + rank] = e;
+                             q.w[t * kp + rank] = w;
+                         }
+                     });
+    }
+    __syncthreads();
+    const int n_lists = build_lists<kDecSelfRoutes / 256>(
+        a.R, q.rpe, c.cnt, c.off, c.wsum, [&](int i) { return phi.v[c.idx[i]]; },
+        [&](int n, int slot, int o, int k) {
+            sh.slot[n] = slot;
+            sh.off[n] = o;
+            sh.cnt[n] = k;
+            if (writes) {
+                a.l.slot[n] = slot;
+                a.l.off[n] = o;
+                a.l.cnt[n] = k;
+            }
+        },
+        [&](int place, int i) {
+            sh.rec[place] = i;
+            if (writes) a.l.rec[place] = i;
+        });
+    const int n = __builtin_amdgcn_readfirstlane(n_lists);   // the same in every lane, and now known to be
+    if (writes && tid == 0) *a.l.n_act = n;
+    __syncthreads();
+    proj_tiles<WF, RPE, NT, NW, true>(a, n, sh);
+}
+
 // Persistent workgroups: two per compute unit of the 256.
 constexpr int kDecGrid = DEC_GRID;
 
@@ -731,6 +822,38 @@ static hipError_t launch_route_t(const DecRouteArgs &a, const PhiArg &phi, hipSt
     else
         hipLaunchKernelGGL((k_dec_route<TX, 4>), grid, dim3(256), 0, st, a, phi);
     return hipGetLastError();
+}
+
+// The routing within the gate/up launch: at most 64 experts, 16 tokens and 256
+// routes, and each wave has few round trips to memory to make for it.
+bool dec_self_routes(const moe_shape &s, bool router)
+{
+    if (s.E > 64 || s.T > 16 || s.T * (s.k + s.n_shared) > kDecSelfRoutes || dec_rpe(s) > 16) return false;
+#ifdef DEC_SELF
+    return DEC_SELF;
+#endif
+    return !router || (s.d <= 1024 && ((s.T + 3) / 4) * ((s.E + 3) / 4) <= 2);
+}
+
+template <int WF>
+static hipError_t launch_route_proj_t(DecArgs a, const DecRouteArgs &q, const PhiArg &phi, hipStream_t st)
+{
+    a.nchunk = (a.N + 63) / 64;
+    const unsigned grid = (unsigned)std::min<int64_t>(kDecGrid * 2, (int64_t)a.entries * a.nchunk);
+    if (a.rpe == 5)
+        hipLaunchKernelGGL((k_dec_route_proj<WF, 5>), dim3(grid), dim3(256), 0, st, a, q, phi);
+    else
+        hipLaunchKernelGGL((k_dec_route_proj<WF, 16>), dim3(grid), dim3(256), 0, st, a, q, phi);
+    return hipGetLastError();
+}
+
+hipError_t launch_dec_route_proj(const moe_shape &s, const DecArgs &a, const DecRouteArgs &q, const PhiArg &phi,
+                                 hipStream_t st)
+{
+    if (s.dtype == MOE_DT_F32) return launch_route_proj_t<W_F32>(a, q, phi, st);
+    if (w_fp8(s)) return launch_route_proj_t<W_FP8>(a, q, phi, st);
+    if (w_fp4(s)) return launch_route_proj_t<W_FP4>(a, q, phi, st);
+    return launch_route_proj_t<W_BF16>(a, q, phi, st);
 }
 
 hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const PhiArg &phi, hipStream_t st)

@@ -357,15 +357,6 @@ __device__ __forceinline__ bf16x8_t fp4_operand(uint32_t w, float scale)
     return __builtin_bit_cast(bf16x8_t, u);
 }
 
-#ifndef DEC_U
-#define DEC_U ((WF == W_BF16 || WF == W_F32) && (RPE <= 16 || (RPE == 32 && PL == 1)) ? 2 : 1)
-#endif
-#ifndef DEC_PRE
-#define DEC_PRE 48
-#endif
-#ifndef DEC_GRID
-#define DEC_GRID 512
-#endif
 constexpr uint32_t kNowhere = 0x80000000u;   // a buffer offset past every slice: such a load gives zeros and reads nothing
 
 // Workgroup barrier that waits for this wave's LDS traffic only: loads in
@@ -405,9 +396,12 @@ __device__ __forceinline__ void proj_tiles(const DecArgs &a, const int n_act, Pr
     constexpr int PL = !GATEUP && WF != W_F32 ? 3 : 1;                 // terms (columns) per route
     constexpr int RG = 16 / PL, G = (RPE + RG - 1) / RG;               // routes per operand, operands
     constexpr int MT = (RPE + 15) / 16;                                // 16-route groups of the joined sums
-    constexpr int U = DEC_U; // steps per stretch
-    constexpr int GP = G < DEC_PRE / (U * NI * 4) ? G : (DEC_PRE / (U * NI * 4) > 1 ? DEC_PRE / (U * NI * 4) : 1);
-                                                                       // operands requested ahead of the weights
+    // Steps per stretch: 4 KB of weights a wave and step in bf16, as much with two
+    // of MXFP4 or fp8; more do not gain and cost registers (16 tokens of 8 routes
+    // on 64 experts, MXFP4: 66 us with one, 72 with two).
+    constexpr int U = (WF == W_BF16 || WF == W_F32) && (RPE <= 16 || (RPE == 32 && PL == 1)) ? 2 : 1;
+    constexpr int XR = U * NI * 4;                                     // registers of one operand's stretch
+    constexpr int GP = G * XR <= 48 ? G : (48 / XR > 1 ? 48 / XR : 1); // operands requested ahead of the weights
     constexpr int ROWB = WF == W_F32 ? 0 : WF == W_BF16 ? 64 : WF == W_FP8 ? 32 : 16;   // bytes of a row in a K piece
     auto &red = sh.red;
     const int32_t *s_slot = sh.slot, *s_off = sh.off, *s_cnt = sh.cnt, *s_rec = sh.rec;
@@ -784,7 +778,7 @@ __global__ __launch_bounds__(256, 2) void k_dec_route_proj(DecArgs a, DecRouteAr
 }
 
 // Persistent workgroups: two per compute unit of the 256.
-constexpr int kDecGrid = DEC_GRID;
+constexpr int kDecGrid = 512;
 
 template <int WF, int RPE, int NT, int NW, bool GATEUP>
 hipError_t launch_proj_n(const moe_shape &s, DecArgs a, hipStream_t st)
@@ -829,9 +823,6 @@ static hipError_t launch_route_t(const DecRouteArgs &a, const PhiArg &phi, hipSt
 bool dec_self_routes(const moe_shape &s, bool router)
 {
     if (s.E > 64 || s.T > 16 || s.T * (s.k + s.n_shared) > kDecSelfRoutes || dec_rpe(s) > 16) return false;
-#ifdef DEC_SELF
-    return DEC_SELF;
-#endif
     return !router || (s.d <= 1024 && ((s.T + 3) / 4) * ((s.E + 3) / 4) <= 2);
 }
 
@@ -865,16 +856,16 @@ hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const Phi
 // that hold most slots' routes whole (7/4 of the mean of the experts hit). A
 // slot with more has several entries and its weights are read again for each;
 // a kernel for more routes has more sums, and with them fewer waves a compute
-// unit. (16 tokens of 8 routes on 64 experts, MXFP4: RPE_A us for 5, RPE_B for 16.)
+// unit. Measured, us a layer with 5 / 16 / 32 / 64: 64 experts of 2048 x 1024, top-8,
+// MXFP4, 16 tokens 65 / 70 / 95 / 109; the same in bf16, 64 tokens 210 / 182 / 198 / 218;
+// 8 experts of 4096 x 14336, top-2, bf16, 32 tokens 888 / 504 / 521 / 573, 64 tokens
+// 1389 / 701 / 584 / 661.
 int dec_rpe(const moe_shape &s)
 {
     double miss = 1.0;   // that a routed expert is hit by none of the tokens
     for (int t = 0; t < s.T; ++t) miss *= 1.0 - (double)s.k / s.E;
     const double mean = (double)s.T * s.k / (s.E * (1.0 - miss));
     const double want = std::min<double>(s.T, 1.75 * mean);
-#ifdef DEC_RPE
-    return DEC_RPE;
-#endif
     return want <= 5 ? 5 : want <= 16 ? 16 : want <= 32 ? 32 : 64;
 }
 

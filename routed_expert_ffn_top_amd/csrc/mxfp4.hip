@@ -619,9 +619,6 @@ hipError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, 
 // slot of 512 rows 13 against 19, of 2048 rows 38 against 20).
 static bool ring_pays(const MxArgs &a)
 {
-#ifdef MX_RING_ROWS
-    return a.M >= (int64_t)MX_RING_ROWS * a.P;
-#endif
     const int64_t slots = std::min(a.P, a.M), rows = a.M / slots;
     const int64_t pieces = slots * ((rows + 31) / 32) * (a.N / 64);
     return rows >= 16 && pieces >= (rows <= 128 ? 512 : 768);

@@ -415,3 +415,134 @@ def test_decode_no_tokens():
     X, A = tokens(SMALL, 0)
     layer.decode(X, A)
     torch.cuda.synchronize()
+
+
+# ---- routing: skewed, within the gate/up launch, at the limits ----
+
+def skewed(T, E, k, seed=1):
+    """Logits that send every token to experts 3, 4, .. (k of them), in an order of its own."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    L = torch.empty((T, E), device="cuda").uniform_(-1, 0, generator=gen)
+    L[:, 3:3 + k] += 5.0
+    return L
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [7, 16, 23, 64])
+def test_decode_skewed_routing(T, dtype):
+    """Far more routes on an expert than the mean: several entries of the lists
+    for one slot, the last of them short."""
+    say(f"decode, every token on the same experts, T={T} {dtype}")
+    cfg = MoEConfig(name="dec_skew", index=79, T=4, d=192, f=128, E=96, k=2, n_shared=1, dtype=dtype)
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    X, A = tokens(cfg, T)
+    Y = A.clone()
+    layer.decode(X, Y, logits=skewed(T, 96, 2))
+    r = layer.decode_routes(T)
+    check(inp, weights, X, A, Y, r, f"T={T}")
+    assert set(r["topk_idx"][:, :2].unique().tolist()) == {3, 4} and r["topk_idx"][:, 2].eq(96).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cfg", [SMALL, SHARED, F32ODD.with_(d=128)], ids=lambda c: c.name)
+def test_decode_given_logits(cfg, dtype):
+    """Few tokens, experts and given logits: routed within the gate/up launch."""
+    say(f"decode with given logits, {cfg.name} {dtype}")
+    cfg = cfg.with_(dtype=dtype, f=128)
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    for T in (1, 3, 8, 16):
+        X, A = tokens(cfg, T)
+        L = make_logits(T, cfg.E, T, device="cuda")
+        if T > 1:
+            L[1, 2] = float("nan")
+            L[0, 1] = L[0, 0] = 2.0      # a tie
+        Y = A.clone()
+        layer.decode(X, Y, logits=L)
+        r = layer.decode_routes(T)
+        check(inp, weights, X, A, Y, r, f"T={T}")
+        prompt = MoELayer(type(inp)(**{**inp.__dict__, "cfg": cfg.with_(T=T), "X": X, "A": A}))
+        prompt.forward(A.clone(), logits=L)
+        torch.cuda.synchronize()
+        assert torch.equal(r["topk_idx"], prompt.routes["topk_idx"]) and torch.equal(r["topk_w"], prompt.routes["topk_w"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cfg", [SMALL, ONE, WIDE, F32ODD.with_(d=128), MoEConfig(name="dec_d1088", index=80, T=4, d=1088, f=64, E=8, k=2)],
+                         ids=lambda c: c.name)
+def test_decode_routes_few_tokens_as_the_prompt_layer(cfg, dtype):
+    say(f"decode routes few tokens as the prompt layer does, {cfg.name} {dtype}")
+    for T in (1, 2, 4, 5, 9):
+        c = cfg.with_(T=T, dtype=dtype, f=64)
+        inp = gpu_inputs(c)
+        layer = MoELayer(inp)
+        layer.forward(inp.A.clone())
+        layer.decode(inp.X, inp.A.clone())
+        torch.cuda.synchronize()
+        r = layer.decode_routes(T)
+        assert torch.equal(r["topk_idx"], layer.routes["topk_idx"]) and torch.equal(r["topk_w"], layer.routes["topk_w"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "bf16_fp4w"])
+def test_decode_largest_expert_table_and_route_count(dtype):
+    say(f"decode: 256 + 2 experts in 512 slots; 1024 routes, {dtype}")
+    from routed_expert_ffn_top_amd.inputs import random_phi
+    cfg = MoEConfig(name="dec_e256", index=81, T=4, d=128, f=64, E=256, k=6, n_shared=2, dtype=dtype, renorm=False)
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp, phi=random_phi(258, 512, 4).tolist(), P=512), plain_weights(inp)
+    for T in (1, 64):
+        X, A = tokens(cfg, T)
+        Y = A.clone()
+        layer.decode(X, Y)
+        check(inp, weights, X, A, Y, layer.decode_routes(T), f"T={T}")
+    layer.close()
+    cfg = MoEConfig(name="dec_r1024", index=82, T=4, d=64, f=64, E=40, k=40, n_shared=24, dtype=dtype)
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    for T in (1, 16):
+        X, A = tokens(cfg, T)
+        Y = A.clone()
+        layer.decode(X, Y)
+        check(inp, weights, X, A, Y, layer.decode_routes(T), f"T={T}, 64 routes a token")
+
+
+def test_decode_arena_past_4_gib():
+    say("decode: a gate/up plane of 5.4 GB, slots past 2^32 bytes")
+    cfg = MoEConfig(name="dec_big", index=83, T=4, d=4096, f=4096, E=80, k=4)
+    inp = gpu_inputs(cfg)
+    layer = MoELayer(inp)
+    X, A = tokens(cfg, 3)
+    L = torch.full((3, 80), -1.0, device="cuda")
+    L[:, 76:] = torch.arange(4, device="cuda") * 0.3
+    Y = A.clone()
+    layer.decode(X, Y, logits=L)
+    torch.cuda.synchronize()
+    weights = [torch.zeros(80, 1, 1)] * 3
+    small = [w[76:].double() for w in (inp.Wg, inp.Wu, inp.Wd)]
+    sub = type(inp)(**{**inp.__dict__, "cfg": cfg.with_(E=4)})
+    r = layer.decode_routes(3)
+    assert int(r["topk_idx"].min()) >= 76
+    ref, bound = reference(sub, small, X, A, r["topk_idx"].long() - 76, r["topk_w"])
+    assert bool(((Y.double() - ref).abs() <= bound).all())
+
+
+def test_decode_workspace_serves_several_shapes_and_layers():
+    say("decode: one workspace for two layers and three token counts, call after call")
+    cfgs = [SMALL, WIDE]
+    layers = [MoELayer(gpu_inputs(c)) for c in cfgs]
+    shapes = [(l, c, T, B.make_shape(T, c.d, c.f, c.E, c.k, dtype=c.dtype)) for l, c in zip(layers, cfgs) for T in (64, 1, 9)]
+    ws = max((B.alloc_decode_workspace(s) for *_, s in shapes), key=lambda w: w.numel())
+    for rep in range(3):
+        got = []
+        for l, c, T, s in shapes:
+            X, A = tokens(c, T, seed=90 + rep)
+            Y = A.clone()
+            B.moe_layer_decode(s, X, l.Wr, None, None, Y, l.arena, B.alloc_routes(s), ws)
+            got.append((l, X, A, Y))
+        torch.cuda.synchronize()
+        for l, X, A, Y in got:
+            Z = A.clone()
+            l.decode(X, Z)
+            torch.cuda.synchronize()
+            assert torch.equal(Y, Z)

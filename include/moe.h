@@ -113,6 +113,16 @@ typedef void *moe_stream; /* a hipStream_t */
                            d % 128 == 0 and an unsplit down projection (see
                            moe_expert_ffn), MOE_ERR_UNSUPPORTED otherwise. */
 
+#define MOE_FFN_ACT_MXFP4 16 /* MXFP4 weights: the activations are MXFP4 too. X
+                                is the source slice of the T tokens (codes
+                                [T][d/2], then scale bytes [T][d/32], as
+                                moe_quantize_mxfp4 writes them; ldx is not
+                                used), H is quantised the same way, from its
+                                fp32 values, and both projections multiply
+                                codes by codes on the scaled matrix
+                                instructions. MOE_ERR_UNSUPPORTED for other
+                                weights and with the two flags above. */
+
 /* Residency states (section 3.3, "Bounded Parameter Arena and Safe Slot Reuse") */
 #define MOE_SLOT_AVAILABLE 0
 #define MOE_SLOT_FILLING 1
@@ -273,7 +283,7 @@ moe_status moe_route_build(const moe_shape *shape, int32_t t0, int32_t nt,
  *          (MOE_ERR_SLOT_STATE otherwise); the stream waits for each such
  *          slot's load, and each slot's release is recorded after the work.
  *   flags  MOE_FFN_EXPERTS and/or MOE_FFN_FINALIZE (and optionally
- *          MOE_FFN_SIMPLE_KERNEL or MOE_FFN_FUSED).
+ *          MOE_FFN_SIMPLE_KERNEL, MOE_FFN_FUSED or MOE_FFN_ACT_MXFP4).
  * MOE_FFN_EXPERTS: for each record p of slot s, H[p] = SiLU(g) * u with
  * (g, u) = X[rec_token[p]] times slot s's gate/up slice, then
  * Yr[rec_route[p]] = alpha * (H[p] times slot s's down slice); the route is

@@ -44,6 +44,7 @@ MOE_FFN_EXPERTS = 1
 MOE_FFN_FINALIZE = 2
 MOE_FFN_SIMPLE_KERNEL = 4
 MOE_FFN_FUSED = 8
+MOE_FFN_ACT_MXFP4 = 16
 MOE_SLOT_AVAILABLE, MOE_SLOT_FILLING, MOE_SLOT_READY, MOE_SLOT_IN_USE = 0, 1, 2, 3
 MOE_MAX_EXPERTS = 512
 MOE_DECODE_MAX_T = 64

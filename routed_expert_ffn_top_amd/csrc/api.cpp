@@ -338,6 +338,47 @@ GemmArgs gemm_args(const moe_shape &s, const moe_routes &r, const moe_arena *a)
     return g;
 }
 
+// The projections on MXFP4 activations: X and H as codes and scale bytes.
+moe_status experts_mxfp4_impl(const moe_shape &s, const WsLayout &w, const void *X, const moe_routes &r, moe_arena *a,
+                              int max_rows, void *ws, hipStream_t st)
+{
+    // H: codes [C][f/2], then scale bytes [C][f/32], in the bf16 H's place
+    uint8_t *H = ws_at<uint8_t>(ws, w.H), *Hs = H + (size_t)s.capacity * s.f / 2;
+    MxArgs g{};
+    g.A = (const uint8_t *)X;
+    g.As = g.A + (size_t)s.T * s.d / 2;
+    g.A_rows = s.T;
+    g.row_index = r.rec_token;
+    g.slot_offset = r.slot_offset;
+    g.P = s.P;
+    g.B = (const uint8_t *)a->plane_gu;
+    g.B_stride = a->stride_gu;
+    g.M = max_rows;
+    g.N = 2 * s.f;
+    g.K = s.d;
+    g.C = H;
+    g.Hs = Hs;
+    HIP_TRY(TIMED(MOE_KERNEL_GATE_UP, st, launch_gate_up_mxfp4(g, st)), "gate/up launch");
+    MxArgs h = g;
+    h.A = H;
+    h.As = Hs;
+    h.A_rows = s.capacity;
+    h.row_index = nullptr;
+    h.B = (const uint8_t *)a->plane_d;
+    h.B_stride = a->stride_d;
+    h.N = s.d;
+    h.K = s.f;
+    h.C = ws_at<float>(ws, w.Yr);
+    h.ldc = s.d;
+    h.rec_route = r.rec_route;
+    h.topk_w = r.topk_w;
+    h.done = ws_at<int32_t>(ws, w.done);
+    h.splits = down_splits(s);
+    h.split_stride = (int64_t)s.T * (s.k + s.n_shared) * s.d;
+    HIP_TRY(TIMED(MOE_KERNEL_DOWN, st, launch_down_mxfp4(h, st)), "down launch");
+    return MOE_OK;
+}
+
 moe_status experts_impl(const moe_shape &s, const WsLayout &w, const void *X, const moe_routes &r,
                         moe_arena *a, int max_rows, bool simple, void *ws, hipStream_t st, bool fused = false)
 {
@@ -477,13 +518,18 @@ moe_status moe_expert_ffn(const moe_shape *shape, const void *X, float *Y, const
             return fail(MOE_ERR_INVALID_ARG, "arena was made for another shape");
         if (act_bf16(*shape) && !aligned(X, 16))
             return fail(MOE_ERR_INVALID_ARG, "X must be 16-byte aligned");
+        if ((flags & MOE_FFN_ACT_MXFP4) && (!w_fp4(*shape) || (flags & (MOE_FFN_SIMPLE_KERNEL | MOE_FFN_FUSED))))
+            return fail(MOE_ERR_UNSUPPORTED, "MXFP4 activations need MXFP4 weights and neither the plain nor the fused kernel");
         PhiArg pa;
         MOE_TRY(check_phi(shape, phi, &pa));
         std::lock_guard<std::mutex> lk(arena->mu);
         MOE_TRY(arena_acquire(arena, phi, S(stream)));
         const int max_rows = std::min<int64_t>(shape->capacity, (int64_t)shape->T * (shape->k + shape->n_shared));
-        MOE_TRY(experts_impl(*shape, w, X, *routes, arena, max_rows, (flags & MOE_FFN_SIMPLE_KERNEL) != 0, ws,
-                             S(stream), (flags & MOE_FFN_FUSED) != 0));
+        if (flags & MOE_FFN_ACT_MXFP4)
+            MOE_TRY(experts_mxfp4_impl(*shape, w, X, *routes, arena, max_rows, ws, S(stream)));
+        else
+            MOE_TRY(experts_impl(*shape, w, X, *routes, arena, max_rows, (flags & MOE_FFN_SIMPLE_KERNEL) != 0, ws,
+                                 S(stream), (flags & MOE_FFN_FUSED) != 0));
         MOE_TRY(arena_release_after(arena, phi, S(stream)));
     }
     if (flags & MOE_FFN_FINALIZE) {

@@ -24,7 +24,19 @@ struct MxArgs {
     void *C;
     int c_bf16;
     int64_t ldc;
+    // the expert FFN's projections only
+    uint8_t *Hs;                 // gate/up: scale bytes [M][N/64] of H, whose codes [M][N/4] are C
+    const int32_t *rec_route;    // down: route of a record; C is Yr, fp32 [splits][routes][ldc]
+    const float *topk_w;
+    int32_t *done;
+    int splits;                  // partial rows a route has: the first holds the result, the others zeros
+    int64_t split_stride;
 };
 hipError_t launch_matmul_mxfp4(const MxArgs &a, hipStream_t st);
+// The expert FFN's projections on MXFP4 activations, over a route build:
+// gate/up with SwiGLU and the quantisation of H, and down with the route
+// weights, a row of C per route.
+hipError_t launch_gate_up_mxfp4(const MxArgs &a, hipStream_t st);
+hipError_t launch_down_mxfp4(const MxArgs &a, hipStream_t st);
 
 }  // namespace moe

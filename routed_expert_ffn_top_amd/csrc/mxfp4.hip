@@ -8,6 +8,7 @@
 // infinity or a NaN gets the byte 255 (NaN) and codes 0. A zero has no sign.
 #include <algorithm>
 #include <type_traits>
+#include <utility>
 
 #include "mxfp4.h"
 
@@ -18,6 +19,25 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// Scale byte of a block from the bits of its largest magnitude, and the factor
+// 2^(127 - byte) that its values are quantised with (1 for a NaN block).
+__device__ __forceinline__ uint32_t block_scale(uint32_t top)
+{
+    const int e = (int)(top >> 23);
+    return e == 255 ? 255u : (uint32_t)max(e - 2, 0);
+}
+__device__ __forceinline__ float block_unit(uint32_t byte)
+{
+    // byte <= 252, so the exponent field is at least 2
+    return byte == 255 ? 1.0f : __uint_as_float((254u - byte) << 23);
+}
+// Eight codes without the signs of those of magnitude 0.
+__device__ __forceinline__ uint32_t unsigned_zeros(uint32_t q)
+{
+    const uint32_t m = q & 0x77777777u, nz = (m | m >> 1 | m >> 2) & 0x11111111u;
+    return m | (q & nz << 3);
+}
 
 // Element offset of group i of 8 values (i < 2^31), rows of K8 groups ld elements apart.
 __device__ __forceinline__ int64_t place(int64_t i, int K8, int64_t ld)
@@ -59,10 +79,8 @@ __global__ __launch_bounds__(256) void k_quantize(const void *__restrict__ src, 
     for (int c = 0; c < 8; ++c) top = max(top, v[c] & 0x7fffffffu);
     top = max(top, (uint32_t)__shfl_xor((int)top, 1, 64));
     top = max(top, (uint32_t)__shfl_xor((int)top, 2, 64));
-    const int e = (int)(top >> 23);
-    const int byte = e == 255 ? 255 : max(e - 2, 0);
-    // 2^(127 - byte): byte <= 252, so the exponent field is at least 2
-    const float up = __uint_as_float((uint32_t)(254 - min(byte, 252)) << 23);
+    const uint32_t byte = block_scale(top);
+    const float up = block_unit(byte);
     uint32_t q = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -74,10 +92,7 @@ __global__ __launch_bounds__(256) void k_quantize(const void *__restrict__ src, 
         default: q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, a, b, 1.0f, 3); break;
         }
     }
-    // drop the sign of codes of magnitude 0
-    const uint32_t m = q & 0x77777777u, nz = (m | m >> 1 | m >> 2) & 0x11111111u;
-    q = m | (q & nz << 3);
-    codes[i] = byte == 255 ? 0u : q;
+    codes[i] = byte == 255 ? 0u : unsigned_zeros(q);
     if ((threadIdx.x & 3) == 0) scales[i >> 2] = (uint8_t)byte;
 }
 
@@ -283,7 +298,81 @@ constexpr int kStream = 2;   // buffer stores of C, which is not read here: non-
 // scales) one word is copied. The tiles of an XCD (workgroup id mod 8) are one
 // contiguous range, column block major, walked in step, so that tiles which
 // share weights or rows share that XCD's L2.
-template <int BM, int NS, bool SHIFT>
+//
+// EPI: what becomes of a tile. STORE: C, rounded to its type. GATE_UP: the
+// slice's rows alternate 32 gate, 32 up, so a wave's two column blocks are gate
+// and up of the same 32 units, one unit a lane: H = SiLU(g) u is one MXFP4 block
+// for each row of a wave, quantised in registers (block maximum over the 32
+// lanes, codes of 8 rows gathered in a word and transposed over 8 lanes) and
+// written as codes and scale bytes; the fp32 and bf16 H never exist. DOWN: C is
+// the routes' fp32 rows, alpha times the record's, and the routes are marked.
+//
+// The epilogue of gate/up is as long as its products unless its instructions are
+// few: the 16 rows' block maxima by halving (24 + 12 + 6 + 3 operations and one
+// exchange, not 16 times 10), one scale a lane, brought to the row's 16 lanes as
+// an operand of the multiplication (32768 x 2048 x 2048
+// over 64 slots 195 -> 151 us; the bf16-activation kernel takes 290).
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    // hardware exp2 and reciprocal: off by (|g| + 4) 2^-23 at most, before 4 bits are kept
+    const float e = __builtin_amdgcn_exp2f(-g * 1.4426950408889634f);
+    return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+// One halving: of 2n values the lane keeps n, those of its side, each joined with
+// the partner's (which CTRL names and which is on the other side).
+template <int CTRL, int n>
+__device__ __forceinline__ void halve(uint32_t *t, bool upper)
+{
+#pragma unroll
+    for (int r = 0; r < n; ++r) {
+        const uint32_t keep = upper ? t[r + n] : t[r], give = upper ? t[r] : t[r + n];
+        t[r] = max(keep, dpp<CTRL>(give));
+    }
+}
+// Bits of the largest magnitude (infinities and NaN above all) over the 32 lanes
+// of a half of h[lane % 16].
+__device__ __forceinline__ uint32_t block_tops(const float *h, int lane)
+{
+    uint32_t t[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) t[r] = __float_as_uint(h[r]) & 0x7fffffffu;
+    halve<0x128, 8>(t, lane & 8);   // lane ^ 8: a rotation by 8 of 16
+    halve<0x141, 4>(t, lane & 4);   // 7 - lane of 8
+    halve<0x4E, 2>(t, lane & 2);    // lane ^ 2
+    halve<0xB1, 1>(t, lane & 1);    // lane ^ 1
+    return max(t[0], (uint32_t)__builtin_amdgcn_ds_swizzle((int)t[0], (16 << 10) | 0x1f));   // lane ^ 16
+}
+// h[r] times the unit that lane r of each 16 holds.
+template <int... R>
+__device__ __forceinline__ void scale_rows(float *h, float unit, std::integer_sequence<int, R...>)
+{
+    ((h[R] *= __uint_as_float(dpp<0x150 + R>(__float_as_uint(unit)))), ...);
+}
+// h[r] with the bits that lane r of each 16 keeps.
+template <int... R>
+__device__ __forceinline__ void zero_rows(float *h, int keep, std::integer_sequence<int, R...>)
+{
+    ((h[R] = __uint_as_float(__float_as_uint(h[R]) & dpp<0x150 + R>((uint32_t)keep))), ...);
+}
+// 8 x 8 nibbles over 8 lanes: lane l's nibble j becomes lane j's nibble l.
+__device__ __forceinline__ uint32_t transpose8(uint32_t q, int lane)
+{
+    uint32_t o = (uint32_t)__builtin_amdgcn_ds_swizzle((int)q, (4 << 10) | 0x1f);
+    q = (lane & 4) ? (o >> 16) | (q & 0xffff0000u) : (q & 0xffffu) | (o << 16);
+    o = dpp<0x4E>(q);
+    q = (lane & 2) ? ((o >> 8) & 0x00ff00ffu) | (q & 0xff00ff00u) : (q & 0x00ff00ffu) | ((o & 0x00ff00ffu) << 8);
+    o = dpp<0xB1>(q);
+    return (lane & 1) ? ((o >> 4) & 0x0f0f0f0fu) | (q & 0xf0f0f0f0u) : (q & 0x0f0f0f0fu) | ((o & 0x0f0f0f0fu) << 4);
+}
+
+enum { EPI_STORE = 0, EPI_GATE_UP = 1, EPI_DOWN = 2 };
+
+template <int BM, int NS, bool SHIFT, int EPI>
 __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
 {
     constexpr int BN = 256, WM = 2, WN = 4, TM = BM / WM, TN = BN / WN, MI = TM / 32, NI = TN / 32;
@@ -295,6 +384,8 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
     __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE];
     __shared__ int32_t s_tpref[kMaxExp + 1], s_lo[kMaxExp], s_cnt[kMaxExp];
     __shared__ int32_t s_shift[SHIFT ? BM : 1];   // bytes from the aligned word to a row's scales
+    __shared__ int32_t s_route[2][EPI == EPI_DOWN ? BM : 1];   // by tile parity
+    __shared__ float s_alpha[2][EPI == EPI_DOWN ? BM : 1];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -475,8 +566,28 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
         }
     };
 
-    int tl = li;
+    // down: route and weight of row tid, asked for during a tile and put into
+    // LDS for the next one
+    int pre_route = 0;
+    float pre_alpha = 0.0f;
+    auto fetch_route = [&](const Tile &t) {
+        if (EPI == EPI_DOWN && tid < BM) pre_route = a.rec_route[t.row0 + min(tid, t.rows - 1)];
+    };
+    auto fetch_alpha = [&]() {
+        if (EPI == EPI_DOWN && tid < BM) pre_alpha = a.topk_w[pre_route];
+    };
+    auto store_route = [&](int par) {
+        if (EPI == EPI_DOWN && tid < BM) {
+            s_route[par][tid] = pre_route;
+            s_alpha[par][tid] = pre_alpha;
+        }
+    };
+
+    int tl = li, par = 0;
     Tile cur = decode(start_x + tl);
+    fetch_route(cur);
+    fetch_alpha();
+    store_route(0);
     int rows[AI + 1];
     fetch_rows(cur, rows);
     set_sources(cur, rows);
@@ -510,7 +621,11 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
                 wait_vmcnt_stages<LOADS, NS - 3>(min(NS - 3, nk - 2 - kt));
                 __builtin_amdgcn_s_barrier();
             }
-            if (has_next && kt == 0) fetch_rows(nxt, rows);
+            if (has_next && kt == 0) {
+                fetch_rows(nxt, rows);
+                fetch_route(nxt);
+            }
+            if (has_next && kt == 1) fetch_alpha();
             if (more && kt + NS - 1 < nk) issue(kt + NS - 1);
             if (wave_active) {
                 read_frags(stage, 1, 1);
@@ -524,8 +639,10 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
         }
         const Tile done = cur;
         if (has_next) {
+            if (nk < 2) fetch_alpha();
             __syncthreads();   // nothing reads the ring any more
             set_sources(nxt, rows);
+            store_route(par ^ 1);   // last read a tile ago
 #pragma unroll
             for (int p = 0; p < NS - 1; ++p)
                 if (p < nk) issue(p);
@@ -536,7 +653,60 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
         // buffer: stores to rows past its last one are dropped by its bounds
         // check, so no store has a branch. A wave's 64 columns are all in N or
         // all past it.
-        if (wave_active && done.n0 + wn * TN < N) {
+        if constexpr (EPI == EPI_GATE_UP) {
+            if (wave_active && done.n0 + wn * TN < N) {
+                // opaque, as ld below: the rows' offsets are not held through the tile loop
+                int f = N / 2;
+                asm volatile("" : "+s"(f));
+                const int blk = (done.n0 + wn * TN) / 64;   // block of 32 units
+                uint8_t *hc = (uint8_t *)a.C + (int64_t)done.row0 * (f / 2) + blk * 16;
+                uint8_t *hs = a.Hs + (int64_t)done.row0 * (f / 32) + blk;
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    float h[16];
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) h[r] = silu_mul(acc[i][0][r], acc[i][1][r]);
+                    const uint32_t byte = block_scale(block_tops(h, lane));   // of register lane % 16's row
+                    const float unit = block_unit(byte);
+                    scale_rows(h, unit, std::make_integer_sequence<int, 16>());
+                    if (__any(byte == 255)) zero_rows(h, byte == 255 ? 0 : -1, std::make_integer_sequence<int, 16>());
+#pragma unroll
+                    for (int r8 = 0; r8 < 16; r8 += 8) {
+                        uint32_t q = 0;   // nibble r: this lane's unit in row r8 + r
+                        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, h[r8 + 0], h[r8 + 1], 1.0f, 0);
+                        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, h[r8 + 2], h[r8 + 3], 1.0f, 1);
+                        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, h[r8 + 4], h[r8 + 5], 1.0f, 2);
+                        q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, h[r8 + 6], h[r8 + 7], 1.0f, 3);
+                        q = transpose8(unsigned_zeros(q), lane);   // row r8 + lane % 8, units 8 (lane / 8) .. +7
+                        const int rr = r8 + (lane & 7);
+                        const int m = wm * TM + i * 32 + 8 * (rr / 4) + 4 * half + (rr & 3);
+                        if (m < done.rows) *(uint32_t *)(hc + (int64_t)m * (f / 2) + ((lane & 31) >> 3) * 4) = q;
+                    }
+                    const int rr = lane & 15, m = wm * TM + i * 32 + 8 * (rr / 4) + 4 * half + (rr & 3);
+                    if ((lane & 16) == 0 && m < done.rows) hs[(int64_t)m * (f / 32)] = (uint8_t)byte;
+                }
+            }
+        } else if constexpr (EPI == EPI_DOWN) {
+            if (wave_active && done.n0 + wn * TN < N) {
+                float *C = (float *)a.C + done.n0 + wn * TN + (lane & 31);
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int m = wm * TM + i * 32 + 8 * (r / 4) + 4 * half + (r & 3);
+                        if (m >= done.rows) continue;
+                        const float al = s_alpha[par][m];
+                        float *y = C + (int64_t)s_route[par][m] * a.ldc;
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) y[j * 32] = al * acc[i][j][r];
+                        for (int q = 1; q < a.splits; ++q)
+#pragma unroll
+                            for (int j = 0; j < NI; ++j) y[q * a.split_stride + j * 32] = 0.0f;
+                    }
+            }
+            if (done.n0 == 0)
+                for (int m = tid; m < done.rows; m += 512) a.done[s_route[par][m]] = 1;
+        } else if (wave_active && done.n0 + wn * TN < N) {
             const int esz = a.c_bf16 ? 2 : 4;
             char *base = (char *)a.C + ((int64_t)done.row0 * a.ldc + done.n0 + wn * TN) * esz;
             // opaque, or the rows' offsets are computed before the tile loop and
@@ -578,6 +748,7 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
         if (!has_next) break;
         cur = nxt;
         tl = tn;
+        par ^= 1;
     }
 }
 
@@ -624,18 +795,32 @@ static bool ring_pays(const MxArgs &a)
     return rows >= 16 && pieces >= (rows <= 128 ? 512 : 768);
 }
 
+template <int EPI>
+static hipError_t launch_ring(const MxArgs &a, hipStream_t st)
+{
+    const int64_t tiles = ((int64_t)(a.M + 255) / 256 + std::min(a.P, a.M) - 1) * ((a.N + 255) / 256);
+    const unsigned grid = (unsigned)std::min<int64_t>(tiles, 256);   // one workgroup per compute unit
+    if (a.K % 128 == 0 && ((uintptr_t)a.As & 3) == 0)
+        hipLaunchKernelGGL((k_matmul_ring<256, 4, false, EPI>), dim3(grid), dim3(512), 0, st, a);
+    else
+        hipLaunchKernelGGL((k_matmul_ring<256, 4, true, EPI>), dim3(grid), dim3(512), 0, st, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_gate_up_mxfp4(const MxArgs &a, hipStream_t st)
+{
+    return a.M == 0 ? hipSuccess : launch_ring<EPI_GATE_UP>(a, st);
+}
+
+hipError_t launch_down_mxfp4(const MxArgs &a, hipStream_t st)
+{
+    return a.M == 0 ? hipSuccess : launch_ring<EPI_DOWN>(a, st);
+}
+
 hipError_t launch_matmul_mxfp4(const MxArgs &a, hipStream_t st)
 {
     if (a.M == 0) return hipSuccess;
-    if (ring_pays(a)) {
-        const int64_t tiles = ((int64_t)(a.M + 255) / 256 + std::min(a.P, a.M) - 1) * ((a.N + 255) / 256);
-        const unsigned grid = (unsigned)std::min<int64_t>(tiles, 256);   // one workgroup per compute unit
-        if (a.K % 128 == 0 && ((uintptr_t)a.As & 3) == 0)
-            hipLaunchKernelGGL((k_matmul_ring<256, 4, false>), dim3(grid), dim3(512), 0, st, a);
-        else
-            hipLaunchKernelGGL((k_matmul_ring<256, 4, true>), dim3(grid), dim3(512), 0, st, a);
-        return hipGetLastError();
-    }
+    if (ring_pays(a)) return launch_ring<EPI_STORE>(a, st);
     // at most this many row tiles: one partial tile per slot with records
     const int64_t mt = (int64_t)(a.M + 63) / 64 + std::min(a.P, a.M) - 1;
     hipLaunchKernelGGL(k_matmul_small, dim3((unsigned)(mt * (a.N / 64))), dim3(256), 0, st, a);

@@ -44,6 +44,7 @@ class MoELayer:
         self.bias = None if inp.bias is None else inp.bias.to(self.device).contiguous()
         self.routes = B.alloc_routes(self.shape, self.device)
         self.ws = B.alloc_workspace(self.shape, self.device)
+        self._xq = None     # MXFP4 blocks of X (forward_mxfp4)
         self._decode = {}   # by token count: shape, routes, workspace
         self.paged = paged
         self.arena = B.Arena(self.shape, G=(cfg.G if paged else None), device=self.device)
@@ -85,6 +86,26 @@ class MoELayer:
         bias = None if logits is not None else self.bias
         B.moe_layer_prefill(self.shape, self.X, Wr, bias, logits, Y, self.arena,
                             self.host_gu, self.host_d, self.routes, self.ws, compute, copy)
+        return Y
+
+    def forward_mxfp4(self, Y: torch.Tensor, logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The resident layer with MXFP4 weights on MXFP4 activations: X is
+        routed as it is, then quantised, and H is quantised between the
+        projections. Y holds the residual on entry and the layer output on
+        return."""
+        s, cfg = self.shape, self.cfg
+        if not cfg.fp4_weights or self.paged or s.capacity < cfg.T * cfg.kp:
+            raise ValueError("needs a resident layer with MXFP4 weights and capacity for every route")
+        if logits is None:
+            logits = torch.empty((cfg.T, cfg.E), dtype=torch.float32, device=self.device)
+            B.moe_router_logits(s, self.X, self.Wr, self.bias, logits, stream)
+        n = cfg.T * cfg.d
+        if self._xq is None:
+            self._xq = torch.empty(n // 2 + n // 32, dtype=torch.uint8, device=self.device)
+        B.moe_quantize_mxfp4(self.X, self._xq[: n // 2], self._xq[n // 2:], stream)
+        B.moe_route_build(s, 0, cfg.T, logits, self.phi, B.MOE_ROUTE_RESET, self.routes, self.ws, stream)
+        B.moe_expert_ffn(s, self._xq, Y, self.routes, self.arena, self.phi,
+                         B.MOE_FFN_EXPERTS | B.MOE_FFN_FINALIZE | B.MOE_FFN_ACT_MXFP4, self.ws, stream)
         return Y
 
     def decode(self, X: torch.Tensor, Y: torch.Tensor, logits: Optional[torch.Tensor] = None,

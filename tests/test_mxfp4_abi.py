@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from routed_expert_ffn_top_amd import binding as B
+from test_abi import _FakeWs, _fake_routes
 
 INV, UN = B.MOE_ERR_INVALID_ARG, B.MOE_ERR_UNSUPPORTED
 L = B.load()
@@ -66,3 +67,17 @@ def test_binding_refuses_other_layouts():
                dict(row_index=torch.zeros(3, dtype=torch.int32)), dict(slot_offset=torch.zeros(1, dtype=torch.int32))):
         with pytest.raises(ValueError):
             B.moe_matmul_mxfp4(**dict(ok, **kw))
+
+
+@pytest.mark.parametrize("dtype,flags", [("bf16", 0), ("f32", 0), ("bf16_fp8w", 0), ("bf16_fp4w", B.MOE_FFN_SIMPLE_KERNEL),
+                                         ("bf16_fp4w", B.MOE_FFN_FUSED)])
+def test_mxfp4_activations_refused(dtype, flags):
+    """Before the arena's state is looked at (nothing is loaded here)."""
+    s = B.make_shape(4, 128, 64, 8, 2, dtype=dtype)
+    h = B.moe_arena_create(s, 0x100000, 0x200000, 2 * s.f * s.d, s.f * s.d, s.P)
+    arena = type("Arena", (), {"handle": h})()
+    with pytest.raises(B.MoEError) as e:
+        B.moe_expert_ffn(s, 0x1000, 0x3000, _fake_routes(s), arena, list(range(8)),
+                         B.MOE_FFN_EXPERTS | B.MOE_FFN_ACT_MXFP4 | flags, _FakeWs(B.moe_workspace_bytes(s)), 0)
+    assert e.value.status == UN
+    B.moe_arena_destroy(h)

@@ -74,7 +74,7 @@ def test_binding_refuses_other_layouts():
 def test_mxfp4_activations_refused(dtype, flags):
     """Before the arena's state is looked at (nothing is loaded here)."""
     s = B.make_shape(4, 128, 64, 8, 2, dtype=dtype)
-    h = B.moe_arena_create(s, 0x100000, 0x200000, 2 * s.f * s.d, s.f * s.d, s.P)
+    h = B.moe_arena_create(s, 0x100000, 0x200000, 4 * s.f * s.d, 2 * s.f * s.d, s.P)
     arena = type("Arena", (), {"handle": h})()
     with pytest.raises(B.MoEError) as e:
         B.moe_expert_ffn(s, 0x1000, 0x3000, _fake_routes(s), arena, list(range(8)),

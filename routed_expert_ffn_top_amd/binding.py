@@ -165,6 +165,20 @@ def _stream(s) -> Optional[int]:
     return s.cuda_stream
 
 
+def _stream_of(t, s) -> Optional[int]:
+    """_stream(s) for work on t, whose GPU has to be the current one: a launch
+    goes to the current device, wherever its pointers lead."""
+    if t is not None and not isinstance(t, int):
+        if t.get_device() < 0:
+            raise ValueError("the tensors must be on the GPU")
+        here = torch.cuda.current_device()
+        if t.get_device() != here or getattr(s, "device_index", here) != here:
+            raise ValueError(f"the tensors and the stream must be on the current device, cuda:{here}")
+        if s is None:
+            return _raw_stream(here)
+    return _stream(s)
+
+
 def make_shape(T, d, f, E, k, n_shared=0, P=None, capacity=None, dtype="bf16", renorm=True,
                ldx=None, ldy=None) -> moe_shape:
     kp = k + n_shared
@@ -269,65 +283,78 @@ def moe_layer_decode(shape, X, W_r, bias, logits, Y, arena, routes: dict, ws, st
     rs = routes_struct(routes)
     _check(load().moe_layer_decode(ctypes.byref(shape), _ptr(X), _ptr(W_r), _ptr(bias), _ptr(logits), _ptr(Y),
                                    arena.handle, ctypes.byref(rs), _ptr(ws), ws.numel() * ws.element_size(),
-                                   _stream(stream)))
+                                   _stream_of(X, stream)))
 
 
 _VAL_DTYPE = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
 
 
 def _mx_views(values, codes, scales):
-    """rows, K and row stride of [..., K] values and their blocks; leading
-    dimensions that one row stride covers count as rows."""
-    if values.dtype not in _VAL_DTYPE:
+    """Type code, rows, K and row stride of [..., K] values and their blocks;
+    leading dimensions that one row stride covers count as rows."""
+    # one row's calls are as long as what the host does: each attribute is asked for once
+    dtype = _VAL_DTYPE.get(values.dtype)
+    if dtype is None:
         raise ValueError("values must be float32 or bfloat16")
-    K = values.shape[-1]
-    rows = values.numel() // K if K else 0
-    for t, cols, name in ((codes, K // 2, "codes"), (scales, K // 32, "scales")):
-        if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != rows * cols or K % 32:
-            raise ValueError(f"{name}: need contiguous uint8 [rows][{cols}], K a multiple of 32")
-    if values.dim() == 2:
-        if values.stride(1) != 1:
-            raise ValueError("values: rows must be contiguous")
-        ld = row_stride(values)
-    elif values.is_contiguous():
+    shape, n, dev = values.shape, values.numel(), values.get_device()
+    K = shape[-1]
+    if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or K % 32 or codes.numel() * 2 != n
+            or scales.numel() * 32 != n or not codes.is_contiguous() or not scales.is_contiguous()):
+        raise ValueError("need contiguous uint8 codes [rows][K/2] and scales [rows][K/32], K a multiple of 32")
+    if codes.get_device() != dev or scales.get_device() != dev:
+        raise ValueError("values, codes and scales must be on one device")
+    if values.is_contiguous():
         ld = K
-    else:
+    elif len(shape) != 2:
         raise ValueError("values: only a matrix may have a row stride")
-    return rows, K, ld
+    else:
+        ld, step = values.stride()
+        if step != 1:
+            raise ValueError("values: rows must be contiguous")
+    return dtype, n // K if K else 0, K, ld
 
 
 def moe_quantize_mxfp4(values, codes, scales, stream=None):
-    rows, K, ld = _mx_views(values, codes, scales)
-    _check(load().moe_quantize_mxfp4(_ptr(values), _VAL_DTYPE[values.dtype], rows, K, ld, _ptr(codes), _ptr(scales),
-                                     _stream(stream)))
+    dtype, rows, K, ld = _mx_views(values, codes, scales)
+    _check(load().moe_quantize_mxfp4(values.data_ptr(), dtype, rows, K, ld, codes.data_ptr(), scales.data_ptr(),
+                                     _stream_of(values, stream)))
 
 
 def moe_dequantize_mxfp4(codes, scales, values, stream=None):
-    rows, K, ld = _mx_views(values, codes, scales)
-    _check(load().moe_dequantize_mxfp4(_ptr(codes), _ptr(scales), rows, K, _ptr(values), _VAL_DTYPE[values.dtype], ld,
-                                       _stream(stream)))
+    dtype, rows, K, ld = _mx_views(values, codes, scales)
+    _check(load().moe_dequantize_mxfp4(codes.data_ptr(), scales.data_ptr(), rows, K, values.data_ptr(), dtype, ld,
+                                       _stream_of(values, stream)))
 
 
 def moe_matmul_mxfp4(A_codes, A_scales, B, C, slot_offset=None, row_index=None, stream=None):
     """C [M][N] = rows of A times the packed slices B [P][bytes] (or one slice
     [bytes]); A_codes uint8 [A_rows][K/2], A_scales uint8 [A_rows][K/32]."""
-    A_rows, K = A_codes.shape[0], 2 * A_codes.shape[1]
+    u8 = torch.uint8
+    A_rows, half = A_codes.shape
     M, N = C.shape
-    P = 1 if B.dim() == 1 else B.shape[0]
-    if A_codes.dtype != torch.uint8 or A_scales.dtype != torch.uint8 or B.dtype != torch.uint8:
+    K = 2 * half
+    dtype, dev = _VAL_DTYPE.get(C.dtype), C.get_device()
+    b_shape, b_stride = B.shape, B.stride()
+    P = 1 if len(b_shape) == 1 else b_shape[0]
+    if A_codes.dtype is not u8 or A_scales.dtype is not u8 or B.dtype is not u8:
         raise ValueError("A_codes, A_scales and B must be uint8")
-    if not A_codes.is_contiguous() or not A_scales.is_contiguous() or tuple(A_scales.shape) != (A_rows, K // 32):
+    if not A_codes.is_contiguous() or not A_scales.is_contiguous() or A_scales.shape != (A_rows, K // 32):
         raise ValueError("A_codes [A_rows][K/2] and A_scales [A_rows][K/32] must be contiguous")
-    if C.dtype not in _VAL_DTYPE or C.stride(1) != 1 or (M > 1 and C.stride(0) < N):
+    ldc, step = C.stride()
+    if M <= 1:
+        ldc = (N + 7) // 8 * 8   # one row: any aligned stride does
+    if dtype is None or (step != 1 and N > 1) or ldc < N:
         raise ValueError("C must be float32 or bfloat16 with contiguous rows")
-    if B.shape[-1] < fp4_slice_bytes(N, K) or B.stride(-1) != 1:
+    if b_shape[-1] < fp4_slice_bytes(N, K) or b_stride[-1] != 1:
         raise ValueError("B: a slice is smaller than [N][K]")
+    if A_codes.get_device() != dev or A_scales.get_device() != dev or B.get_device() != dev:
+        raise ValueError("the operands must be on one device")
     for t, n, name in ((slot_offset, P + 1, "slot_offset"), (row_index, M, "row_index")):
-        if t is not None and (t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous()):
+        if t is not None and (t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous() or t.get_device() != dev):
             raise ValueError(f"{name}: need int32 [{n}]")
-    _check(load().moe_matmul_mxfp4(M, N, K, _ptr(A_codes), _ptr(A_scales), A_rows, _ptr(row_index), _ptr(slot_offset), P,
-                                   _ptr(B), B.stride(0) if B.dim() > 1 else B.numel(), _ptr(C), _VAL_DTYPE[C.dtype],
-                                   row_stride(C), _stream(stream)))
+    _check(load().moe_matmul_mxfp4(M, N, K, A_codes.data_ptr(), A_scales.data_ptr(), A_rows, _ptr(row_index),
+                                   _ptr(slot_offset), P, B.data_ptr(), b_stride[0] if len(b_shape) > 1 else b_shape[0],
+                                   C.data_ptr(), dtype, ldc, _stream_of(C, stream)))
 
 
 def moe_pack_gate_up(shape, Wg, Wu, dst, n, src_stride, dst_stride, stream=None):

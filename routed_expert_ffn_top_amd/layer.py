@@ -92,16 +92,24 @@ class MoELayer:
         """The resident layer with MXFP4 weights on MXFP4 activations: X is
         routed as it is, then quantised, and H is quantised between the
         projections. Y holds the residual on entry and the layer output on
-        return."""
+        return. One call at a time, as with ``forward``: they share the workspace."""
         s, cfg = self.shape, self.cfg
         if not cfg.fp4_weights or self.paged or s.capacity < cfg.T * cfg.kp:
             raise ValueError("needs a resident layer with MXFP4 weights and capacity for every route")
-        if logits is None:
-            logits = torch.empty((cfg.T, cfg.E), dtype=torch.float32, device=self.device)
-            B.moe_router_logits(s, self.X, self.Wr, self.bias, logits, stream)
+        B.check_rows(Y, torch.float32, cfg.d, "Y")
+        if logits is not None:
+            B.check_rows(logits, torch.float32, cfg.E, "logits")
+        for t, name in ((Y, "Y"), (logits, "logits")):
+            if t is not None and (t.shape[0] != cfg.T or not t.is_contiguous()):
+                raise ValueError(f"{name}: need {cfg.T} rows, contiguous")
         n = cfg.T * cfg.d
         if self._xq is None:
             self._xq = torch.empty(n // 2 + n // 32, dtype=torch.uint8, device=self.device)
+            self._logits = torch.empty((cfg.T, cfg.E), dtype=torch.float32, device=self.device)
+            torch.cuda.synchronize(self.device)   # whatever stream comes next, its memory's last use is over
+        if logits is None:
+            logits = self._logits
+            B.moe_router_logits(s, self.X, self.Wr, self.bias, logits, stream)
         B.moe_quantize_mxfp4(self.X, self._xq[: n // 2], self._xq[n // 2:], stream)
         B.moe_route_build(s, 0, cfg.T, logits, self.phi, B.MOE_ROUTE_RESET, self.routes, self.ws, stream)
         B.moe_expert_ffn(s, self._xq, Y, self.routes, self.arena, self.phi,
@@ -113,7 +121,9 @@ class MoELayer:
         """The layer on a few new tokens X [T][d] (rows may be strided), with
         the resident experts: Y [T][d] holds the residual on entry and the
         layer output on return. Route ids and weights are in
-        ``decode_routes(T)``. One call at a time (one workspace a token count)."""
+        ``decode_routes(T)``. One call at a time with a token count, graphs
+        included: they share its workspace. It is made by the first call, so
+        that one cannot be a captured one."""
         B.check_rows(X, self.X.dtype, self.cfg.d, "X")
         B.check_rows(Y, torch.float32, self.cfg.d, "Y")
         if X.shape[0] != Y.shape[0] or (logits is not None and tuple(logits.shape) != (X.shape[0], self.cfg.E)):
@@ -122,7 +132,8 @@ class MoELayer:
         shape.ldx, shape.ldy = B.row_stride(X), B.row_stride(Y)
         if logits is not None:
             B.check_rows(logits, torch.float32, self.cfg.E, "logits")
-            logits = logits.contiguous()
+            if not logits.is_contiguous():   # a copy made here could be reused before another stream has read it
+                raise ValueError("logits must be contiguous")
         B.moe_layer_decode(shape, X, None if logits is not None else self.Wr, None if logits is not None else self.bias,
                            logits, Y, self.arena, routes, ws, stream)
         return Y
@@ -133,12 +144,15 @@ class MoELayer:
 
     def _decode_buffers(self, T: int):
         if T not in self._decode:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError(f"decode {T} tokens once, or ask for decode_routes({T}), before capturing it")
             c = self.cfg
             shape = B.make_shape(T, c.d, c.f, c.E, c.k, c.n_shared, P=self.shape.P, capacity=1, dtype=c.dtype,
                                  renorm=c.renorm)
             ws = B.alloc_decode_workspace(shape, self.device)
             routes = dict(topk_idx=torch.zeros((T, c.kp), dtype=torch.int32, device=self.device),
                           topk_w=torch.zeros((T, c.kp), dtype=torch.float32, device=self.device))
+            torch.cuda.synchronize(self.device)   # cleared for whatever stream comes next
             self._decode[T] = (shape, routes, ws)
         return self._decode[T]
 

@@ -546,3 +546,27 @@ def test_decode_workspace_serves_several_shapes_and_layers():
             l.decode(X, Z)
             torch.cuda.synchronize()
             assert torch.equal(Y, Z)
+
+
+def test_decode_first_call_not_captured_and_strided_logits_refused():
+    """The workspace's clearing, recorded and not run, would leave the next eager
+    call with counters of anything."""
+    say("decode: a first call within a capture, logits that would be copied")
+    cfg = SMALL
+    inp = gpu_inputs(cfg)
+    layer = MoELayer(inp)
+    X, Y = inp.X[:2].contiguous(), inp.A[:2].contiguous()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        X.mul_(1.0)
+        with pytest.raises(RuntimeError):
+            layer.decode(X, Y)
+    with pytest.raises(ValueError):
+        layer.decode(X, Y, logits=torch.zeros(2, 2 * cfg.E, device="cuda")[:, : cfg.E])
+    Z = Y.clone()
+    layer.decode(X, Y)                   # makes the workspace; a stream of its own may come next
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    layer.decode(X, Z, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, Z)

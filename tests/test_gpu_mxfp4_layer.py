@@ -204,6 +204,10 @@ def test_refusals():
             B.moe_expert_ffn(layer.shape, xq, inp.A, layer.routes, layer.arena, layer.phi,
                              B.MOE_FFN_EXPERTS | B.MOE_FFN_ACT_MXFP4 | other, layer.ws)
         assert ei.value.status == B.MOE_ERR_UNSUPPORTED
+    for kw in (dict(Y=inp.A[:3]), dict(Y=inp.A, logits=torch.zeros(3, 2, device="cuda")),
+               dict(Y=inp.A, logits=torch.zeros(4, 4, device="cuda")[:, :2])):
+        with pytest.raises(ValueError):
+            layer.forward_mxfp4(**kw)
     bf = gpu_inputs(cfg.with_(dtype="bf16", name="mx_layer_bf16"))
     with pytest.raises(ValueError):
         MoELayer(bf).forward_mxfp4(bf.A)

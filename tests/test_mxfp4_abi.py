@@ -81,3 +81,26 @@ def test_mxfp4_activations_refused(dtype, flags):
                          B.MOE_FFN_EXPERTS | B.MOE_FFN_ACT_MXFP4 | flags, _FakeWs(B.moe_workspace_bytes(s)), 0)
     assert e.value.status == UN
     B.moe_arena_destroy(h)
+
+
+class _On:
+    """A tensor or stream of some device, as far as the check looks."""
+
+    def __init__(self, device):
+        self.device_index = device
+
+    def get_device(self):
+        return self.device_index
+
+
+def test_other_devices_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(B, "_raw_stream", lambda device: 100 + device)
+    assert B._stream_of(_On(1), None) == 101
+    assert B._stream_of(0x1000, 7) == 7
+    with pytest.raises(ValueError):
+        B._stream_of(_On(0), None)
+    with pytest.raises(ValueError):
+        B._stream_of(torch.zeros(4), None)      # host memory
+    with pytest.raises(ValueError):
+        B._stream_of(_On(1), _On(0))

@@ -358,8 +358,9 @@ moe_status moe_layer_prefill_noalloc(const moe_shape *shape, const void *X,
  *   H_i = SiLU(W_g x_t) * (W_u x_t),  o_i = alpha_i * (W_d H_i),
  *   Y[t] += o_i over the token's routes i = t*K'..t*K'+K'-1, ascending,
  * in fp32: unlike the prompt layer's bf16 H, H is not rounded, so the outputs
- * of the two differ by that rounding. Each expert hit is read once. Y is
- * bitwise run-to-run identical and independent of phi and P.
+ * of the two differ by that rounding. Each expert hit is read once (once for
+ * every 5 to 64 of its routes, whichever suits the shape). Y is bitwise
+ * run-to-run identical and independent of phi and P.
  *   shape    T <= MOE_DECODE_MAX_T tokens, T * K' <= MOE_DECODE_MAX_ROUTES,
  *            d <= MOE_DECODE_MAX_D, a packed gate/up slice below 2 GiB
  *            (MOE_ERR_UNSUPPORTED otherwise); every dtype; `capacity` is not
@@ -577,7 +578,9 @@ moe_status moe_selftest_mfma_layout(float *out, moe_stream stream);
  * launches (process-wide): each such launch is bracketed by a pair of HIP
  * events recorded on the launch's stream. moe_profile_end waits for those
  * events, writes up to n per-launch durations in milliseconds to ms (host),
- * stores the number of timed launches in *recorded and disarms. */
+ * stores the number of timed launches in *recorded and disarms.
+ * moe_layer_decode's launches are ROUTER (where routing has one), GATE_UP and
+ * DOWN (combine included); calls under stream capture are not to be timed. */
 moe_status moe_profile_begin(int32_t kernel, int32_t max_launches);
 moe_status moe_profile_end(int32_t kernel, float *ms, int32_t n,
                            int32_t *recorded);

@@ -6,8 +6,9 @@
 //
 // With one to a few rows an expert, the layer's time is that of reading the
 // weights of the experts hit, once; every product is a matrix times at most 64
-// columns. A workgroup takes 64 rows of one slot's weight slice over all of K
-// and all of the slot's routes, so that a weight is read by one workgroup only.
+// columns. A workgroup takes 64 rows (32 where 64 routes share a slot) of one
+// slot's weight slice over all of K and an entry's routes (dec_rpe: most slots'
+// routes are one entry), so that a weight is read by one workgroup only.
 // Its waves cut K among themselves (each its own stretch of the slice, whose
 // 64 rows of a K piece are contiguous in the tiled layout) and add their sums
 // in a fixed order through LDS.
@@ -777,7 +778,7 @@ __global__ __launch_bounds__(256, 2) void k_dec_route_proj(DecArgs a, DecRouteAr
     proj_tiles<WF, RPE, NT, NW, true>(a, n, sh);
 }
 
-// Persistent workgroups: two per compute unit of the 256.
+// Persistent workgroups: two of 8 waves, or four of 4, per compute unit of the 256.
 constexpr int kDecGrid = 512;
 
 template <int WF, int RPE, int NT, int NW, bool GATEUP>

@@ -282,6 +282,35 @@ __device__ __forceinline__ void wait_vmcnt_stages(int n)
     }
 }
 
+// Workgroup barrier that waits for this wave's LDS traffic only (see wait_vmcnt).
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// BYTES (4 or 16) a lane from src to LDS, lane after lane from address dst (the
+// same in every lane). Written out: of the builtin the compiler does not know
+// which bytes it writes, and may let LDS reads of other stages wait for it (gate/up
+// with MXFP4 H, 32768 x 2048 x 2048 over 64 slots: 151 -> 116 us). No register is written and the address is read
+// at issue, so wait_vmcnt is all that has to know of it.
+template <int BYTES>
+__device__ __forceinline__ void copy_to_lds(const void *src, uint32_t dst)
+{
+    if constexpr (BYTES == 16)
+        asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(dst), "v"(src) : "memory");
+    else
+        asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(dst), "v"(src) : "memory");
+}
+// The same, 16 bytes, from base (the same in every lane) + off.
+__device__ __forceinline__ void copy_to_lds(const void *base, uint32_t off, uint32_t dst)
+{
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(dst), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) { return (uint32_t)(uintptr_t)(LDS_AS const void *)p; }
+
 constexpr int kXcd = 8;
 constexpr int kStream = 2;   // buffer stores of C, which is not read here: non-temporal (fp32 C 141 -> 132 us)
 
@@ -293,9 +322,11 @@ constexpr int kStream = 2;   // buffer stores of C, which is not read here: non-
 // read byte by byte, are the fewer. A rows are stored with their 16-byte chunk
 // c at c ^ ((row >> 2) & 3), which keeps the fragment reads free of bank
 // conflicts; the pieces of B are so as they stand. A row's scale bytes of a
-// stage are one 32-bit word, aligned or not: SHIFT copies the two aligned words
-// that hold it and the lanes cut it out; without it (K % 128 == 0 and aligned
-// scales) one word is copied. The tiles of an XCD (workgroup id mod 8) are one
+// stage are one 32-bit word, aligned or not: with SHIFT the lanes cut it out of
+// the two aligned words that hold it; without it (K % 128 == 0 and aligned
+// scales) it is a word. The words of four stages, a panel, are copied together, a
+// quarter of the rows a stage: a word at a time each is a request of its own to
+// the L2, 256 of a stage's 650 (copies alone 95 -> 74 us). The tiles of an XCD (workgroup id mod 8) are one
 // contiguous range, column block major, walked in step, so that tiles which
 // share weights or rows share that XCD's L2.
 //
@@ -311,7 +342,8 @@ constexpr int kStream = 2;   // buffer stores of C, which is not read here: non-
 // few: the 16 rows' block maxima by halving (24 + 12 + 6 + 3 operations and one
 // exchange, not 16 times 10), one scale a lane, brought to the row's 16 lanes as
 // an operand of the multiplication (32768 x 2048 x 2048
-// over 64 slots 195 -> 151 us; the bf16-activation kernel takes 290).
+// over 64 slots 195 -> 151 us, and 116 with the copies written out; the bf16-activation
+// kernel takes 290).
 __device__ __forceinline__ float silu_mul(float g, float u)
 {
     // hardware exp2 and reciprocal: off by (|g| + 4) 2^-23 at most, before 4 bits are kept
@@ -376,16 +408,21 @@ template <int BM, int NS, bool SHIFT, int EPI>
 __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
 {
     constexpr int BN = 256, WM = 2, WN = 4, TM = BM / WM, TN = BN / WN, MI = TM / 32, NI = TN / 32;
-    constexpr int ACODE = BM * 64, BCODE = BN * 64, ASC = BM * (SHIFT ? 8 : 4), BSC = BN * 4;
-    constexpr int STAGE = ACODE + BCODE + ASC + BSC;
-    constexpr int AI = BM / 128, BI = 2, SI = SHIFT ? 2 : 1;   // copies per wave and stage
-    constexpr int LOADS = AI + BI + SI;
-    static_assert(BM == 256 && NS >= 3, "the copies of the scales are laid out for 256 rows");
-    __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE];
+    constexpr int ACODE = BM * 64, BCODE = BN * 64, BSC = BN * 4;
+    constexpr int STAGE = ACODE + BCODE + BSC;
+    constexpr int AI = BM / 128, BI = 2;           // code copies per wave and stage
+    constexpr int LOADS = AI + BI + 1;             // and one of scales
+    constexpr int APANEL = BM * 16, NP = 3;        // A's scales of 4 stages, [row][4 words]; panels there at a time
+    static_assert(BM == 256 && NS == 4, "the copies of the scales are laid out for 256 rows and panels of 4 stages");
+    __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE + NP * APANEL];
+    char *const apanel = lds + NS * STAGE;
     __shared__ int32_t s_tpref[kMaxExp + 1], s_lo[kMaxExp], s_cnt[kMaxExp];
     __shared__ int32_t s_shift[SHIFT ? BM : 1];   // bytes from the aligned word to a row's scales
-    __shared__ int32_t s_route[2][EPI == EPI_DOWN ? BM : 1];   // by tile parity
+    // of three tiles, this one, the next and the one after it: the rows of A of
+    // its records, or (down, where record p is row p) their routes
+    __shared__ int32_t s_rows[3][BM];
     __shared__ float s_alpha[2][EPI == EPI_DOWN ? BM : 1];
+    const uint32_t lds_at = lds_address(lds), rows_at = lds_address(s_rows), alpha_at = lds_address(s_alpha);
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -427,33 +464,42 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
             if (s_tpref[mid] <= L) lo = mid; else hi = mid - 1;
         }
         const int mt = (s_cnt[lo] + BM - 1) / BM, local = L - s_tpref[lo], ml = local % mt;
-        Tile t;
-        t.slot = lo;
-        t.row0 = s_lo[lo] + ml * BM;
+        Tile t;   // the same in every lane
+        t.slot = __builtin_amdgcn_readfirstlane(lo);
+        t.row0 = __builtin_amdgcn_readfirstlane(s_lo[lo] + ml * BM);
         t.rows = __builtin_amdgcn_readfirstlane(min(BM, s_cnt[lo] - ml * BM));
-        t.n0 = (local / mt) * BN;
+        t.n0 = __builtin_amdgcn_readfirstlane((local / mt) * BN);
         return t;
     };
 
     // Copies of this wave: A codes rows 16 (wave AI + j) .. +15 (lane: row + l/4,
     // chunk position l % 4), B codes 64 rows 64 ((2 wave + j) % 4) .. of piece
-    // (2 wave + j) / 4, and scales: waves 0-3 those of A rows 64 wave .. +63,
-    // waves 4-7 the 256 of B's piece wave - 4.
-    const char *asrc[AI], *bsrc[BI], *ssrc[SI];
+    // (2 wave + j) / 4, and scales: waves 0-3 those of A rows 64 wave + 16 q .. +15
+    // (lane: row + l/4, word l % 4), q = stage % 4, of the next panel, waves 4-7
+    // the 256 of B's piece wave - 4.
+    const char *asrc[AI], *bsrc;   // bsrc: the same in every lane
+    uint32_t boff[BI], soff;
+    int srow[4];
     int bstep = 0;
-    auto fetch_rows = [&](const Tile &t, int *rows) {
-#pragma unroll
-        for (int j = 0; j < AI; ++j) rows[j] = row_of(a, t.row0 + min((wave * AI + j) * 16 + (lane >> 2), t.rows - 1));
-        rows[AI] = row_of(a, t.row0 + min((wave & 3) * 64 + lane, t.rows - 1));
+    // A tile's rows or routes to LDS. No register waits for them: a load into one
+    // would be waited for with everything requested after it.
+    auto fetch_rows = [&](const Tile &t, int buf) {
+        const int32_t *src = EPI == EPI_DOWN ? a.rec_route : a.row_index;
+        if (src && wave < BM / 64)
+            copy_to_lds<4>(src + t.row0 + min(wave * 64 + lane, t.rows - 1), rows_at + (buf * BM + wave * 64) * 4);
+    };
+    auto row_in = [&](const Tile &t, int buf, int i) {
+        const int r = min(i, t.rows - 1);
+        return EPI != EPI_DOWN && a.row_index ? min(max(s_rows[buf][r], 0), a.A_rows - 1) : t.row0 + r;
     };
     auto scales_at = [&](int row) { return (uintptr_t)a.As + (uintptr_t)((int64_t)row * (K / 32)); };
     // the last aligned word that holds scale bytes
     const uintptr_t last_word = (scales_at(a.A_rows) - 1) & ~(uintptr_t)3;
-    auto set_sources = [&](const Tile &t, const int *rows) {
+    auto set_sources = [&](const Tile &t, int buf) {
 #pragma unroll
         for (int j = 0; j < AI; ++j) {
             const int r = (wave * AI + j) * 16 + (lane >> 2);
-            asrc[j] = (const char *)a.A + (int64_t)rows[j] * (K / 2) + ((lane & 3) ^ ((r >> 2) & 3)) * 16;
+            asrc[j] = (const char *)a.A + (int64_t)row_in(t, buf, r) * (K / 2) + ((lane & 3) ^ ((r >> 2) & 3)) * 16;
         }
         const int nb = t.n0 / kWRows, rows_nb = min(kWRows, N - nb * kWRows);
         const int64_t pb = fp4_piece_bytes(rows_nb);
@@ -462,53 +508,43 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
 #pragma unroll
         for (int j = 0; j < BI; ++j) {
             const int c = wave * BI + j;
-            bsrc[j] = Bblk + (c >> 2) * pb + min((c & 3) * 64 + lane, rows_nb - 1) * 16;
+            boff[j] = (uint32_t)((c >> 2) * pb) + min((c & 3) * 64 + lane, rows_nb - 1) * 16;
         }
-        if (wave < 4) {
-            const uintptr_t p = scales_at(rows[AI]) & ~(uintptr_t)3;
-            ssrc[0] = (const char *)p;
-            if constexpr (SHIFT) {
-                ssrc[1] = (const char *)p;
-                s_shift[wave * 64 + lane] = (int)(scales_at(rows[AI]) & 3);   // read after the tile's first barrier
-            }
-        } else {
-            ssrc[0] = Bblk + (wave - 4) * pb + rows_nb * 16 + ((lane & 15) * 16 < rows_nb ? (lane & 15) * 16 : 0);
-            if constexpr (SHIFT) ssrc[1] = ssrc[0];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            srow[q] = row_in(t, buf, (wave & 3) * 64 + q * 16 + (lane >> 2));
+            if (SHIFT && wave < 4)   // read after the tile's first barrier
+                s_shift[wave * 64 + q * 16 + (lane >> 2)] = (int)(scales_at(srow[q]) & 3);
         }
+        soff = (uint32_t)((wave & 3) * pb) + rows_nb * 16 + ((lane & 15) * 16 < rows_nb ? (lane & 15) * 16 : 0);
+        bsrc = Bblk;
     };
     const int nk = (K + 127) / 128;
     const bool odd = SHIFT && (K & 64) != 0;   // the last stage has 64 k
+    // the 16 rows q of this wave's 64, words of panel pn; past the last row's, the last
+    auto issue_ascales = [&](int pn, int q, int row) {
+        const uintptr_t p = (scales_at(row) & ~(uintptr_t)3) + (uintptr_t)(pn * 16 + (lane & 3) * 4);
+        copy_to_lds<4>((const void *)(p < last_word ? p : last_word), lds_at + NS * STAGE + pn % NP * APANEL + (wave * 4 + q) * 256);
+    };
     auto issue = [&](int kt) {
-        char *st = lds + (kt % NS) * STAGE;
+        const uint32_t st = lds_at + (kt % NS) * STAGE;
         // the pieces past K of a last half stage are those of its first half again, and not used
         const bool tail = odd && kt == nk - 1;
 #pragma unroll
         for (int j = 0; j < AI; ++j) {
             const int c = (lane & 3) ^ ((((wave * AI + j) * 16 + (lane >> 2)) >> 2) & 3);
-            __builtin_amdgcn_global_load_lds((const GLOBAL_AS void *)(asrc[j] + (int64_t)kt * 64 - (tail && c >= 2 ? 32 : 0)),
-                                             (LDS_AS void *)(st + (wave * AI + j) * 1024), 16, 0, 0);
+            copy_to_lds<16>(asrc[j] + (int64_t)kt * 64 - (tail && c >= 2 ? 32 : 0), st + (wave * AI + j) * 1024);
         }
 #pragma unroll
         for (int j = 0; j < BI; ++j) {
             const int c = wave * BI + j;
-            __builtin_amdgcn_global_load_lds(
-                (const GLOBAL_AS void *)(bsrc[j] + (int64_t)kt * bstep - (tail && (c >> 2) >= 2 ? bstep / 2 : 0)),
-                (LDS_AS void *)(st + ACODE + c * 1024), 16, 0, 0);
+            copy_to_lds(bsrc + (int64_t)kt * bstep - (tail && (c >> 2) >= 2 ? bstep / 2 : 0), boff[j], st + ACODE + c * 1024);
         }
         if (wave < 4) {
-#pragma unroll
-            for (int q = 0; q < SI; ++q) {
-                const uintptr_t p = (uintptr_t)ssrc[q] + (uintptr_t)kt * 4 + 4 * q;
-                __builtin_amdgcn_global_load_lds((const GLOBAL_AS void *)(p < last_word ? p : last_word),
-                                                 (LDS_AS void *)(st + ACODE + BCODE + q * BM * 4 + wave * 256), 4, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int q = 0; q < SI; ++q)
-                if (lane < 16)
-                    __builtin_amdgcn_global_load_lds(
-                        (const GLOBAL_AS void *)(ssrc[q] + (int64_t)kt * bstep - (tail && wave >= 6 ? bstep / 2 : 0)),
-                        (LDS_AS void *)(st + ACODE + BCODE + ASC + (wave - 4) * 256), 16, 0, 0);
+            const int q = kt & 3;
+            issue_ascales(kt / 4 + 1, q, q & 2 ? (q & 1 ? srow[3] : srow[2]) : (q & 1 ? srow[1] : srow[0]));
+        } else if (lane < 16) {
+            copy_to_lds(bsrc + (int64_t)kt * bstep - (tail && wave >= 6 ? bstep / 2 : 0), soff, st + ACODE + BCODE + (wave - 4) * 256);
         }
     };
 
@@ -518,23 +554,24 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
     u32x4_t af[2][MI], bf[2][NI];
     int as[MI], bs[2][NI];   // A: this lane's scale bytes at bytes 0 (step 0) and 2 (step 1)
     int asn[MI];
-    auto read_frags = [&](int stage, int ks, int set) {
-        const char *st = lds + stage * STAGE;
+    auto read_frags = [&](int kt, int ks, int set) {
+        const char *st = lds + (kt % NS) * STAGE;
         const char *As = st + wm * TM * 64 + foff[ks];
 #pragma unroll
         for (int i = 0; i < MI; ++i) af[set][i] = *(const u32x4_t *)(As + i * 32 * 64);
         const char *Bs = st + ACODE + (2 * ks + half) * (BN * 16) + (wn * TN + (lane & 31)) * 16;
 #pragma unroll
         for (int j = 0; j < NI; ++j) bf[set][j] = *(const u32x4_t *)(Bs + j * 32 * 16);
-        const char *Bc = st + ACODE + BCODE + ASC + (2 * ks + half) * BN + wn * TN + (lane & 31);
+        const char *Bc = st + ACODE + BCODE + (2 * ks + half) * BN + wn * TN + (lane & 31);
 #pragma unroll
         for (int j = 0; j < NI; ++j) bs[set][j] = *(const uint8_t *)(Bc + j * 32);
         if (ks == 0) {
-            const char *Ac = st + ACODE + BCODE + (wm * TM + (lane & 31)) * 4;
+            const char *Ac = apanel + (wm * TM + (lane & 31)) * 16;
+            const int w0 = (kt >> 2) % NP * APANEL + (kt & 3) * 4, w1 = ((kt + 1) >> 2) % NP * APANEL + ((kt + 1) & 3) * 4;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                uint32_t w = *(const uint32_t *)(Ac + i * 128);
-                if constexpr (SHIFT) w = __builtin_amdgcn_alignbyte(*(const uint32_t *)(Ac + BM * 4 + i * 128), w,
+                uint32_t w = *(const uint32_t *)(Ac + w0 + i * 512);
+                if constexpr (SHIFT) w = __builtin_amdgcn_alignbyte(*(const uint32_t *)(Ac + w1 + i * 512), w,
                                                                   s_shift[wm * TM + i * 32 + (lane & 31)]);
                 asn[i] = (int)(w >> (8 * half));
             }
@@ -566,86 +603,73 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
         }
     };
 
-    // down: route and weight of row tid, asked for during a tile and put into
-    // LDS for the next one
-    int pre_route = 0;
-    float pre_alpha = 0.0f;
-    auto fetch_route = [&](const Tile &t) {
-        if (EPI == EPI_DOWN && tid < BM) pre_route = a.rec_route[t.row0 + min(tid, t.rows - 1)];
-    };
-    auto fetch_alpha = [&]() {
-        if (EPI == EPI_DOWN && tid < BM) pre_alpha = a.topk_w[pre_route];
-    };
-    auto store_route = [&](int par) {
-        if (EPI == EPI_DOWN && tid < BM) {
-            s_route[par][tid] = pre_route;
-            s_alpha[par][tid] = pre_alpha;
-        }
+    // A tile's first requests: rows of the tile after it, the weights of its
+    // routes, the first panel of A's scales, the first stages. They are the oldest
+    // of what the wait for its first stage waits for.
+    auto begin = [&](const Tile &t, int buf, int par, const Tile &after, int after_buf) {
+        fetch_rows(after, after_buf);
+        if (EPI == EPI_DOWN && wave < BM / 64)
+            copy_to_lds<4>(a.topk_w + s_rows[buf][wave * 64 + lane], alpha_at + (par * BM + wave * 64) * 4);
+        if (wave < 4)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) issue_ascales(0, q, srow[q]);
+#pragma unroll
+        for (int p = 0; p < NS - 1; ++p)
+            if (p < nk) issue(p);
     };
 
-    int tl = li, par = 0;
-    Tile cur = decode(start_x + tl);
-    fetch_route(cur);
-    fetch_alpha();
-    store_route(0);
-    int rows[AI + 1];
-    fetch_rows(cur, rows);
-    set_sources(cur, rows);
-#pragma unroll
-    for (int p = 0; p < NS - 1; ++p)
-        if (p < nk) issue(p);
+    int tl = li, par = 0, buf = 0;
+    Tile cur = decode(start_x + tl), nxt = tl + nwg < cnt_x ? decode(start_x + tl + nwg) : cur;
+    fetch_rows(cur, 0);
+    wait_vmcnt<0>();
+    __syncthreads();
+    set_sources(cur, 0);
+    begin(cur, 0, 0, nxt, 1);
     for (;;) {
         const bool wave_active = wm * TM < cur.rows;
         const int tn = tl + nwg;
         const bool has_next = tn < cnt_x;
-        const Tile nxt = has_next ? decode(start_x + tn) : cur;
+        const Tile after = tn + nwg < cnt_x ? decode(start_x + tn + nwg) : nxt;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-        // Loads return in order: stage 0 is there once no more than the copies
-        // of the min(NS - 2, nk - 1) stages requested after it are outstanding.
-        wait_vmcnt_stages<LOADS, NS - 2>(min(NS - 2, nk - 1));
-        __syncthreads();
+        // The first stages, and the last tile's stores (leaving these under way
+        // gains nothing).
+        wait_vmcnt<0>();
+        lds_barrier();
         if (wave_active) read_frags(0, 0, 0);
         // At the top of step kt stage kt is visible to every wave, and this wave
         // holds its step-0 fragments. Stage kt + 1 is made visible (own copies
-        // waited for, then a barrier) and stage kt + NS - 1 requested into the
-        // slot of stage kt - 1, which every wave finished before that barrier.
+        // waited for, unless it is one of the first, then a barrier) and stage
+        // kt + NS - 1 requested into the slot of stage kt - 1, which every wave
+        // finished before that barrier. Loads return in order: stage kt + 1 is there
+        // once no more than the copies of the next one are outstanding.
         for (int kt = 0; kt < nk; ++kt) {
-            const int stage = kt % NS;
             const bool more = kt + 1 < nk;
             if (more) {
-                wait_vmcnt_stages<LOADS, NS - 3>(min(NS - 3, nk - 2 - kt));
+                if (kt + 1 >= NS - 1) wait_vmcnt_stages<LOADS, NS - 3>(min(NS - 3, nk - 2 - kt));
                 __builtin_amdgcn_s_barrier();
             }
-            if (has_next && kt == 0) {
-                fetch_rows(nxt, rows);
-                fetch_route(nxt);
-            }
-            if (has_next && kt == 1) fetch_alpha();
             if (more && kt + NS - 1 < nk) issue(kt + NS - 1);
             if (wave_active) {
-                read_frags(stage, 1, 1);
+                read_frags(kt, 1, 1);
                 mfmas(std::integral_constant<int, 0>());
                 interleave();
                 // on the last step this reads a resident stage again; the values are not used
-                read_frags((kt + 1) % NS, 0, 0);
+                read_frags(kt + 1, 0, 0);
                 if (!(odd && !more)) mfmas(std::integral_constant<int, 1>());
                 interleave();
             }
         }
         const Tile done = cur;
         if (has_next) {
-            if (nk < 2) fetch_alpha();
-            __syncthreads();   // nothing reads the ring any more
-            set_sources(nxt, rows);
-            store_route(par ^ 1);   // last read a tile ago
-#pragma unroll
-            for (int p = 0; p < NS - 1; ++p)
-                if (p < nk) issue(p);
+            lds_barrier();   // nothing reads the ring any more
+            const int nb = buf == 2 ? 0 : buf + 1;
+            set_sources(nxt, nb);
+            begin(nxt, nb, par ^ 1, after, nb == 2 ? 0 : nb + 1);
         }
         // Register r of lane l holds row 8 (r / 4) + 4 (l / 32) + r % 4 and column
         // l % 32 of its block. bf16: adjacent lanes swap a value of rows R, R + 1,
@@ -696,7 +720,7 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
                         const int m = wm * TM + i * 32 + 8 * (r / 4) + 4 * half + (r & 3);
                         if (m >= done.rows) continue;
                         const float al = s_alpha[par][m];
-                        float *y = C + (int64_t)s_route[par][m] * a.ldc;
+                        float *y = C + (int64_t)s_rows[buf][m] * a.ldc;
 #pragma unroll
                         for (int j = 0; j < NI; ++j) y[j * 32] = al * acc[i][j][r];
                         for (int q = 1; q < a.splits; ++q)
@@ -705,7 +729,7 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
                     }
             }
             if (done.n0 == 0)
-                for (int m = tid; m < done.rows; m += 512) a.done[s_route[par][m]] = 1;
+                for (int m = tid; m < done.rows; m += 512) a.done[s_rows[buf][m]] = 1;
         } else if (wave_active && done.n0 + wn * TN < N) {
             const int esz = a.c_bf16 ? 2 : 4;
             char *base = (char *)a.C + ((int64_t)done.row0 * a.ldc + done.n0 + wn * TN) * esz;
@@ -747,8 +771,10 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
         }
         if (!has_next) break;
         cur = nxt;
+        nxt = after;
         tl = tn;
         par ^= 1;
+        buf = buf == 2 ? 0 : buf + 1;
     }
 }
 

@@ -295,19 +295,20 @@ __device__ __forceinline__ void lds_barrier()
 // same in every lane). Written out: of the builtin the compiler does not know
 // which bytes it writes, and may let LDS reads of other stages wait for it (gate/up
 // with MXFP4 H, 32768 x 2048 x 2048 over 64 slots: 151 -> 116 us). No register is written and the address is read
-// at issue, so wait_vmcnt is all that has to know of it.
+// at issue, so wait_vmcnt is all that has to know of it. s_nop: a scalar register
+// that a vector instruction wrote is not to be read by the next five.
 template <int BYTES>
 __device__ __forceinline__ void copy_to_lds(const void *src, uint32_t dst)
 {
     if constexpr (BYTES == 16)
-        asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(dst), "v"(src) : "memory");
+        asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(dst), "v"(src) : "memory");
     else
-        asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" ::"{m0}"(dst), "v"(src) : "memory");
+        asm volatile("s_nop 4\n\tglobal_load_lds_dword %1, off" ::"{m0}"(dst), "v"(src) : "memory");
 }
 // The same, 16 bytes, from base (the same in every lane) + off.
 __device__ __forceinline__ void copy_to_lds(const void *base, uint32_t off, uint32_t dst)
 {
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(dst), "v"(off), "s"(base) : "memory");
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(dst), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ uint32_t lds_address(const void *p) { return (uint32_t)(uintptr_t)(LDS_AS const void *)p; }
 

@@ -809,12 +809,13 @@ hipError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, 
     return hipGetLastError();
 }
 
-// The ring kernel's time is that of whole tiles: 13 us for one round of tiles of
-// up to 128 rows and 19 us above (K = 2048), whatever they hold. The small
+// The ring kernel's time is that of whole tiles: 15 us for one round of tiles of
+// up to 128 rows and 20 us above (K = 2048), whatever they hold. The small
 // kernel's grows with its 32 x 64 pieces, 2.5 us for each 64 of them, and with
 // less than 16 rows a slot it is ahead at any size (64 slots of N = K = 2048: 1
-// row each 18 against 27 us, 16 rows 32 against 31, 64 rows 84 against 31; one
-// slot of 512 rows 13 against 19, of 2048 rows 38 against 20).
+// row each 18 against 30 us, 16 rows 32 against 32, 64 rows 84 against 32; one
+// slot of 512 rows 12 against 20, of 2048 rows 37 against 21). At the borders the
+// other one is up to 14 % faster (one slot of 128 rows, N = 8192: 21 against 24).
 static bool ring_pays(const MxArgs &a)
 {
     const int64_t slots = std::min(a.P, a.M), rows = a.M / slots;

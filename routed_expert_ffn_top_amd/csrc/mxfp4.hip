@@ -652,7 +652,9 @@ __global__ __launch_bounds__(512) void k_matmul_ring(MxArgs a)
             const bool more = kt + 1 < nk;
             if (more) {
                 if (kt + 1 >= NS - 1) wait_vmcnt_stages<LOADS, NS - 3>(min(NS - 3, nk - 2 - kt));
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");   // for the compiler: reads stay behind
                 __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
             }
             if (more && kt + NS - 1 < nk) issue(kt + NS - 1);
             if (wave_active) {

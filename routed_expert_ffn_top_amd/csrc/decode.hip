@@ -219,26 +219,41 @@ __device__ __forceinline__ void wave_topk(const DecRouteArgs &a, uint64_t *keys,
 
 // The routes by slot, by a workgroup of 256: counts, offsets, places; at most
 // rpe routes to an entry. slot_of(i) of route i < R; put_entry(n, slot, off, cnt),
-// put_rec(place, i); returns the number of entries. The order of the routes
-// within a slot is that of LDS atomics and is not fixed: it only says which
-// column of a matrix operand a route takes, and columns do not mix.
+// put_rec(place, i); returns the number of entries. The routes of a slot stand in
+// ascending order, whichever workgroup does this: where gate/up routes for itself
+// every workgroup does, and the entries it takes a part of have to be the same in
+// all. So 64 routes at a time take their places, not whichever wave comes first.
 template <int RT, typename S, typename PE, typename PR>
 __device__ __forceinline__ int build_lists(int R, int rpe, int32_t *cnt, int32_t *off, int32_t *wsum, S slot_of,
                                            PE put_entry, PR put_rec)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    static_assert(kMaxExp == 512, "two slots a thread, 9 bits a slot");
     cnt[tid] = cnt[tid + 256] = 0;
     __syncthreads();
     int slot[RT], pos[RT];
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
-        const int i = tid + 256 * q;
-        if (i < R) {
-            slot[q] = slot_of(i);
-            pos[q] = atomicAdd(&cnt[slot[q]], 1);
+        if (256 * q >= R) continue;
+        const bool is = tid + 256 * q < R;
+        slot[q] = is ? slot_of(tid + 256 * q) : 0;
+        // the wave's routes of the same slot
+        uint64_t same = __ballot(is);
+#pragma unroll
+        for (int b = 0; b < 9; ++b) {
+            const uint64_t one = __ballot((slot[q] >> b) & 1);
+            same &= (slot[q] >> b) & 1 ? one : ~one;
+        }
+        const int before = __popcll(same & ((1ull << lane) - 1));
+        for (int w = 0; w < 4 && 256 * q + 64 * w < R; ++w) {
+            if (wave == w && is) {
+                const int base = cnt[slot[q]];
+                pos[q] = base + before;
+                if (before == 0) cnt[slot[q]] = base + __popcll(same);
+            }
+            __syncthreads();
         }
     }
-    __syncthreads();
     // thread tid: slots 2 tid and 2 tid + 1
     const int c0 = cnt[2 * tid], c1 = cnt[2 * tid + 1];
     const int e0 = (c0 + rpe - 1) / rpe, e1 = (c1 + rpe - 1) / rpe;

@@ -570,3 +570,22 @@ def test_decode_first_call_not_captured_and_strided_logits_refused():
     layer.decode(X, Z, stream=st)
     torch.cuda.synchronize()
     assert torch.equal(Y, Z)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_decode_skewed_routing_within_gate_up(dtype):
+    """Every workgroup of gate/up sorts the routes for itself: their entries have
+    to agree where a slot has several and its routes are those of several waves."""
+    say(f"decode, every token on the same experts, routed within gate/up, {dtype}")
+    cfg = MoEConfig(name="dec_skew_self", index=82, T=4, d=128, f=1024, E=64, k=8, dtype=dtype)
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    X, A = tokens(cfg, 16)
+    L = skewed(16, 64, 8)
+    first = A.clone()
+    layer.decode(X, first, logits=L)
+    check(inp, weights, X, A, first, layer.decode_routes(16), "first")
+    for _ in range(200):
+        Y = A.clone()
+        layer.decode(X, Y, logits=L)
+        assert torch.equal(Y, first)

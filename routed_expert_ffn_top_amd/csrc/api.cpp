@@ -902,7 +902,8 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
     q.w = r.topk_w;
     q.ctr = ctr;
     q.l = lists;
-    const bool self = dec_self_routes(s, W_r != nullptr);
+    const bool self = dec_self_routes(s, W_r != nullptr), sorts = dec_gate_up_sorts(s, W_r != nullptr);
+    q.sort = !sorts;
     if (!self) HIP_TRY(TIMED(MOE_KERNEL_ROUTER, st, launch_dec_route(s, q, phi, st)), "route launch");
     DecArgs g{};
     g.l = lists;
@@ -926,8 +927,8 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
     g.K = s.d;
     g.out = ws_at<char>(ws, w.H);
     g.ldo = s.f;
-    if (self)
-        HIP_TRY(TIMED(MOE_KERNEL_GATE_UP, st, launch_dec_route_proj(s, g, q, phi, st)), "gate/up launch");
+    if (self || sorts)
+        HIP_TRY(TIMED(MOE_KERNEL_GATE_UP, st, launch_dec_route_proj(s, g, q, phi, self, st)), "gate/up launch");
     else
         HIP_TRY(TIMED(MOE_KERNEL_GATE_UP, st, launch_dec_proj(s, g, true, st)), "gate/up launch");
     h.X = g.out;

@@ -80,16 +80,19 @@ struct DecRouteArgs {
     const float *given;
     float *logits;
     int T, d, E, k, n_shared, renorm, P, rpe;
+    int sort;                 // the route launch sorts the routes by slot too
     int32_t *idx;
     float *w;
     int32_t *ctr;
     DecLists l;
 };
 
-// Whether gate/up does the routing itself (launch_dec_route_proj instead of
-// launch_dec_route and launch_dec_proj).
+// Whether gate/up does all of the routing, or its last part, the sorting by slot,
+// itself (launch_dec_route_proj, with `route` for the first, instead of
+// launch_dec_proj).
 bool dec_self_routes(const moe_shape &s, bool router);
-hipError_t launch_dec_route_proj(const moe_shape &s, const DecArgs &a, const DecRouteArgs &q, const PhiArg &phi,
+bool dec_gate_up_sorts(const moe_shape &s, bool router);
+hipError_t launch_dec_route_proj(const moe_shape &s, const DecArgs &a, const DecRouteArgs &q, const PhiArg &phi, bool route,
                                  hipStream_t st);
 hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const PhiArg &phi, hipStream_t st);
 hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a, bool gateup, hipStream_t st);

@@ -292,7 +292,7 @@ __device__ __forceinline__ int build_lists(int R, int rpe, int32_t *cnt, int32_t
     return all;
 }
 
-// Router, top-k and the routes by slot, in one launch. A workgroup takes 4
+// Router, top-k and (`sort`) the routes by slot, in one launch. A workgroup takes 4
 // experts for 4 tokens, a wave a token; the last workgroup of a token block
 // does its top-k, and the last block of all sorts the routes by slot. Bound by
 // latency: a wave has 32 KB of W_r to read for d = 2048, asked for at once (16
@@ -330,6 +330,7 @@ __global__ __launch_bounds__(256) void k_dec_route(DecRouteArgs a, PhiArg phi)
             a.w[r0 + rank] = w;
         });
     }
+    if (!a.sort) return;
     const bool alone = gridDim.x == 1;   // every token's ids are this workgroup's own
     if (!alone && !last_to_arrive(a.ctr, gridDim.x)) return;
     sphi[tid] = phi0;
@@ -742,10 +743,11 @@ __global__ __launch_bounds__(NW * 64, 2) void k_dec_proj(DecArgs a)
     proj_tiles<WF, RPE, NT, NW, GATEUP>(a, n_act, sh);
 }
 
-// Gate/up that routes for itself: every workgroup does the whole routing, and
-// the first writes it down. For few tokens and experts, where that takes less
-// than a launch of its own (dec_self_routes).
-template <int WF, int RPE>
+// Gate/up that sorts the routes by slot for itself: every workgroup does it, and
+// the first writes it down for down. ROUTE: and does all of the routing before,
+// for few tokens and experts, where that takes less than a launch of its own
+// (dec_self_routes); otherwise the route launch has left the ids.
+template <int WF, int RPE, bool ROUTE>
 __global__ __launch_bounds__(256, 2) void k_dec_route_proj(DecArgs a, DecRouteArgs q, PhiArg phi)
 {
     constexpr int NT = 4, NW = 4;
@@ -753,14 +755,18 @@ __global__ __launch_bounds__(256, 2) void k_dec_route_proj(DecArgs a, DecRouteAr
     struct Scratch {   // in the place of the sums, which come later
         float part[4][64], logit[4][64];
         uint64_t keys[4][66];
-        int32_t cnt[kMaxExp], off[kMaxExp], wsum[8], idx[kDecSelfRoutes];
+        int32_t cnt[kMaxExp], off[kMaxExp], wsum[8], phi[kMaxExp], idx[ROUTE ? kDecSelfRoutes : kDecMaxRoutes];
     };
     __shared__ ProjShared<WF, RPE, NT, NW> sh;
     static_assert(sizeof(Scratch) <= sizeof(sh.red), "scratch");
     Scratch &c = *(Scratch *)&sh.red;
     const int tid = threadIdx.x, wave = tid >> 6, kp = a.kp;
     const bool writes = blockIdx.x == 0;
-    for (int t = wave; t < a.T; t += NW) {
+    // asked for before anything waits: kernel arguments come from far away
+    const int32_t phi0 = phi.v[tid], phi1 = phi.v[tid + 256];
+    if (!ROUTE)
+        for (int i = tid; i < a.R; i += 256) c.idx[i] = q.idx[i];
+    for (int t = wave; ROUTE && t < a.T; t += NW) {
         if (q.Wr)
             for (int e0 = 0; e0 < q.E; e0 += 4)
                 wave_logits<TX, 8>(q, t, e0, c.part[wave], [&](int e, float l) { c.logit[wave][e] = l; });
@@ -773,9 +779,11 @@ __global__ __launch_bounds__(256, 2) void k_dec_route_proj(DecArgs a, DecRouteAr
                          }
                      });
     }
+    c.phi[tid] = phi0;
+    c.phi[tid + 256] = phi1;
     __syncthreads();
-    const int n_lists = build_lists<kDecSelfRoutes / 256>(
-        a.R, q.rpe, c.cnt, c.off, c.wsum, [&](int i) { return phi.v[c.idx[i]]; },
+    const int n_lists = build_lists<(ROUTE ? kDecSelfRoutes : kDecMaxRoutes) / 256>(
+        a.R, q.rpe, c.cnt, c.off, c.wsum, [&](int i) { return c.phi[c.idx[i]]; },
         [&](int n, int slot, int o, int k) {
             sh.slot[n] = slot;
             sh.off[n] = o;
@@ -845,25 +853,41 @@ bool dec_self_routes(const moe_shape &s, bool router)
     return !router || (s.d <= 1024 && ((s.T + 3) / 4) * ((s.E + 3) / 4) <= 2);
 }
 
-template <int WF>
+// Sorting the routes within the gate/up launch, after a route launch of several
+// token blocks: that one then has one hand-over less (64 experts of 2048 x 1024, top-8,
+// MXFP4, 16 tokens: 65.5 -> 64.3 us; small layers of 8 to 50 tokens 2 - 4 %). With
+// one block it sorts its own routes at once.
+bool dec_gate_up_sorts(const moe_shape &s, bool router)
+{
+    return !dec_self_routes(s, router) && s.T > kDecTokBlock && dec_rpe(s) <= 16;
+}
+
+template <int WF, bool ROUTE>
 static hipError_t launch_route_proj_t(DecArgs a, const DecRouteArgs &q, const PhiArg &phi, hipStream_t st)
 {
     a.nchunk = (a.N + 63) / 64;
     const unsigned grid = (unsigned)std::min<int64_t>(kDecGrid * 2, (int64_t)a.entries * a.nchunk);
     if (a.rpe == 5)
-        hipLaunchKernelGGL((k_dec_route_proj<WF, 5>), dim3(grid), dim3(256), 0, st, a, q, phi);
+        hipLaunchKernelGGL((k_dec_route_proj<WF, 5, ROUTE>), dim3(grid), dim3(256), 0, st, a, q, phi);
     else
-        hipLaunchKernelGGL((k_dec_route_proj<WF, 16>), dim3(grid), dim3(256), 0, st, a, q, phi);
+        hipLaunchKernelGGL((k_dec_route_proj<WF, 16, ROUTE>), dim3(grid), dim3(256), 0, st, a, q, phi);
     return hipGetLastError();
 }
 
-hipError_t launch_dec_route_proj(const moe_shape &s, const DecArgs &a, const DecRouteArgs &q, const PhiArg &phi,
+template <bool ROUTE>
+static hipError_t launch_route_proj_f(const moe_shape &s, const DecArgs &a, const DecRouteArgs &q, const PhiArg &phi,
+                                      hipStream_t st)
+{
+    if (s.dtype == MOE_DT_F32) return launch_route_proj_t<W_F32, ROUTE>(a, q, phi, st);
+    if (w_fp8(s)) return launch_route_proj_t<W_FP8, ROUTE>(a, q, phi, st);
+    if (w_fp4(s)) return launch_route_proj_t<W_FP4, ROUTE>(a, q, phi, st);
+    return launch_route_proj_t<W_BF16, ROUTE>(a, q, phi, st);
+}
+
+hipError_t launch_dec_route_proj(const moe_shape &s, const DecArgs &a, const DecRouteArgs &q, const PhiArg &phi, bool route,
                                  hipStream_t st)
 {
-    if (s.dtype == MOE_DT_F32) return launch_route_proj_t<W_F32>(a, q, phi, st);
-    if (w_fp8(s)) return launch_route_proj_t<W_FP8>(a, q, phi, st);
-    if (w_fp4(s)) return launch_route_proj_t<W_FP4>(a, q, phi, st);
-    return launch_route_proj_t<W_BF16>(a, q, phi, st);
+    return route ? launch_route_proj_f<true>(s, a, q, phi, st) : launch_route_proj_f<false>(s, a, q, phi, st);
 }
 
 hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const PhiArg &phi, hipStream_t st)

@@ -359,7 +359,7 @@ moe_status moe_layer_prefill_noalloc(const moe_shape *shape, const void *X,
  *   Y[t] += o_i over the token's routes i = t*K'..t*K'+K'-1, ascending,
  * in fp32: unlike the prompt layer's bf16 H, H is not rounded, so the outputs
  * of the two differ by that rounding. Each expert hit is read once (once for
- * every 5 to 64 of its routes, whichever suits the shape). Y is bitwise
+ * every 5 to 32 of its routes, whichever suits the shape). Y is bitwise
  * run-to-run identical and independent of phi and P.
  *   shape    T <= MOE_DECODE_MAX_T tokens, T * K' <= MOE_DECODE_MAX_ROUTES,
  *            d <= MOE_DECODE_MAX_D, a packed gate/up slice below 2 GiB

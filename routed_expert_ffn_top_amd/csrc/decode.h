@@ -8,7 +8,7 @@ namespace moe {
 constexpr int kDecMaxT = MOE_DECODE_MAX_T;             // a slot has at most this many rows
 constexpr int kDecMaxRoutes = MOE_DECODE_MAX_ROUTES;   // T * K'
 
-constexpr int kDecRows = 32;                           // fewest output columns per workgroup (one counter each)
+constexpr int kDecRows = 64;                           // output columns per workgroup (one counter each)
 constexpr int kDecMaxD = MOE_DECODE_MAX_D;
 constexpr int kDecTokBlock = 4;                        // tokens per route workgroup
 constexpr int kDecSelfRoutes = 256;                    // at most, where gate/up routes for itself
@@ -16,7 +16,7 @@ constexpr int kDecSelfRoutes = 256;                    // at most, where gate/up
 // The routes sorted by slot, at most rpe to an entry: entry a < *n_act is a slot
 // and up to rpe of its routes, rec[off .. off + cnt).
 constexpr int kDecMaxEntries = kMaxExp + kDecMaxRoutes / 5;
-int dec_rpe(const moe_shape &s);   // 5, 16, 32 or 64
+int dec_rpe(const moe_shape &s);   // 5, 16 or 32
 inline int dec_entries(const moe_shape &s)   // at most this many
 {
     const int R = s.T * (s.k + s.n_shared), ne = s.E + s.n_shared;

@@ -6,12 +6,11 @@
 //
 // With one to a few rows an expert, the layer's time is that of reading the
 // weights of the experts hit, once; every product is a matrix times at most 64
-// columns. A workgroup takes 64 rows (32 where 64 routes share a slot) of one
-// slot's weight slice over all of K and an entry's routes (dec_rpe: most slots'
-// routes are one entry), so that a weight is read by one workgroup only.
-// Its waves cut K among themselves (each its own stretch of the slice, whose
-// 64 rows of a K piece are contiguous in the tiled layout) and add their sums
-// in a fixed order through LDS.
+// columns. A workgroup takes 64 rows of one slot's weight slice over all of K
+// and an entry's routes (dec_rpe: most slots' routes are one entry), so that a
+// weight is read by one workgroup only. Its waves cut K among themselves (each its
+// own stretch of the slice, whose 64 rows of a K piece are contiguous in the tiled
+// layout) and add their sums in a fixed order through LDS.
 //
 // The weights are the first matrix operand (16 rows of the slice), the tokens
 // the second (16 of them), v_mfma_f32_16x16x32_bf16: lane l holds row l % 16
@@ -824,9 +823,7 @@ hipError_t launch_proj_t(const moe_shape &s, const DecArgs &a, hipStream_t st)
     switch (a.rpe) {
     case 5: return launch_proj_n<WF, 5, 4, 4, GATEUP>(s, a, st);
     case 16: return launch_proj_n<WF, 16, 4, 4, GATEUP>(s, a, st);
-    case 32: return launch_proj_n<WF, 32, 4, 8, GATEUP>(s, a, st);
-    // 64 routes in three terms each: 32 rows, or the sums do not fit the registers
-    default: return launch_proj_n<WF, 64, GATEUP ? 4 : 2, 8, GATEUP>(s, a, st);
+    default: return launch_proj_n<WF, 32, 4, 8, GATEUP>(s, a, st);
     }
 }
 
@@ -895,21 +892,26 @@ hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const Phi
     return act_bf16(s) ? launch_route_t<uint16_t>(a, phi, st) : launch_route_t<float>(a, phi, st);
 }
 
-// Routes per entry of the lists: the fewest of what the kernels are built for
-// that hold most slots' routes whole (7/4 of the mean of the experts hit). A
-// slot with more has several entries and its weights are read again for each;
-// a kernel for more routes has more sums, and with them fewer waves a compute
-// unit. Measured, us a layer with 5 / 16 / 32 / 64: 64 experts of 2048 x 1024, top-8,
-// MXFP4, 16 tokens 65 / 70 / 95 / 109; the same in bf16, 64 tokens 210 / 182 / 198 / 218;
-// 8 experts of 4096 x 14336, top-2, bf16, 32 tokens 888 / 504 / 521 / 573, 64 tokens
-// 1389 / 701 / 584 / 661.
+// Routes per entry of the lists: what holds most slots' routes whole (7/4 of the
+// mean of the experts hit), but more than 16 only for large experts. A slot with
+// more has several entries and its weights are read again for each (by then from
+// the L2 or the cache behind it); a kernel for more routes has more sums, and
+// with them fewer waves a compute unit, and fewer workgroups, each with a longer
+// chain of loads. Measured, us a layer with 5 / 16 / 32 / 64 (which none is built
+// for): 64 experts of 2048 x 1024, top-8, MXFP4, 16 tokens 65 / 70 / 95 / 109; the same
+// in bf16, 64 tokens 210 / 182 / 198 / 218; 8 experts of 4096 x 14336, top-2, bf16, 32
+// tokens 888 / 504 / 521 / 573, 64 tokens 1389 / 701 / 584 / 661; 3 + 2 experts of 512 x
+// 3392, top-1, fp8, 62 tokens 50 / 46 / 59 / 82; 7 + 1 of 3840 x 1280, top-6, bf16, 53
+// tokens 225 / 136 / 143 / 148; against it 9 + 1 of 1408 x 1856, top-5, bf16, 64 tokens
+// 176 / 119 / 104 / 104.
 int dec_rpe(const moe_shape &s)
 {
     double miss = 1.0;   // that a routed expert is hit by none of the tokens
     for (int t = 0; t < s.T; ++t) miss *= 1.0 - (double)s.k / s.E;
     const double mean = (double)s.T * s.k / (s.E * (1.0 - miss));
     const double want = std::min<double>(s.T, 1.75 * mean);
-    return want <= 5 ? 5 : want <= 16 ? 16 : want <= 32 ? 32 : 64;
+    const bool large = gu_slice_bytes(s) + d_slice_bytes(s) >= (size_t)64 << 20;
+    return want <= 5 ? 5 : want <= 16 || !large ? 16 : 32;
 }
 
 hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a, bool gateup, hipStream_t st)

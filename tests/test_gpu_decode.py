@@ -589,3 +589,19 @@ def test_decode_skewed_routing_within_gate_up(dtype):
         Y = A.clone()
         layer.decode(X, Y, logits=L)
         assert torch.equal(Y, first)
+
+
+@pytest.mark.parametrize("T", [19, 64])
+@pytest.mark.parametrize("dtype,d,f", [("bf16", 2048, 5632), ("f32", 2048, 2816), ("bf16_fp8w", 2048, 11264), ("bf16_fp4w", 4096, 10304)])
+def test_decode_large_experts_many_routes(dtype, d, f, T):
+    """Experts of more than 64 MB with many routes each: entries of 32 routes, one or two of them a slot."""
+    say(f"decode, experts of {d} x {f} {dtype}, T={T}")
+    cfg = MoEConfig(name="dec_large", index=83, T=4, d=d, f=f, E=2, k=1, dtype=dtype)
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    X, A = tokens(cfg, T)
+    L = torch.zeros(T, 2, device="cuda")
+    L[: T - 3, 1] = 1.0
+    Y = A.clone()
+    layer.decode(X, Y, logits=L)
+    check(inp, weights, X, A, Y, layer.decode_routes(T), f"T={T}")

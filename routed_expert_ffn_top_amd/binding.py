@@ -7,6 +7,7 @@ raises ``MoEError`` carrying the library's message.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -177,6 +178,22 @@ def _stream_of(t, s) -> Optional[int]:
         if s is None:
             return _raw_stream(here)
     return _stream(s)
+
+
+@contextlib.contextmanager
+def on_stream(stream):
+    """``stream`` (None: as it is) is torch's current stream within, behind what
+    the current one holds so far: temporaries of calls on a stream come from its
+    own pool, so that their memory is neither used by another stream's work
+    before nor given to it while these calls are queued."""
+    if stream is None:
+        yield
+        return
+    if isinstance(stream, int):   # a handle; 0 is the default stream's
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    stream.wait_stream(torch.cuda.current_stream(stream.device))
+    with torch.cuda.stream(stream):
+        yield
 
 
 def make_shape(T, d, f, E, k, n_shared=0, P=None, capacity=None, dtype="bf16", renorm=True,
@@ -507,26 +524,31 @@ class Arena:
         """Pack and publish every expert e with phi[e] >= 0 into slot phi[e].
         scales: (Sg, Su, Sd) row scales (fp8 codes) or block scales (MXFP4).
         An MXFP4 arena takes fp32 or bf16 weights too, without scales: they
-        are quantised on the way (moe_quantize_mxfp4)."""
+        are quantised on the way (moe_quantize_mxfp4). With a stream, the work
+        is queued there, behind the current stream's; the weights are the
+        caller's to keep until it is done."""
         quantise = self.shape.dtype == MOE_DT_BF16_FP4W and scales is None and Wg.dtype in _VAL_DTYPE
-        for e, s in enumerate(phi):
-            if s < 0:
-                continue
-            if quantise:
-                g, u, dn = (mxfp4_slice(W[e], stream) for W in (Wg, Wu, Wd))
-            else:
-                g, u, dn = expert_slices(Wg, Wu, Wd, scales, e)
-            moe_pack_gate_up(self.shape, g, u, self.plane_gu[s], 1, 0, 0, stream)
-            moe_pack_down(self.shape, dn, self.plane_d[s], 1, 0, 0, stream)
-            arena_publish_slot(self, s, e, stream)
+        with on_stream(stream):
+            for e, s in enumerate(phi):
+                if s < 0:
+                    continue
+                if quantise:
+                    g, u, dn = (mxfp4_slice(W[e]) for W in (Wg, Wu, Wd))
+                else:
+                    g, u, dn = expert_slices(Wg, Wu, Wd, scales, e)
+                moe_pack_gate_up(self.shape, g, u, self.plane_gu[s], 1, 0, 0)
+                moe_pack_down(self.shape, dn, self.plane_d[s], 1, 0, 0)
+                arena_publish_slot(self, s, e)
 
 
 def mxfp4_slice(W, stream=None) -> torch.Tensor:
     """W [N][K] (fp32 or bf16) as a source slice of the packing calls: MXFP4
-    codes [N][K/2], then scale bytes [N][K/32]."""
+    codes [N][K/2], then scale bytes [N][K/32]. With a stream, the slice
+    belongs to it: it is written, to be read and may be dropped there."""
     N, K = W.shape
-    out = torch.empty(N * K // 2 + N * K // 32, dtype=torch.uint8, device=W.device)
-    moe_quantize_mxfp4(W, out[: N * K // 2], out[N * K // 2:], stream)
+    with on_stream(stream):
+        out = torch.empty(N * K // 2 + N * K // 32, dtype=torch.uint8, device=W.device)
+        moe_quantize_mxfp4(W, out[: N * K // 2], out[N * K // 2:])
     return out
 
 

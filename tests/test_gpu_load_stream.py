@@ -7,6 +7,7 @@ import torch
 from gpu_util import gpu_inputs, say
 from routed_expert_ffn_top_amd import binding as B
 from routed_expert_ffn_top_amd.inputs import MoEConfig
+from routed_expert_ffn_top_amd.layer import MoELayer
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,18 @@ def test_slice_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     del junk
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "bf16_fp8w", "bf16_fp4w"])
+def test_paged_layer_set_up_on_another_stream(dtype):
+    """The host planes of a paged layer hold each expert's slices as they are
+    after its packing, also where that is queued on a busy stream."""
+    say(f"paged layer set up on a busy side stream, {dtype}")
+    inp = gpu_inputs(cfg_of(dtype).with_(P=4, G=2))
+    want = MoELayer(inp, paged=True)
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(PAUSE)
+    got = MoELayer(inp, paged=True, stream=st)
+    for a, b in ((want.host_gu_plane, got.host_gu_plane), (want.host_d_plane, got.host_d_plane)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))

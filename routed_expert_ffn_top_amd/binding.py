@@ -180,6 +180,21 @@ def _stream_of(t, s) -> Optional[int]:
     return _stream(s)
 
 
+def _stream_of_all(tensors, s) -> Optional[int]:
+    """_stream_of for work on several tensors (handles and None pass), which have
+    to be on one GPU."""
+    first = dev = None
+    for t in tensors:
+        get_device = getattr(t, "get_device", None)
+        if get_device is None:
+            continue
+        if first is None:
+            first, dev = t, get_device()
+        elif get_device() != dev:
+            raise ValueError("the operands must be on one device")
+    return _stream_of(first, s)
+
+
 @contextlib.contextmanager
 def on_stream(stream):
     """``stream`` (None: as it is) is torch's current stream within, behind what
@@ -293,14 +308,15 @@ def moe_decode_workspace_bytes(shape: moe_shape) -> int:
 
 def moe_decode_workspace_init(shape, ws, stream=None):
     _check(load().moe_decode_workspace_init(ctypes.byref(shape), _ptr(ws), ws.numel() * ws.element_size(),
-                                            _stream(stream)))
+                                            _stream_of_all((ws,), stream)))
 
 
 def moe_layer_decode(shape, X, W_r, bias, logits, Y, arena, routes: dict, ws, stream=None):
     rs = routes_struct(routes)
+    st = _stream_of_all((X, W_r, bias, logits, Y, ws, routes.get("topk_idx"), routes.get("topk_w"),
+                         getattr(arena, "plane_gu", None)), stream)
     _check(load().moe_layer_decode(ctypes.byref(shape), _ptr(X), _ptr(W_r), _ptr(bias), _ptr(logits), _ptr(Y),
-                                   arena.handle, ctypes.byref(rs), _ptr(ws), ws.numel() * ws.element_size(),
-                                   _stream_of(X, stream)))
+                                   arena.handle, ctypes.byref(rs), _ptr(ws), ws.numel() * ws.element_size(), st))
 
 
 _VAL_DTYPE = {torch.float32: MOE_DT_F32, torch.bfloat16: MOE_DT_BF16}
@@ -448,6 +464,11 @@ def check_rows(t: torch.Tensor, dtype, cols: int, name: str) -> None:
         raise ValueError(f"{name}: need a GPU matrix [rows][{cols}] of {dtype}")
     if cols > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < cols:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+
+
+def check_device(tensors, stream=None) -> None:
+    """The tensors and the stream are on the current GPU."""
+    _stream_of_all(tensors, stream)
 
 
 def alloc_routes(shape: moe_shape, device="cuda") -> dict:

@@ -85,3 +85,84 @@ def test_decode_needs_contiguous_rows():
         B.check_rows(x, torch.float32, 8, "X")          # not on the GPU
     assert B.row_stride(torch.zeros(4, 24)[:, :8]) == 24
     assert B.row_stride(torch.zeros(1, 8)) == 8
+
+
+class _On:
+    """A tensor of some device and address, as far as the binding looks."""
+
+    def __init__(self, device, addr=0x1000, n=1 << 30):
+        self.device, self.addr, self.n = device, addr, n
+
+    def get_device(self):
+        return self.device
+
+    def data_ptr(self):
+        return self.addr
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return 1
+
+
+def test_decode_operands_on_one_device(monkeypatch):
+    """Every operand, not X alone: a kernel of one GPU would follow the pointer
+    into another's memory, or the host's."""
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: calls.append((name, a)) or B.MOE_OK
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(B, "_raw_stream", lambda device: 100 + device)
+    monkeypatch.setattr(B, "load", lambda: Lib())
+    s = _shape()
+    arena = _Arena(0x5000)
+    arena.plane_gu = arena.plane_d = _On(1)
+    base = dict(X=_On(1), W_r=_On(1), bias=_On(1), logits=_On(1), Y=_On(1), ws=_On(1), idx=_On(1), w=_On(1), arena=arena)
+
+    def call(**kw):
+        a = dict(base, **kw)
+        B.moe_layer_decode(s, a["X"], a["W_r"], a["bias"], a["logits"], a["Y"], a["arena"],
+                           dict(topk_idx=a["idx"], topk_w=a["w"]), a["ws"])
+    call()
+    call(bias=None, logits=None)
+    assert [c[0] for c in calls] == ["moe_layer_decode"] * 2 and calls[0][1][-1] == 101
+    other = _Arena(0x5000)
+    other.plane_gu = other.plane_d = _On(0)
+    for dev in (0, -1):
+        for name in ("X", "W_r", "bias", "logits", "Y", "ws", "idx", "w"):
+            with pytest.raises(ValueError):
+                call(**{name: _On(dev)})
+        with pytest.raises(ValueError):
+            B.moe_decode_workspace_init(s, _On(dev))
+    with pytest.raises(ValueError):
+        call(arena=other)
+    B.moe_decode_workspace_init(s, _On(1))
+    with pytest.raises(ValueError):       # all of them on a GPU that is not the current one
+        call(**{k: _On(0) for k in base if k != "arena"}, arena=other)
+    assert len(calls) == 3
+
+
+def test_layer_operands_on_the_layers_device(monkeypatch):
+    """forward_mxfp4 looks before its first launch, which is the router's."""
+    from routed_expert_ffn_top_amd.inputs import MoEConfig
+    from routed_expert_ffn_top_amd.layer import MoELayer
+    layer = MoELayer.__new__(MoELayer)
+    layer.cfg = MoEConfig(name="on_device", index=85, T=4, d=128, f=64, E=8, k=2, dtype="bf16_fp4w")
+    layer.shape, layer.paged, layer.X = _shape(dtype="bf16_fp4w"), False, _On(1)
+    launched = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(B, "_raw_stream", lambda device: 100 + device)
+    monkeypatch.setattr(B, "check_rows", lambda *a: None)
+    for f in ("moe_router_logits", "moe_quantize_mxfp4"):
+        monkeypatch.setattr(B, f, lambda *a: launched.append(a))
+    layer._xq, layer._logits = torch.zeros(1), None
+    with pytest.raises(ValueError):
+        layer.forward_mxfp4(torch.zeros(4, 128))       # in host memory
+    layer.X = _On(0)
+    with pytest.raises(ValueError):
+        layer.forward_mxfp4(torch.zeros(4, 128))
+    assert not launched

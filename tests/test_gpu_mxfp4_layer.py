@@ -20,7 +20,7 @@ import torch
 from gpu_util import OracleRun, gpu_inputs, say
 from oracle import oracle as oracle_mod
 from routed_expert_ffn_top_amd import binding as B
-from routed_expert_ffn_top_amd.inputs import MoEConfig
+from routed_expert_ffn_top_amd.inputs import MoEConfig, quantize_mxfp4
 from routed_expert_ffn_top_amd.layer import MoELayer
 from test_gpu_mxfp4 import MAG, U, gamma, quantise, two_to, values
 
@@ -213,3 +213,43 @@ def test_refusals():
         MoELayer(bf).forward_mxfp4(bf.A)
     with pytest.raises(ValueError):
         MoELayer(inp, capacity=2).forward_mxfp4(inp.A)
+
+
+def test_far_negative_gates():
+    """SiLU(g) u where exp(-g) leaves fp32's range and the product does not: g of
+    -86 to -92 with u of 2^116 to 2^126, and -104 with 2^126. g and u are exact
+    here, and Y is H as it is stored: each value is (16 + 2 |g|) u off before, far
+    from the borders between codes (asserted), so that Y is known to the bit."""
+    say("MXFP4 activations: gates far below zero, large up values")
+    cfg = cfg_of(3, 64, 64, 1, 1)
+    inp = gpu_inputs(cfg)
+    near = [-86, -87, -88, -88.5, -89, -89.5, -90, -90.5, -91, -91.5, -92, 1, -2, 0, 3, -40]
+    g = torch.tensor(near + near + [-104.0] * 32, dtype=torch.float64)
+    silu = g * torch.exp(g) / (1 + torch.exp(g))
+    n = torch.where(g == -104, 126, torch.where(silu == 0, 1, (1 - torch.frexp(silu)[1])))
+    n[16:32] += 1                                  # other values of a block, up to two powers of two below its top
+    n = n.clamp(max=126)
+    Wg, Wu, Wd, X = torch.zeros(64, 64), torch.zeros(64, 64), torch.eye(64), torch.zeros(3, 64)
+    for j in range(64):                            # 32 ones times codes that add up to g
+        rest, c = abs(float(g[j])), 0
+        while rest > 0:
+            v = max(m for m in (0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0) if m <= rest)
+            Wg[j, c], rest, c = (v if g[j] > 0 else -v), rest - v, c + 1
+        Wu[j, 32] = 2.0 ** int(n[j] - 63)
+    X[:, :32], X[:, 32] = 1.0, 2.0 ** 63
+    quant = lambda W: tuple(t.cuda()[None] for t in quantize_mxfp4(W))
+    (inp.Wg, inp.Sg), (inp.Wu, inp.Su), (inp.Wd, inp.Sd) = quant(Wg), quant(Wu), quant(Wd)
+    inp.X, inp.A = X.to(torch.bfloat16).cuda(), torch.zeros(3, 64, device="cuda")
+    h = (silu * two_to(n.int())).reshape(2, 32)
+    byte = scale_of(h.abs().amax(-1))
+    want = stored_at(h, byte)
+    off = (16 + 2 * g.abs().reshape(2, 32)) * U
+    for s in (1 - off, 1 + off):
+        assert torch.equal(stored_at(h * s, byte), want) and torch.equal(scale_of((h * s).abs().amax(-1)), byte)
+    assert int((want[0] != 0).sum()) >= 24 and bool((want[1] != 0).all())
+    layer = MoELayer(inp)
+    Y = inp.A.clone()
+    layer.forward_mxfp4(Y)
+    torch.cuda.synchronize()
+    t, j = (Y.double().cpu() != want.reshape(64)).nonzero(as_tuple=True)
+    assert not len(j), f"g = {sorted(set(g[j].tolist()))}"

@@ -373,6 +373,17 @@ __device__ __forceinline__ bf16x8_t fp4_operand(uint32_t w, float scale)
     return __builtin_bit_cast(bf16x8_t, u);
 }
 
+// SiLU(g) u. Below -88, where exp(-g) leaves the range: 1 + exp(-g) is exp(-g) there, and
+// exp(g) is taken in two halves, u between them, that stay normal numbers (down to g = -174).
+__device__ __forceinline__ float silu_mul(float g, float u)
+{
+    if (g < -88.0f) {
+        const float e = expf(0.5f * g);
+        return g * e * u * e;
+    }
+    return g / (1.0f + expf(-g)) * u;
+}
+
 constexpr uint32_t kNowhere = 0x80000000u;   // a buffer offset past every slice: such a load gives zeros and reads nothing
 
 // Workgroup barrier that waits for this wave's LDS traffic only: loads in
@@ -664,7 +675,7 @@ __device__ __forceinline__ void proj_tiles(const DecArgs &a, const int n_act, Pr
                 const int64_t at = (int64_t)route * a.ldo + chunk * 32 + rn;
                 float v[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) v[c] = g[c] / (1.0f + expf(-g[c])) * u[c];
+                for (int c = 0; c < 4; ++c) v[c] = silu_mul(g[c], u[c]);
                 if constexpr (WF == W_F32) {
                     *(float4 *)((float *)a.out + at) = make_float4(v[0], v[1], v[2], v[3]);
                 } else {

@@ -605,3 +605,47 @@ def test_decode_large_experts_many_routes(dtype, d, f, T):
     Y = A.clone()
     layer.decode(X, Y, logits=L)
     check(inp, weights, X, A, Y, layer.decode_routes(T), f"T={T}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_decode_far_negative_gates(dtype):
+    """SiLU(g) u where exp(-g) leaves fp32's range and the product does not. g, u
+    and W_d H are exact (one term each, or 32 whose sums are), so Y is H, off by
+    the roundings of SiLU(g) u alone: exp of g / 2 within 1 ulp (2u) in each of two
+    factors and three products (u each), or exp, 1 +, a division and a product:
+    8u in either form, and one more for alpha = 1 times it."""
+    say(f"decode: gates far below zero, large up values, {dtype}")
+    cfg = MoEConfig(name="dec_far", index=86, T=4, d=64, f=64, E=1, k=1, dtype=dtype)
+    inp = gpu_inputs(cfg)
+    g = torch.tensor([-80, -86, -87, -87.5, -88, -88.5, -89, -89.5, -90, -91, -92, -96, -100, -104, -120, -150] * 4,
+                     dtype=torch.float64)
+    silu = g * torch.exp(g) / (1 + torch.exp(g))
+    n = (-torch.frexp(silu)[1]).clamp(max=126)     # u = 2^n: H near 1, or as near as fp32 allows
+    Wg, Wu, Wd, X = torch.zeros(64, 64), torch.zeros(64, 64), torch.eye(64), torch.zeros(3, 64)
+    for j in range(64):
+        rest, c = abs(float(g[j])), 0
+        while rest > 0:
+            v = max(m for m in (0.5, 1.0, 2.0, 4.0, 6.0) if m <= rest)
+            Wg[j, c], rest, c = -v, rest - v, c + 1
+        Wu[j, 32] = 2.0 ** int(n[j] - 63)
+    X[:, :32], X[:, 32] = 1.0, 2.0 ** 63
+    if cfg.fp8_weights:
+        q8 = lambda W: W.to(torch.float8_e4m3fn).view(torch.uint8).cuda()[None]
+        one = torch.ones(1, 64, device="cuda")
+        inp.Wg, inp.Sg, inp.Wd, inp.Sd = q8(Wg), one, q8(Wd), one.clone()
+        inp.Wu, inp.Su = q8((Wu > 0).float()), Wu.sum(-1).cuda()[None]
+    elif cfg.fp4_weights:
+        from routed_expert_ffn_top_amd.inputs import quantize_mxfp4
+        (inp.Wg, inp.Sg), (inp.Wu, inp.Su), (inp.Wd, inp.Sd) = (tuple(t.cuda()[None] for t in quantize_mxfp4(W))
+                                                                for W in (Wg, Wu, Wd))
+    else:
+        inp.Wg, inp.Wu, inp.Wd = (W.to(cfg.torch_dtype).cuda()[None] for W in (Wg, Wu, Wd))
+    layer = MoELayer(inp)
+    for logits in (torch.zeros(3, 1, device="cuda"), None):
+        Y = torch.zeros(3, 64, device="cuda")
+        layer.decode(X.to(cfg.torch_dtype).cuda(), Y, logits=logits)
+        torch.cuda.synchronize()
+        want = (silu * torch.pow(2.0, n.double())).expand(3, 64)
+        off = (Y.cpu().double() - want).abs() / want.abs()
+        say(f"  largest error {float(off.max() / U):.3g} u")
+        assert bool((off <= 9 * U).all()), f"g = {sorted(set(g.expand(3, 64)[off > 9 * U].tolist()))}"

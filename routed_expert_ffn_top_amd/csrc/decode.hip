@@ -818,7 +818,7 @@ __global__ __launch_bounds__(256, 2) void k_dec_route_proj(DecArgs a, DecRouteAr
 constexpr int kDecGrid = 512;
 
 template <int WF, int RPE, int NT, int NW, bool GATEUP>
-hipError_t launch_proj_n(const moe_shape &s, DecArgs a, hipStream_t st)
+hipError_t launch_proj_n(DecArgs a, hipStream_t st)
 {
     a.nchunk = (a.N + 16 * NT - 1) / (16 * NT);
     const int64_t most = kDecGrid * 8 / NW, tiles = (int64_t)a.entries * a.nchunk;
@@ -828,14 +828,16 @@ hipError_t launch_proj_n(const moe_shape &s, DecArgs a, hipStream_t st)
     return hipGetLastError();
 }
 
+// Gate/up with entries of 16 sorts the routes for itself (dec_gate_up_sorts: more than
+// 4 tokens, or the entries were of 5) and is launch_route_proj_t's.
 template <int WF, bool GATEUP>
-hipError_t launch_proj_t(const moe_shape &s, const DecArgs &a, hipStream_t st)
+hipError_t launch_proj_t(const DecArgs &a, hipStream_t st)
 {
-    switch (a.rpe) {
-    case 5: return launch_proj_n<WF, 5, 4, 4, GATEUP>(s, a, st);
-    case 16: return launch_proj_n<WF, 16, 4, 4, GATEUP>(s, a, st);
-    default: return launch_proj_n<WF, 32, 4, 8, GATEUP>(s, a, st);
-    }
+    if (a.rpe == 5) return launch_proj_n<WF, 5, 4, 4, GATEUP>(a, st);
+    if constexpr (!GATEUP)
+        if (a.rpe == 16) return launch_proj_n<WF, 16, 4, 4, GATEUP>(a, st);
+    if (a.rpe == 32) return launch_proj_n<WF, 32, 4, 8, GATEUP>(a, st);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -877,8 +879,10 @@ static hipError_t launch_route_proj_t(DecArgs a, const DecRouteArgs &q, const Ph
     const unsigned grid = (unsigned)std::min<int64_t>(kDecGrid * 2, (int64_t)a.entries * a.nchunk);
     if (a.rpe == 5)
         hipLaunchKernelGGL((k_dec_route_proj<WF, 5, ROUTE>), dim3(grid), dim3(256), 0, st, a, q, phi);
-    else
+    else if (a.rpe == 16)
         hipLaunchKernelGGL((k_dec_route_proj<WF, 16, ROUTE>), dim3(grid), dim3(256), 0, st, a, q, phi);
+    else
+        return hipErrorInvalidValue;
     return hipGetLastError();
 }
 
@@ -928,15 +932,15 @@ int dec_rpe(const moe_shape &s)
 hipError_t launch_dec_proj(const moe_shape &s, const DecArgs &a, bool gateup, hipStream_t st)
 {
     if (gateup) {
-        if (s.dtype == MOE_DT_F32) return launch_proj_t<W_F32, true>(s, a, st);
-        if (w_fp8(s)) return launch_proj_t<W_FP8, true>(s, a, st);
-        if (w_fp4(s)) return launch_proj_t<W_FP4, true>(s, a, st);
-        return launch_proj_t<W_BF16, true>(s, a, st);
+        if (s.dtype == MOE_DT_F32) return launch_proj_t<W_F32, true>(a, st);
+        if (w_fp8(s)) return launch_proj_t<W_FP8, true>(a, st);
+        if (w_fp4(s)) return launch_proj_t<W_FP4, true>(a, st);
+        return launch_proj_t<W_BF16, true>(a, st);
     }
-    if (s.dtype == MOE_DT_F32) return launch_proj_t<W_F32, false>(s, a, st);
-    if (w_fp8(s)) return launch_proj_t<W_FP8, false>(s, a, st);
-    if (w_fp4(s)) return launch_proj_t<W_FP4, false>(s, a, st);
-    return launch_proj_t<W_BF16, false>(s, a, st);
+    if (s.dtype == MOE_DT_F32) return launch_proj_t<W_F32, false>(a, st);
+    if (w_fp8(s)) return launch_proj_t<W_FP8, false>(a, st);
+    if (w_fp4(s)) return launch_proj_t<W_FP4, false>(a, st);
+    return launch_proj_t<W_BF16, false>(a, st);
 }
 
 }  // namespace moe

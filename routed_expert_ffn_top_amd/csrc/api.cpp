@@ -896,7 +896,6 @@ moe_status decode_impl(const moe_shape &s, const DecLayout &w, const void *X, co
     q.k = s.k;
     q.n_shared = s.n_shared;
     q.renorm = s.renorm;
-    q.P = s.P;
     q.rpe = dec_rpe(s);
     q.idx = r.topk_idx;
     q.w = r.topk_w;

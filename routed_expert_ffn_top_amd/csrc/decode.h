@@ -79,7 +79,7 @@ struct DecRouteArgs {
     const float *Wr, *bias;   // Wr null: logits holds the caller's
     const float *given;
     float *logits;
-    int T, d, E, k, n_shared, renorm, P, rpe;
+    int T, d, E, k, n_shared, renorm, rpe;
     int sort;                 // the route launch sorts the routes by slot too
     int32_t *idx;
     float *w;

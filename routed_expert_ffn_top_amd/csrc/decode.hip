@@ -513,7 +513,7 @@ __device__ __forceinline__ void proj_tiles(const DecArgs &a, const int n_act, Pr
                 if constexpr (WF == W_F32) {
                     // K pieces of the last columns are narrower, and N may end inside the tile
                     const int piece = k / kWK, wd = min(kWK, K - piece * kWK);
-                    const int rb = min((int)p.at / 1 + 16 * t, p.rows - 1);
+                    const int rb = min((int)p.at + 16 * t, p.rows - 1);
                     at = (uint32_t)(p.nb * kWRows * K + piece * p.rows * kWK + rb * wd + k % kWK) * 4;
                 } else {
                     at = p.at + (uint32_t)(s + u) * p.stride + t * 16 * ROWB;

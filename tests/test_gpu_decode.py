@@ -649,3 +649,82 @@ def test_decode_far_negative_gates(dtype):
         off = (Y.cpu().double() - want).abs() / want.abs()
         say(f"  largest error {float(off.max() / U):.3g} u")
         assert bool((off <= 9 * U).all()), f"g = {sorted(set(g.expand(3, 64)[off > 9 * U].tolist()))}"
+
+
+def integer_layer(cfg, at):
+    """A layer whose every step is exact in fp32, for tokens that are zero but at
+    the hidden indices `at`: g in [64, 1536], so SiLU(g) = g, |h| < 2^21, and two
+    units an output. Returns (layer, Wg, Wu [E][f][len(at)], Wd [E][d][f])."""
+    inp = gpu_inputs(cfg)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    E, d, f = cfg.E, cfg.d, cfg.f
+    W = torch.zeros(2, E, f, d, device="cuda")
+    some = torch.randint(1, 7, (2, E, f, len(at)), generator=gen, device="cuda").float()
+    some[some == 5] = 4.0
+    some[1] *= torch.where(torch.rand(some[1].shape, generator=gen, device="cuda") < 0.5, -1.0, 1.0)
+    W[..., at] = some
+    Wd = torch.zeros(E, d, f, device="cuda")
+    n = torch.arange(d, device="cuda")
+    for e in range(E):
+        Wd[e, n, n % f], Wd[e, n, (n * 5 + 3 + e) % f] = 1.0, -1.0
+    if cfg.fp4_weights:
+        table = torch.zeros(7, dtype=torch.uint8, device="cuda")
+        for v, c in {1: 2, 2: 4, 3: 5, 4: 6, 6: 7}.items():
+            table[v] = c
+        enc = lambda w: (table[w.abs().long()] | ((w < 0).to(torch.uint8) << 3))
+        pack = lambda w: (enc(w)[..., 0::2] | enc(w)[..., 1::2] << 4).contiguous()
+        inp.Wg, inp.Wu, inp.Wd = pack(W[0]), pack(W[1]), pack(Wd)
+        for s in (inp.Sg, inp.Su, inp.Sd):
+            s.fill_(127)
+    elif cfg.fp8_weights:
+        inp.Wg, inp.Wu, inp.Wd = (w.to(torch.float8_e4m3fn).view(torch.uint8) for w in (W[0], W[1], Wd))
+        for s in (inp.Sg, inp.Su, inp.Sd):
+            s.fill_(1.0)
+    else:
+        inp.Wg, inp.Wu, inp.Wd = (w.to(cfg.torch_dtype) for w in (W[0], W[1], Wd))
+    return MoELayer(inp), some[0].double(), some[1].double(), Wd
+
+
+@pytest.mark.parametrize("d,f,dtype", [(131072, 64, "bf16"), (131072, 64, "f32"), (131072, 64, "bf16_fp8w"),
+                                       (131072, 64, "bf16_fp4w"), (65600, 64, "bf16"), (49152, 256, "bf16"),
+                                       (49156, 224, "f32")])
+def test_decode_widest_layers(d, f, dtype):
+    """More chunks of output columns than workgroups, to the last counter: a
+    workgroup of down takes several chunks, and is the only arrival at each.
+    Up to 16 routes an entry and, for experts of 64 MB and more, 32."""
+    say(f"decode, d={d} f={f} {dtype}")
+    cfg = MoEConfig(name="dec_widest", index=87, T=4, d=d, f=f, E=2, k=1, dtype=dtype)
+    at = sorted({0, 31, 32, 127, 128, d // 2, d - 129, d - 64, d - 1} | set(range(7, d, d // 55)))[:64]
+    layer, Wg, Wu, Wd = integer_layer(cfg, at)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for T in (1, 5, 45):
+        X = torch.zeros(T, d, device="cuda")
+        x = torch.randint(1, 5, (T, len(at)), generator=gen, device="cuda").float()
+        X[:, at] = x
+        X = X.to(cfg.torch_dtype)
+        L = torch.zeros(T, 2, device="cuda")
+        L[1::2, 1] = 1.0
+        for logits in (L, None):
+            Y = torch.zeros(T, d, device="cuda")
+            layer.decode(X, Y, logits=logits)
+            torch.cuda.synchronize()
+            r = layer.decode_routes(T)
+            e = r["topk_idx"][:, 0].long()
+            if logits is not None:
+                assert torch.equal(e, L.argmax(-1))
+            g = (Wg[e] * x.double()[:, None]).sum(-1)
+            h = g * (Wu[e] * x.double()[:, None]).sum(-1)
+            assert float(g.min()) > 40 and float(h.abs().max()) < 2 ** 22
+            # column n holds W_d's two entries: +1 at n % f, -1 beside it (or 0, where both fall on one unit)
+            n = torch.arange(d, device="cuda")
+            for t in range(T):
+                w = Wd[e[t]]
+                ref = h[t, (n * 5 + 3 + e[t]) % f] * w[n, (n * 5 + 3 + e[t]) % f].double()
+                two = (n % f) != (n * 5 + 3 + e[t]) % f
+                ref = ref + torch.where(two, h[t, n % f] * w[n, n % f].double(), 0.0)
+                assert torch.equal(Y[t].double(), ref), f"T={T} token {t}"
+            for _ in range(2):      # the counters are clear again
+                Z = torch.zeros(T, d, device="cuda")
+                layer.decode(X, Z, logits=logits)
+                torch.cuda.synchronize()
+                assert torch.equal(Z, Y)

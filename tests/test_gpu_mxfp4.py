@@ -515,3 +515,57 @@ def with_nan(w, n, k):
     w = w.clone()
     w[n, k] = float("nan")
     return B.mxfp4_slice(w)
+
+
+# ---- ring workgroups with several tiles each ----
+
+def ring_tiles(sizes, N):
+    """Tiles of 256 x 256; 256 workgroups take them, so more than 768 are four for some and three for all others."""
+    return sum((n + 255) // 256 for n in sizes) * ((N + 255) // 256)
+
+
+def ring_pieces(sizes, tail, N):
+    """What the choice between the two kernels looks at: 32 x 64 pieces at the mean rows a slot."""
+    M = sum(sizes) + tail
+    slots = min(len(sizes), M)
+    return slots * ((M // slots + 31) // 32) * (N // 64)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [64, 128, 192, 448, 512, 640])
+def test_matmul_several_tiles_a_workgroup(K, dtype, gather):
+    """A tile requested while the one before it is stored: its rows, scales and
+    shifts stand beside the old ones. Partial and empty slots, columns past N."""
+    sizes, tail, N = [0, 5000, 0, 257, 1, 9000, 256, 0, 3000, 255, 4000, 7], 77, 2112
+    say(f"matmul, {ring_tiles(sizes, N)} tiles, K={K}, {dtype}, gather {gather}")
+    assert ring_tiles(sizes, N) > 768 and ring_pieces(sizes, tail, N) >= 768
+    run_matmul(sum(sizes) + tail, N, K, len(sizes), sizes, gather, dtype, tail=tail, scale_spread=5)
+
+
+@pytest.mark.parametrize("K,off", [(64, 2), (128, 2), (320, 6)])
+def test_matmul_several_tiles_unaligned_scales(K, off):
+    say(f"matmul, several tiles a workgroup, scales {off} bytes from a 16-byte address, K={K}")
+    M, N = 24001, 2240
+    assert ring_tiles([M], N) > 768
+    gen = torch.Generator(device="cuda").manual_seed(off + K)
+    x = torch.empty((8000, K), device="cuda").normal_(generator=gen)
+    packed, W = pack(torch.empty((1, N, K), device="cuda").normal_(generator=gen))
+    c, s = quantise(x)
+    buf = torch.full((off + s.numel(),), 255, dtype=torch.uint8, device="cuda")
+    t = buf[off:].view(s.shape)
+    t.copy_(s)
+    rec = torch.randint(8000, (M,), generator=gen, device="cuda", dtype=torch.int32)
+    C = torch.empty(M, N, device="cuda")
+    B.moe_matmul_mxfp4(c, t, packed[0], C, row_index=rec)
+    torch.cuda.synchronize()
+    ref, mag = product(values(c, s).cuda(), W, [0, M], rec.long())
+    assert bool(((C.double() - ref).abs() <= gamma(2 * K) * mag).all())
+
+
+@pytest.mark.parametrize("gather", [False, True])
+def test_matmul_large_groups_uneven(gather):
+    say(f"matmul, large, uneven groups with an empty one, gather {gather}")
+    sizes, tail, N, K = [128, 129, 0, 256, 700], 5, 1280, 1024
+    assert ring_pieces(sizes, tail, N) >= 768
+    run_matmul(sum(sizes) + tail, N, K, len(sizes), sizes, gather, torch.float32, tail=tail, scale_spread=6)

@@ -253,3 +253,127 @@ def test_far_negative_gates():
     torch.cuda.synchronize()
     t, j = (Y.double().cpu() != want.reshape(64)).nonzero(as_tuple=True)
     assert not len(j), f"g = {sorted(set(g[j].tolist()))}"
+
+
+# ---- inputs whose g and u are exact: a bound close enough to tell a wrong tile ----
+
+def exact_inputs(cfg, seed=1):
+    """Layer inputs whose blocks all have one scale: X's values are E2M1's, each block's
+    largest 4 or 6, and the weights' codes any, times 2^-7. Products are at most 144
+    units of 2^-9, and d of them less than 2^24 units, so that every partial sum of g
+    and u is an fp32 number, whatever the order."""
+    assert cfg.d * 36 * 4 < 2 ** 24
+    inp = gpu_inputs(cfg)
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    mag = MAG.float().cuda()
+    pick = torch.randint(8, (cfg.T, cfg.d), generator=gen, device="cuda")
+    pick[:, ::32] = 6 + pick[:, ::32] % 2
+    sign = torch.randint(2, (cfg.T, cfg.d), generator=gen, device="cuda") * 2 - 1
+    inp.X = (mag[pick] * sign).to(torch.bfloat16)
+    for q in (inp.Wg, inp.Wu, inp.Wd):
+        q.random_(0, 256, generator=gen)
+    for s in (inp.Sg, inp.Su, inp.Sd):
+        s.fill_(120)
+    return inp
+
+
+def reference_of_exact(inp, idx, alpha):
+    """(Y, bound) as in `reference`, where g and u are exact: h is off by SiLU's and
+    the product's roundings alone, (16 + 2 |g|) u |h| (and 2^-120, for the range that
+    these g do not reach)."""
+    c = inp.cfg
+    X = values(*quantise(inp.X))
+    orc = oracle_mod.get()
+    dec = lambda q, s: torch.from_numpy(orc.mxfp4_decode(q.cpu().numpy(), s.cpu().numpy())).double()
+    Wg, Wu, Wd = dec(inp.Wg, inp.Sg), dec(inp.Wu, inp.Su), dec(inp.Wd, inp.Sd)
+    Y = inp.A.double().cpu().clone()
+    mag, bound = Y.abs(), torch.zeros_like(Y)
+    for e in range(Wg.shape[0]):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        if not len(t):
+            continue
+        al = alpha[t, j][:, None]
+        g, u = X[t] @ Wg[e].t(), X[t] @ Wu[e].t()
+        h = (g * torch.sigmoid(g) * u).reshape(len(t), -1, 32)
+        err = (16 + 2 * g.abs().reshape(h.shape)) * U * h.abs() + 2.0 ** -120
+        H = stored_at(h, scale_of(h.abs().amax(-1)))
+        reach = torch.zeros_like(H)
+        for byte in (scale_of((h.abs() - err).amax(-1).clamp(min=0)), scale_of((h.abs() + err).amax(-1))):
+            for end in (h - err, h + err):
+                reach = torch.maximum(reach, (stored_at(end, byte) - H).abs())
+        H, reach = H.reshape(g.shape), reach.reshape(g.shape)
+        wd = Wd[e].abs().t()
+        o, m = al * (H @ Wd[e].t()), al * ((H.abs() + reach) @ wd)
+        Y.index_put_((t,), o, accumulate=True)
+        mag.index_put_((t,), m, accumulate=True)
+        bound.index_put_((t,), al * (reach @ wd) + gamma(2 * c.f) * m, accumulate=True)
+    return Y, bound + gamma(c.kp + 2) * mag
+
+
+def check_of_exact(inp, Y, routes, at):
+    """The tokens `at` within the bound, which has to tell a wrong tile, whose error is
+    as large as the expert sums: it is below 1/20 of them. (Of f terms of either sign the
+    sum is about sqrt(f) and the magnitudes' sum 0.8 f times a term, so gamma(2f) alone is
+    0.8 sqrt(f) 2f u of the sum: 0.6 % for f = 1664, as much again for alpha's spread
+    over two routes and for values beside a border between codes.)"""
+    T = inp.cfg.T
+    idx, alpha = routes["topk_idx"].reshape(T, -1), routes["topk_w"].reshape(T, -1)
+    sub = type(inp)(**{**inp.__dict__, "X": inp.X[at].contiguous(), "A": inp.A[at]})
+    ref, bound = reference_of_exact(sub, idx[at].cpu().long(), alpha[at].cpu().double())
+    err = (Y[at].cpu().double() - ref).abs()
+    ffn = (ref - sub.A.cpu().double()).norm()
+    say(f"  max err/bound {float((err / bound).max()):.3g}; of the expert sums: error {float(err.norm() / ffn):.3g}, "
+        f"bound {float(bound.norm() / ffn):.3g}")
+    assert bool((err <= bound).all()) and float(bound.norm()) < 0.05 * float(ffn)
+
+
+@pytest.mark.parametrize("T,d,f,E,k,shared", [(1, 64, 64, 2, 1, 0), (90, 256, 128, 8, 2, 0), (33, 320, 448, 5, 3, 2),
+                                              (700, 576, 256, 4, 2, 1), (130, 1024, 1408, 8, 2, 0)])
+def test_exact_projections(T, d, f, E, k, shared):
+    say(f"MXFP4 activations, exact g and u: T={T} d={d} f={f} E={E} k={k} shared={shared}")
+    cfg = cfg_of(T, d, f, E, k, shared)
+    inp = exact_inputs(cfg)
+    layer = MoELayer(inp)
+    L = torch.empty((T, E), device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(T))
+    Y = inp.A.clone()
+    layer.forward_mxfp4(Y, logits=L)
+    torch.cuda.synchronize()
+    check_of_exact(inp, Y, layer.routes, torch.arange(T, device="cuda"))
+
+
+@pytest.mark.parametrize("d,f", [(3264, 1600), (3200, 1664)])
+def test_several_tiles_a_workgroup(d, f):
+    """Projections of more than 768 tiles, three or four for each of 256
+    workgroups: the same bits as in parts of less than 256 tiles, and within
+    the bound for tokens of every part."""
+    T, E = 8192, 6
+    say(f"MXFP4 activations: several tiles a workgroup, T={T} d={d} f={f}")
+    cfg = cfg_of(T, d, f, E, 2)
+    inp = exact_inputs(cfg)
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    L = torch.empty((T, E), device="cuda").normal_(generator=gen)
+    L[:, 2] -= 20.0                  # an expert without tokens
+    L[:, 4] += 1.5
+    layer = MoELayer(inp)
+    Y = inp.A.clone()
+    layer.forward_mxfp4(Y, logits=L)
+    torch.cuda.synchronize()
+    count = layer.routes["slot_count"].tolist()
+    tiles = lambda counts, N: sum((c + 255) // 256 for c in counts) * ((N + 255) // 256)
+    assert tiles(count, 2 * f) > 768 and tiles(count, d) > 768 and 0 in count
+    step = 1021
+    part = MoELayer(inp, capacity=step * 2)
+    s = part.shape
+    c, sc = quantise(inp.X)
+    xq = torch.cat([c.reshape(-1), sc.reshape(-1)])
+    Z = inp.A.clone()
+    for t0 in range(0, T, step):
+        n = min(step, T - t0)
+        B.moe_route_build(s, t0, n, L, part.phi, B.MOE_ROUTE_RESET, part.routes, part.ws)
+        torch.cuda.synchronize()
+        assert max(tiles(part.routes["slot_count"].tolist(), w) for w in (2 * f, d)) < 256
+        B.moe_expert_ffn(s, xq, None, part.routes, part.arena, part.phi, B.MOE_FFN_EXPERTS | B.MOE_FFN_ACT_MXFP4, part.ws)
+    B.moe_expert_ffn(s, None, Z, part.routes, None, None, B.MOE_FFN_FINALIZE, part.ws)
+    torch.cuda.synchronize()
+    assert torch.equal(Y, Z)
+    check_of_exact(inp, Y, layer.routes, torch.arange(5, T, 293, device="cuda"))

@@ -104,6 +104,8 @@ class MoELayer:
             if t is not None and (t.shape[0] != cfg.T or not t.is_contiguous()):
                 raise ValueError(f"{name}: need {cfg.T} rows, contiguous")
         B.check_device((self.X, Y, logits), stream)
+        if cfg.T == 0:
+            return Y
         n = cfg.T * cfg.d
         if self._xq is None:
             self._xq = torch.empty(n // 2 + n // 32, dtype=torch.uint8, device=self.device)

@@ -377,3 +377,15 @@ def test_several_tiles_a_workgroup(d, f):
     torch.cuda.synchronize()
     assert torch.equal(Y, Z)
     check_of_exact(inp, Y, layer.routes, torch.arange(5, T, 293, device="cuda"))
+
+
+def test_no_tokens():
+    say("MXFP4 activations: a prompt of no tokens, as the bf16 layer takes it")
+    inp = gpu_inputs(cfg_of(4, 64, 64, 2, 1))
+    c = inp.cfg.with_(T=0)
+    layer = MoELayer(type(inp)(**{**inp.__dict__, "cfg": c, "X": inp.X[:0], "A": inp.A[:0]}))
+    Y = torch.zeros(0, 64, device="cuda")
+    layer.forward(Y)
+    layer.forward_mxfp4(Y)
+    layer.forward_mxfp4(Y, logits=torch.zeros(0, 2, device="cuda"))
+    torch.cuda.synchronize()

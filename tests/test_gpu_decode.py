@@ -728,3 +728,60 @@ def test_decode_widest_layers(d, f, dtype):
                 layer.decode(X, Z, logits=logits)
                 torch.cuda.synchronize()
                 assert torch.equal(Z, Y)
+
+
+def test_decode_captured_while_a_slot_loads():
+    """Refused, and nothing is left of it: neither in the capture nor as an error
+    that the next launch would report."""
+    say("decode: a capture while a slot is being loaded")
+    inp = gpu_inputs(SMALL)
+    layer = MoELayer(inp)
+    X, A = tokens(SMALL, 3)
+    want = A.clone()
+    layer.decode(X, want)
+    torch.cuda.synchronize()
+    st, cap = torch.cuda.Stream(), torch.cuda.Stream()
+    B.arena_release_slot(layer.arena, 0)
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(400_000_000)
+        B.moe_pack_gate_up(layer.shape, inp.Wg[0], inp.Wu[0], layer.arena.plane_gu[0], 1, 0, 0)
+        B.moe_pack_down(layer.shape, inp.Wd[0], layer.arena.plane_d[0], 1, 0, 0)
+        B.arena_publish_slot(layer.arena, 0, 0)
+    n = torch.zeros(1, device="cuda")
+    Y = A.clone()
+    g = torch.cuda.CUDAGraph()
+    cap.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(cap):
+        g.capture_begin(capture_error_mode="thread_local")
+        n.add_(1)
+        with pytest.raises(B.MoEError) as e:
+            layer.decode(X, Y)
+        n.add_(1)
+        g.capture_end()
+    assert e.value.status == B.MOE_ERR_SLOT_STATE
+    layer.decode(X, Y)               # eager: waits for the load on its stream
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want) and float(n) == 2.0
+    with torch.cuda.graph(g2 := torch.cuda.CUDAGraph()):     # loaded now
+        layer.decode(X, Y)
+    Y.copy_(A)
+    g2.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, want)
+
+
+@pytest.mark.parametrize("d,f", [(4, 32), (12, 64), (20, 32)])
+def test_decode_narrowest_layers(d, f):
+    say(f"decode, fp32, d={d} f={f}")
+    cfg = MoEConfig(name="dec_narrow", index=88, T=4, d=d, f=f, E=5, k=2, n_shared=1, dtype="f32")
+    inp = gpu_inputs(cfg)
+    layer, weights = MoELayer(inp), plain_weights(inp)
+    for T in (1, 6, 64):
+        X, A = tokens(cfg, T)
+        buf = torch.full((T, d + 4), 7.5, device="cuda")
+        Y = buf[:, :d]
+        Y.copy_(A)
+        layer.decode(X, Y)
+        check(inp, weights, X, A, Y, layer.decode_routes(T), f"T={T}")
+        assert bool((buf[:, d:] == 7.5).all())

@@ -549,6 +549,10 @@ class Arena:
         is queued there, behind the current stream's; the weights are the
         caller's to keep until it is done."""
         quantise = self.shape.dtype == MOE_DT_BF16_FP4W and scales is None and Wg.dtype in _VAL_DTYPE
+        if quantise:   # the packing reads as much as the arena's shape says
+            f, d = self.shape.f, self.shape.d
+            if tuple(Wg.shape[1:]) != (f, d) or tuple(Wu.shape[1:]) != (f, d) or tuple(Wd.shape[1:]) != (d, f):
+                raise ValueError(f"load_resident: need Wg and Wu [experts][{f}][{d}] and Wd [experts][{d}][{f}]")
         with on_stream(stream):
             for e, s in enumerate(phi):
                 if s < 0:

@@ -104,3 +104,16 @@ def test_other_devices_refused(monkeypatch):
         B._stream_of(torch.zeros(4), None)      # host memory
     with pytest.raises(ValueError):
         B._stream_of(_On(1), _On(0))
+
+
+def test_weights_of_another_shape_refused():
+    """Weights that are quantised on their way into an arena: a smaller slice would be
+    read past its end by the packing."""
+    arena = B.Arena.__new__(B.Arena)
+    arena.shape, arena.handle = B.make_shape(4, 128, 64, 2, 1, dtype="bf16_fp4w"), None
+    ok = dict(Wg=(2, 64, 128), Wu=(2, 64, 128), Wd=(2, 128, 64))
+    for kw in (dict(Wg=(2, 64, 64)), dict(Wu=(2, 32, 128)), dict(Wd=(2, 64, 128)), dict(Wd=(2, 128, 32)),
+               dict(Wg=(64, 128))):
+        w = {k: torch.zeros(v) for k, v in dict(ok, **kw).items()}
+        with pytest.raises(ValueError, match="load_resident: need"):
+            arena.load_resident(w["Wg"], w["Wu"], w["Wd"], phi=[0, 1])

@@ -360,7 +360,12 @@ moe_status moe_layer_prefill_noalloc(const moe_shape *shape, const void *X,
  * in fp32: unlike the prompt layer's bf16 H, H is not rounded, so the outputs
  * of the two differ by that rounding. Each expert hit is read once (once for
  * every 5 to 32 of its routes, whichever suits the shape). Y is bitwise
- * run-to-run identical and independent of phi and P.
+ * run-to-run identical and independent of phi and P. A token's bits do not
+ * depend on the other tokens of the call, but may on how many there are:
+ * K is cut among more waves where an expert's entries hold 32 routes, which
+ * follows from T, k, E and the experts' size.
+ * bf16 layers carry H as a sum of three bf16 terms, some of them 0: an
+ * infinity in W_d gives NaN where the formula gives an infinity.
  *   shape    T <= MOE_DECODE_MAX_T tokens, T * K' <= MOE_DECODE_MAX_ROUTES,
  *            d <= MOE_DECODE_MAX_D, a packed gate/up slice below 2 GiB
  *            (MOE_ERR_UNSUPPORTED otherwise); every dtype; `capacity` is not
@@ -485,6 +490,7 @@ moe_status moe_dequantize_mxfp4(const void *codes, const void *scales,
  *   C            device [M][ldc] of c_dtype (MOE_DT_F32 or MOE_DT_BF16), N <=
  *                ldc < 2^21; C and its row stride 16-byte aligned
  * Rows and offsets out of range are brought into it on the device.
+ * MOE_ERR_UNSUPPORTED from (M / 64 + P + 1) * (N / 64) = 2^24 on.
  */
 moe_status moe_matmul_mxfp4(int32_t M, int32_t N, int32_t K,
                             const void *A_codes, const void *A_scales,

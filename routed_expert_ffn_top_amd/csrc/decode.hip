@@ -917,8 +917,13 @@ hipError_t launch_dec_route(const moe_shape &s, const DecRouteArgs &a, const Phi
 // in bf16, 64 tokens 210 / 182 / 198 / 218; 8 experts of 4096 x 14336, top-2, bf16, 32
 // tokens 888 / 504 / 521 / 573, 64 tokens 1389 / 701 / 584 / 661; 3 + 2 experts of 512 x
 // 3392, top-1, fp8, 62 tokens 50 / 46 / 59 / 82; 7 + 1 of 3840 x 1280, top-6, bf16, 53
-// tokens 225 / 136 / 143 / 148; against it 9 + 1 of 1408 x 1856, top-5, bf16, 64 tokens
-// 176 / 119 / 104 / 104.
+// tokens 225 / 136 / 143 / 148. The border at 64 MB, with 16 / 32: 8 experts of 4096 x f,
+// top-2, bf16, f = 1344 (32 MB) 48 tokens 74 / 81, 64 tokens 87 / 88; 2688 (63 MB) 133 / 143,
+// 156 / 152; 4096 (96 MB) 180 / 194, 221 / 202; 5376 225 / 242, 269 / 259; 8192 341 / 338,
+// 424 / 367; fp8, f = 4096 (48 MB) 107 / 124, 129 / 134; 8192 (96 MB) 193 / 206, 246 / 228;
+// up to 32 tokens there the two agree within 3 %. Against it: 9 + 1 experts of 1408 x 1856
+// (15 MB), top-5, bf16, 32 tokens 77 / 62, 48 tokens 78 / 67, 64 tokens 115 / 104; and MXFP4,
+// 4096 x 14336 (89 MB), 64 tokens 311 / 320.
 int dec_rpe(const moe_shape &s)
 {
     double miss = 1.0;   // that a routed expert is hit by none of the tokens

@@ -836,7 +836,10 @@ hipError_t launch_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, 
 // less than 16 rows a slot it is ahead at any size (64 slots of N = K = 2048: 1
 // row each 18 against 30 us, 16 rows 32 against 32, 64 rows 84 against 32; one
 // slot of 512 rows 12 against 20, of 2048 rows 37 against 21). At the borders the
-// other one is up to 14 % faster (one slot of 128 rows, N = 8192: 21 against 24).
+// other one is up to 14 % faster (one slot of 128 rows, N = 8192: 21 against 24). The rule
+// goes by the mean, since only the device knows the slots' rows: where one slot of many
+// holds most of them it takes the small kernel and loses (N = K = 2048, 4096 rows in one
+// of 512 slots 119 us, as one slice 24; with 8192, where the mean is 16, 38 and 32).
 static bool ring_pays(const MxArgs &a)
 {
     const int64_t slots = std::min(a.P, a.M), rows = a.M / slots;

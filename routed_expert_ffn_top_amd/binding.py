@@ -204,8 +204,10 @@ def on_stream(stream):
     if stream is None:
         yield
         return
-    if isinstance(stream, int):   # a handle; 0 is the default stream's
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    if isinstance(stream, int):   # a handle; 0 and 1 (the legacy one) are the default stream's
+        if stream == 2:           # this thread's: torch takes a handle for an address, and would use another stream
+            raise ValueError("the per-thread stream has no torch stream: give one of torch's, or its handle")
+        stream = torch.cuda.ExternalStream(stream) if stream > 2 else torch.cuda.default_stream()
     stream.wait_stream(torch.cuda.current_stream(stream.device))
     with torch.cuda.stream(stream):
         yield

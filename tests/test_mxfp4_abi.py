@@ -1,5 +1,7 @@
 """The MXFP4 operators' checks of their arguments, on the CPU: every call
 below ends in its checks, before any GPU work."""
+import contextlib
+
 import pytest
 import torch
 
@@ -117,3 +119,29 @@ def test_weights_of_another_shape_refused():
         w = {k: torch.zeros(v) for k, v in dict(ok, **kw).items()}
         with pytest.raises(ValueError, match="load_resident: need"):
             arena.load_resident(w["Wg"], w["Wu"], w["Wd"], phi=[0, 1])
+
+
+def test_handles_of_streams_without_an_address(monkeypatch):
+    """0 and 1 name the default stream; the per-thread one (2) torch cannot name, and
+    as an address it would be another stream."""
+    class Stream:
+        device = "cuda:0"
+
+        def __init__(self, handle=0):
+            self.handle = handle
+
+        def wait_stream(self, other):
+            used.append(self.handle)
+
+    used = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "default_stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(5))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    for handle in (0, 1, 0x7f0000000100):
+        with B.on_stream(handle):
+            pass
+    assert used == [0, 0, 0x7f0000000100]
+    with pytest.raises(ValueError):
+        with B.on_stream(2):
+            pass

@@ -29,7 +29,7 @@ def listed():
         # 32 sequences answering, two of eight large experts each: nothing but reading the weights
         dict(name="matmul_mixtral_t32", kind="matmul", M=64, N=4096, K=14336, P=8, gather=False, out="f32", pow2=False),
         # the down projection of a prompt of 4096 tokens, the shared experts among the slots, a checkpoint's own scales
-        dict(name="matmul_dsv2lite_down", kind="matmul", M=32768, N=2048, K=1408, P=66, gather=False, out="f32", pow2=False),
+        dict(name="matmul_dsv2lite_down", kind="matmul", M=32768, N=2048, K=1408, P=66, gather=False, out="bf16", pow2=False),
         # a short prompt: groups of uneven size, some empty, widths that end inside a block
         dict(name="matmul_ragged", kind="matmul", M=777, N=320, K=448, P=7, gather=True, out="f32", pow2=False),
         # an expert FFN for one answering token

@@ -500,6 +500,175 @@ moe_status moe_matmul_mxfp4(int32_t M, int32_t N, int32_t K,
                             int32_t c_dtype, int64_t ldc, moe_stream stream);
 
 /*
+ * fp8 blocks of 128: e4m3 codes (the format of MOE_DT_BF16_FP8W's) with one
+ * scale for each block, in two forms:
+ *   block_rows 1, rows (activations): a block is 128 consecutive values of a
+ *     row, the last one of a row may be 64; its scale is a byte b, 2^(b - 127),
+ *     at scales[row * MOE_FP8_SCALE_BYTES(K) + k / 128] (a row's bytes take
+ *     whole 16-byte pieces; what is behind them is neither read nor written)
+ *   block_rows 128, weights: a block is 128 rows x 128 values, the last ones
+ *     may be smaller; its scale is an fp32 number at
+ *     scales[(row / 128) * ceil(K / 128) + k / 128] (the layout of checkpoints
+ *     whose linear weights come with an inverse scale for each 128 x 128)
+ *   values   device [rows][ld] of val_dtype (MOE_DT_F32 or MOE_DT_BF16), K of
+ *            each row used, K a multiple of 64, rows >= 0, ld >= K; the pointer
+ *            and the row stride 16-byte aligned; at most 2^33 values a call
+ *   codes    device [rows][K], 16-byte aligned
+ * moe_quantize_fp8: a block's scale is the least power of two in 2^-126 ..
+ * 2^120 with max |value| <= 448 scale; each value over it, which is exact, is
+ * rounded to the nearest code, ties to the even one. A block that holds an
+ * infinity or a NaN gets the scale NaN (byte 255) and codes 0.
+ * moe_dequantize_fp8: value = code value * scale, in fp32, for bf16 rounded
+ * once more; exact for the scales that moe_quantize_fp8 gives wherever the
+ * result is a normal number. Any fp32 scale may be given, byte 255 is NaN.
+ */
+#define MOE_FP8_SCALE_BYTES(K) (((int64_t)(K) + 2047) / 2048 * 16)
+#define MOE_FP8_MAX_K 1048576
+moe_status moe_quantize_fp8(const void *values, int32_t val_dtype, int64_t rows,
+                            int32_t K, int64_t ld, int32_t block_rows,
+                            void *codes, void *scales, moe_stream stream);
+moe_status moe_dequantize_fp8(const void *codes, const void *scales,
+                              int64_t rows, int32_t K, int32_t block_rows,
+                              void *values, int32_t val_dtype, int64_t ld,
+                              moe_stream stream);
+
+/*
+ * Product of quantised rows and fp8 weights, one weight slice per group of
+ * rows, as the expert projections are grouped by the route map:
+ *   C[p][n] = sum_k A[row(p)][k] * B_s[n][k]   for the records p of slot s,
+ * both sides as they are stored (scaled matrix instructions), fp32 sums, C
+ * rounded once.
+ *   M            records, rows of C; M >= 0
+ *   N, K         multiples of 64, K <= MOE_FP8_MAX_K
+ *   A_codes, A_scales   device [A_rows][K] and [A_rows][MOE_FP8_SCALE_BYTES(K)],
+ *                rows as moe_quantize_fp8 writes them; 16-byte aligned
+ *   row_index    device [M] int32: row(p), in [0, A_rows) (rec_token of a
+ *                route build); NULL: row(p) = p, and A_rows >= M
+ *   slot_offset  device [P+1] int32 ascending from 0, at most M: slot s holds
+ *                records [slot_offset[s], slot_offset[s+1]) (slot_offset of a
+ *                route build); records from slot_offset[P] on are left as they
+ *                were. NULL: P = 1 and every record is in slot 0
+ *   B_codes, B_scales   device, P slices of codes [N][K] (16-byte aligned),
+ *                B_stride bytes apart (a multiple of 16), with scales
+ *                [ceil(N/128)][ceil(K/128)], B_scale_stride floats apart, as
+ *                moe_quantize_fp8 writes them with block_rows 128; the strides
+ *                are not used with P = 1; P <= 512
+ *   C            device [M][ldc] of c_dtype (MOE_DT_F32 or MOE_DT_BF16), N <=
+ *                ldc < 2^21; C and its row stride 16-byte aligned
+ * A weight's scale may be any fp32 number; a NaN or an infinity makes NaN of
+ * what it meets, one below 2^-126 in magnitude counts as 2^-126 or as itself. Rows and
+ * offsets out of range are brought into it on the device.
+ * MOE_ERR_UNSUPPORTED from (M / 16 + P + 1) * (N / 64) = 2^22 on.
+ */
+moe_status moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void *A_codes,
+                          const void *A_scales, int32_t A_rows,
+                          const int32_t *row_index, const int32_t *slot_offset,
+                          int32_t P, const void *B_codes, const float *B_scales,
+                          int64_t B_stride, int64_t B_scale_stride, void *C,
+                          int32_t c_dtype, int64_t ldc, moe_stream stream);
+
+/*
+ * The gate and up projections of an expert on such operands, with SwiGLU and
+ * the quantisation of H behind them: with g and u the products of a record's
+ * row with its slot's W_g and W_u, both [f][K], as in moe_matmul_fp8,
+ *   H[p] = fp8 rows (block_rows 1) of SiLU(g) * u in fp32.
+ *   Wg_codes, Wg_scales, Wu_codes, Wu_scales   P slices each, as B_codes and
+ *                B_scales above with N = f; both use the two strides (two
+ *                tensors, or the halves of one of [P][2f][K])
+ *   H_codes      device [M][f], 16-byte aligned
+ *   H_scales     device [M][MOE_FP8_SCALE_BYTES(f)]
+ * The other arguments and the limits are those of moe_matmul_fp8, which takes
+ * H for the down projection. SiLU(g) * u is within (|g| + 8) 2^-22 of its
+ * value for the g and u of the fp32 sums, relative.
+ */
+moe_status moe_gate_up_fp8(int32_t M, int32_t f, int32_t K, const void *A_codes,
+                           const void *A_scales, int32_t A_rows,
+                           const int32_t *row_index, const int32_t *slot_offset,
+                           int32_t P, const void *Wg_codes,
+                           const float *Wg_scales, const void *Wu_codes,
+                           const float *Wu_scales, int64_t W_stride,
+                           int64_t W_scale_stride, void *H_codes,
+                           void *H_scales, moe_stream stream);
+
+/*
+ * Combine of rows in record order, as moe_matmul_fp8 and moe_matmul_mxfp4
+ * write them (Eq. 2), and its gradients:
+ *   Y[t] += sum_j topk_w[t*K'+j] * C[route_pos[t*K'+j]],  j ascending, in fp32
+ * over the routes whose position lies in [0, M); the others (-1: left out) add
+ * nothing.
+ *   T, d, kp     tokens, columns (a multiple of 4, at most MOE_COMBINE_MAX_D),
+ *                K' routes a token (1 to 64); T * ceil(d / 1024) < 2^24
+ *   C            device [M][ldc] of c_dtype (MOE_DT_F32, 16-byte aligned, or
+ *                MOE_DT_BF16, 8-byte aligned), ldc >= d a multiple of 4
+ *   route_pos, topk_w   device [T*K'], as moe_route_build writes them
+ *   Y            device [T][ldy] fp32, in place; 16-byte aligned, ldy >= d a
+ *                multiple of 4
+ * moe_combine_backward: for each such route i of token t, with r its record,
+ *   dC[r] = topk_w[i] * dY[t],  d_topk_w[i] = sum_n dY[t][n] * C[r][n] in fp32;
+ * d_topk_w is 0 for the others, and rows of dC that no route has are left as
+ * they were. No record may have two routes. The gradient of Y's first value is
+ * dY itself.
+ *   dY           as Y; dC [M][lddc] as C, or NULL; d_topk_w device [T*K']
+ * The sums are in a fixed order, so results are bitwise run-to-run identical.
+ */
+#define MOE_COMBINE_MAX_D 1048576
+moe_status moe_combine(int32_t T, int32_t d, int32_t kp, int32_t M,
+                       const void *C, int32_t c_dtype, int64_t ldc,
+                       const int32_t *route_pos, const float *topk_w, float *Y,
+                       int64_t ldy, moe_stream stream);
+moe_status moe_combine_backward(int32_t T, int32_t d, int32_t kp, int32_t M,
+                                const void *C, int32_t c_dtype, int64_t ldc,
+                                const int32_t *route_pos, const float *topk_w,
+                                const float *dY, int64_t ldy, void *dC,
+                                int64_t lddc, float *d_topk_w,
+                                moe_stream stream);
+
+/*
+ * Load-balancing loss of a routing, the counts behind it, and the gradient of
+ * the router's logits. With p_t the softmax of token t's logits over all E
+ * (NaN is taken as -infinity, as in the top-k; a row without a finite logit has
+ * p = 0), n_s the counted tokens of sequence s, c_se their routes to expert e
+ * and P_se their mean p_te,
+ *   loss = mean over the sequences with n_s > 0 of E / (k n_s) sum_e c_se P_se
+ * (1 where both are uniform; 0 without any counted token).
+ *   shape        T, E, k, n_shared and renorm are used
+ *   logits       device [T][E] fp32, topk_idx device [T][K'] as
+ *                moe_route_build takes and writes them; ids outside [0, E) and
+ *                the shared ranks count nothing
+ *   seq_offset   device [S+1] int32 ascending, at most T: sequence s holds the
+ *                tokens [seq_offset[s], seq_offset[s+1]); tokens outside are not
+ *                counted. NULL: S = 1 and every token
+ *   S            1 to 4096
+ *   mask         device [T] bytes, 0: the token is not counted; or NULL
+ *   loss         device [1] fp32; counts device [S][E] int32 (c_se); prob device
+ *                [S][E] fp32 (P_se)
+ *   slope        device [S][E] fp32: d loss / d p_te of a counted token less its
+ *                mean over the experts, which a softmax's gradient drops
+ *   ws           at least moe_balance_workspace_bytes(shape, S) bytes, 256-byte
+ *                aligned, of any contents; one call at a time
+ * The sums are in a fixed order, so results are bitwise run-to-run identical.
+ * moe_router_backward: d_logits [T][E] fp32, written for every token, of
+ *   *d_loss * loss + sum d_topk_w * topk_w,
+ * with topk_w the weights that moe_route_build gives for topk_idx.
+ *   slope, d_loss   of moe_balance_loss, with its seq_offset, S and mask (NULL
+ *                slope: without the loss); d_loss device [1] fp32 (NULL: 1)
+ *   d_topk_w     device [T][K'] fp32 or NULL; the shared ranks' are not used,
+ *                nor those of ids outside [0, E). With it, topk_idx is required
+ */
+size_t moe_balance_workspace_bytes(const moe_shape *shape, int32_t S);
+moe_status moe_balance_loss(const moe_shape *shape, const float *logits,
+                            const int32_t *topk_idx, const int32_t *seq_offset,
+                            int32_t S, const uint8_t *mask, float *loss,
+                            int32_t *counts, float *prob, float *slope, void *ws,
+                            size_t ws_bytes, moe_stream stream);
+moe_status moe_router_backward(const moe_shape *shape, const float *logits,
+                               const int32_t *topk_idx, const float *slope,
+                               const float *d_loss, const int32_t *seq_offset,
+                               int32_t S, const uint8_t *mask,
+                               const float *d_topk_w, float *d_logits,
+                               moe_stream stream);
+
+/*
  * Slot arena (Eq. 3: the slice j of slot s starts at plane_j + s * S_j).
  *   plane_gu  device, P slots of packed gate/up slices (2f*d elements,
  *             tiled layout above), slot stride stride_gu

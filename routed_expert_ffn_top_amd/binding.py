@@ -39,6 +39,14 @@ def fp4_slice_bytes(N: int, K: int) -> int:
     piece = lambda rows: rows * 16 + (rows + 15) // 16 * 16
     full, rem = divmod(N, 256)
     return (K // 32) * (full * piece(256) + (piece(rem) if rem else 0))
+
+
+def fp8_scale_bytes(K: int) -> int:
+    """Bytes between the scale rows of rows of K values quantised to fp8: one
+    for each 128, in whole 16-byte pieces."""
+    return (K + 2047) // 2048 * 16
+
+
 MOE_DEVERR_EXPERT_ID = 1
 MOE_ROUTE_RESET = 1
 MOE_FFN_EXPERTS = 1
@@ -51,6 +59,8 @@ MOE_MAX_EXPERTS = 512
 MOE_DECODE_MAX_T = 64
 MOE_DECODE_MAX_ROUTES = 1024
 MOE_DECODE_MAX_D = 131072
+MOE_FP8_MAX_K = 1048576
+MOE_COMBINE_MAX_D = 1048576
 
 
 class MoEError(RuntimeError):
@@ -90,6 +100,16 @@ _SIGS = {
     "moe_quantize_mxfp4": ([_VP, _I32, _I64, _I32, _I64, _VP, _VP, _VP], _I32),
     "moe_dequantize_mxfp4": ([_VP, _VP, _I64, _I32, _VP, _I32, _I64, _VP], _I32),
     "moe_matmul_mxfp4": ([_I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _I64, _VP, _I32, _I64, _VP], _I32),
+    "moe_quantize_fp8": ([_VP, _I32, _I64, _I32, _I64, _I32, _VP, _VP, _VP], _I32),
+    "moe_dequantize_fp8": ([_VP, _VP, _I64, _I32, _I32, _VP, _I32, _I64, _VP], _I32),
+    "moe_matmul_fp8": ([_I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _VP, _I64, _I64, _VP, _I32, _I64, _VP], _I32),
+    "moe_gate_up_fp8": ([_I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _I64, _I64, _VP, _VP, _VP],
+                        _I32),
+    "moe_combine": ([_I32, _I32, _I32, _I32, _VP, _I32, _I64, _VP, _VP, _VP, _I64, _VP], _I32),
+    "moe_combine_backward": ([_I32, _I32, _I32, _I32, _VP, _I32, _I64, _VP, _VP, _VP, _I64, _VP, _I64, _VP, _VP], _I32),
+    "moe_balance_workspace_bytes": ([_VP, _I32], _SZ),
+    "moe_balance_loss": ([_VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP], _I32),
+    "moe_router_backward": ([_VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP, _VP], _I32),
     "moe_decode_workspace_bytes": ([_VP], _SZ),
     "moe_decode_workspace_init": ([_VP, _VP, _SZ, _VP], _I32),
     "moe_layer_decode": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP], _I32),
@@ -392,6 +412,223 @@ def moe_matmul_mxfp4(A_codes, A_scales, B, C, slot_offset=None, row_index=None, 
                                    C.data_ptr(), dtype, ldc, _stream_of(C, stream)))
 
 
+def _fp8_views(values, codes, scales, block_rows):
+    """Type code, rows, K and row stride of [..., K] values and their fp8
+    blocks; leading dimensions that one row stride covers count as rows."""
+    dtype = _VAL_DTYPE.get(values.dtype)
+    if dtype is None:
+        raise ValueError("values must be float32 or bfloat16")
+    shape, n, dev = values.shape, values.numel(), values.get_device()
+    K = shape[-1]
+    rows = n // K if K else 0
+    if codes.dtype is not torch.uint8 or codes.numel() != n or not codes.is_contiguous():
+        raise ValueError("need contiguous uint8 codes [rows][K]")
+    if block_rows == 1:
+        if scales.dtype is not torch.uint8 or scales.numel() != rows * fp8_scale_bytes(K) or not scales.is_contiguous():
+            raise ValueError("need contiguous uint8 scales [rows][fp8_scale_bytes(K)]")
+    elif (scales.dtype is not torch.float32 or scales.numel() != -(-rows // 128) * -(-K // 128)
+          or not scales.is_contiguous()):
+        raise ValueError("need contiguous float32 scales [ceil(rows / 128)][ceil(K / 128)]")
+    if codes.get_device() != dev or scales.get_device() != dev:
+        raise ValueError("values, codes and scales must be on one device")
+    if values.is_contiguous():
+        ld = K
+    elif len(shape) != 2:
+        raise ValueError("values: only a matrix may have a row stride")
+    else:
+        ld, step = values.stride()
+        if step != 1:
+            raise ValueError("values: rows must be contiguous")
+        if rows == 1:
+            ld = (K + 7) // 8 * 8   # one row: any aligned stride does
+    return dtype, rows, K, ld
+
+
+def moe_quantize_fp8(values, codes, scales, block_rows=1, stream=None):
+    """block_rows 1: scales uint8 [rows][fp8_scale_bytes(K)]; 128: float32 [ceil(rows/128)][ceil(K/128)]."""
+    dtype, rows, K, ld = _fp8_views(values, codes, scales, block_rows)
+    _check(load().moe_quantize_fp8(values.data_ptr(), dtype, rows, K, ld, block_rows, codes.data_ptr(), scales.data_ptr(),
+                                   _stream_of(values, stream)))
+
+
+def moe_dequantize_fp8(codes, scales, values, block_rows=1, stream=None):
+    dtype, rows, K, ld = _fp8_views(values, codes, scales, block_rows)
+    _check(load().moe_dequantize_fp8(codes.data_ptr(), scales.data_ptr(), rows, K, block_rows, values.data_ptr(), dtype, ld,
+                                     _stream_of(values, stream)))
+
+
+def _fp8_rows(codes, scales, name):
+    rows, K = codes.shape
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+        raise ValueError(f"{name}: codes and scales must be uint8")
+    if not codes.is_contiguous() or not scales.is_contiguous() or scales.numel() != rows * fp8_scale_bytes(K):
+        raise ValueError(f"{name}: need contiguous codes [rows][K] and scales [rows][fp8_scale_bytes(K)]")
+    return rows, K
+
+
+def _fp8_slices(codes, scales, K, name):
+    """P, N and the strides of weight slices [P][N][K] (or one [N][K]) with
+    their scales; a slice is contiguous, its distance to the next free."""
+    shape, stride = codes.shape, codes.stride()
+    if len(shape) not in (2, 3) or codes.dtype is not torch.uint8 or shape[-1] != K or stride[-1] != 1 or stride[-2] != K:
+        raise ValueError(f"{name}: need uint8 codes [P][N][{K}], a slice contiguous")
+    N, KB, P = shape[-2], -(-K // 128), shape[0] if len(shape) == 3 else 1
+    want, s_stride = (-(-N // 128), KB), scales.stride()
+    if (scales.dtype is not torch.float32 or tuple(scales.shape) != tuple(shape[:-2]) + want
+            or KB > 1 and s_stride[-1] != 1 or want[0] > 1 and s_stride[-2] != KB):
+        raise ValueError(f"{name}: need float32 scales [P][ceil(N / 128)][ceil(K / 128)], a slice's contiguous")
+    return P, N, stride[0] if P > 1 else N * K, s_stride[0] if P > 1 else 0
+
+
+def _groups(M, P, dev, slot_offset, row_index):
+    for t, n, name in ((slot_offset, P + 1, "slot_offset"), (row_index, M, "row_index")):
+        if t is not None and (t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous() or t.get_device() != dev):
+            raise ValueError(f"{name}: need int32 [{n}]")
+
+
+def _one_device(dev, *tensors):
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError("the operands must be on one device")
+
+
+def moe_matmul_fp8(A_codes, A_scales, B_codes, B_scales, C, slot_offset=None, row_index=None, stream=None):
+    """C [M][N] = rows of A times the slices B_codes [P][N][K] (or one [N][K])
+    with their scales; A_codes uint8 [A_rows][K]."""
+    A_rows, K = _fp8_rows(A_codes, A_scales, "A")
+    P, N, b_stride, s_stride = _fp8_slices(B_codes, B_scales, K, "B")
+    M, dtype, dev = C.shape[0], _VAL_DTYPE.get(C.dtype), C.get_device()
+    ldc, step = C.stride()
+    if M <= 1:
+        ldc = (N + 7) // 8 * 8   # one row: any aligned stride does
+    if dtype is None or C.shape[1] != N or step != 1 or ldc < N:
+        raise ValueError(f"C must be float32 or bfloat16 [M][{N}] with contiguous rows")
+    _one_device(dev, A_codes, A_scales, B_codes, B_scales)
+    _groups(M, P, dev, slot_offset, row_index)
+    _check(load().moe_matmul_fp8(M, N, K, A_codes.data_ptr(), A_scales.data_ptr(), A_rows, _ptr(row_index),
+                                 _ptr(slot_offset), P, B_codes.data_ptr(), B_scales.data_ptr(), b_stride, s_stride,
+                                 C.data_ptr(), dtype, ldc, _stream_of(C, stream)))
+
+
+def moe_gate_up_fp8(A_codes, A_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales, H_codes, H_scales, slot_offset=None,
+                    row_index=None, stream=None):
+    """H [M][f] = fp8 rows of SiLU(A Wg^T) * (A Wu^T); Wg_codes and Wu_codes
+    uint8 [P][f][K] (or one [f][K]), of the same strides."""
+    A_rows, K = _fp8_rows(A_codes, A_scales, "A")
+    M, f = _fp8_rows(H_codes, H_scales, "H")
+    gate, up = _fp8_slices(Wg_codes, Wg_scales, K, "Wg"), _fp8_slices(Wu_codes, Wu_scales, K, "Wu")
+    if gate != up or gate[1] != f:
+        raise ValueError(f"Wg and Wu need the same shapes and strides, {f} rows a slice")
+    P, _, w_stride, s_stride = gate
+    dev = H_codes.get_device()
+    _one_device(dev, A_codes, A_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales, H_scales)
+    _groups(M, P, dev, slot_offset, row_index)
+    _check(load().moe_gate_up_fp8(M, f, K, A_codes.data_ptr(), A_scales.data_ptr(), A_rows, _ptr(row_index),
+                                  _ptr(slot_offset), P, Wg_codes.data_ptr(), Wg_scales.data_ptr(), Wu_codes.data_ptr(),
+                                  Wu_scales.data_ptr(), w_stride, s_stride, H_codes.data_ptr(), H_scales.data_ptr(),
+                                  _stream_of(H_codes, stream)))
+
+
+def _strided(t, name, cols=None):
+    """Row stride of a matrix with contiguous rows that do not overlap."""
+    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name}: need a matrix" + (f" of {cols} columns" if cols is not None else ""))
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return row_stride(t)
+
+
+def _combine_args(C, route_pos, topk_w, Y, name):
+    T, d = Y.shape
+    dtype, kp = _VAL_DTYPE.get(C.dtype), topk_w.shape[-1]
+    if dtype is None or Y.dtype is not torch.float32:
+        raise ValueError(f"C must be float32 or bfloat16 and {name} float32")
+    ldc, ldy = _strided(C, "C", d), _strided(Y, name)
+    if topk_w.dtype is not torch.float32 or tuple(topk_w.shape) != (T, kp) or not topk_w.is_contiguous():
+        raise ValueError(f"topk_w: need contiguous float32 [{T}][K']")
+    if route_pos.dtype is not torch.int32 or route_pos.numel() != T * kp or not route_pos.is_contiguous():
+        raise ValueError(f"route_pos: need contiguous int32 [{T * kp}]")
+    _one_device(Y.get_device(), C, route_pos, topk_w)
+    return T, d, kp, C.shape[0], C.data_ptr(), dtype, ldc, route_pos.data_ptr(), topk_w.data_ptr(), Y.data_ptr(), ldy
+
+
+def moe_combine(C, route_pos, topk_w, Y, stream=None):
+    """Y [T][d] += the rows of C [M][d] at route_pos [T*K'], times topk_w [T][K']."""
+    _check(load().moe_combine(*_combine_args(C, route_pos, topk_w, Y, "Y"), _stream_of(Y, stream)))
+
+
+def moe_combine_backward(C, route_pos, topk_w, dY, dC, d_topk_w, stream=None):
+    """dC [M][d] (or None) and d_topk_w [T][K'] of moe_combine."""
+    args = _combine_args(C, route_pos, topk_w, dY, "dY")
+    lddc = 0
+    if dC is not None:
+        if dC.dtype is not C.dtype or dC.shape != C.shape:
+            raise ValueError("dC: need C's shape and type")
+        lddc = _strided(dC, "dC")
+        _one_device(dY.get_device(), dC)
+    if d_topk_w.dtype is not torch.float32 or d_topk_w.shape != topk_w.shape or not d_topk_w.is_contiguous():
+        raise ValueError("d_topk_w: need topk_w's shape, contiguous float32")
+    _one_device(dY.get_device(), d_topk_w)
+    _check(load().moe_combine_backward(*args, _ptr(dC), lddc, d_topk_w.data_ptr(), _stream_of(dY, stream)))
+
+
+def moe_balance_workspace_bytes(shape: moe_shape, S: int = 1) -> int:
+    return int(load().moe_balance_workspace_bytes(ctypes.byref(shape), S))
+
+
+def _whole(t, dtype, shape, name, dev):
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: need contiguous {dtype} {list(shape)}")
+    _one_device(dev, t)
+
+
+def _sequences(shape, seq_offset, mask, dev):
+    S = 1
+    if seq_offset is not None:
+        S = seq_offset.numel() - 1
+        _whole(seq_offset, torch.int32, (S + 1,), "seq_offset", dev)
+    if mask is not None:
+        if mask.dtype not in (torch.uint8, torch.bool):
+            raise ValueError("mask: need uint8 or bool")
+        _whole(mask, mask.dtype, (shape.T,), "mask", dev)
+    return S
+
+
+def moe_balance_loss(shape, logits, topk_idx, loss, counts, prob, slope, ws, seq_offset=None, mask=None, stream=None):
+    """loss [1], counts (int32), prob and slope [S][E] of the routing topk_idx
+    [T][K'] of logits [T][E]; seq_offset int32 [S+1], mask uint8 or bool [T]."""
+    dev, f32, i32 = logits.get_device(), torch.float32, torch.int32
+    S = _sequences(shape, seq_offset, mask, dev)
+    _whole(logits, f32, (shape.T, shape.E), "logits", dev)
+    _whole(topk_idx, i32, (shape.T, shape.k + shape.n_shared), "topk_idx", dev)
+    _whole(loss, f32, (1,), "loss", dev)
+    for t, dt, name in ((counts, i32, "counts"), (prob, f32, "prob"), (slope, f32, "slope")):
+        _whole(t, dt, (S, shape.E), name, dev)
+    _one_device(dev, ws)
+    _check(load().moe_balance_loss(ctypes.byref(shape), logits.data_ptr(), topk_idx.data_ptr(), _ptr(seq_offset), S,
+                                   _ptr(mask), loss.data_ptr(), counts.data_ptr(), prob.data_ptr(), slope.data_ptr(),
+                                   ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(logits, stream)))
+
+
+def moe_router_backward(shape, logits, topk_idx, d_logits, slope=None, d_loss=None, d_topk_w=None, seq_offset=None,
+                        mask=None, stream=None):
+    """d_logits [T][E] of d_loss [1] (None: 1) times the balance loss whose
+    slope is given, plus that of d_topk_w [T][K']."""
+    dev, f32 = logits.get_device(), torch.float32
+    S = _sequences(shape, seq_offset, mask, dev)
+    kp = shape.k + shape.n_shared
+    _whole(logits, f32, (shape.T, shape.E), "logits", dev)
+    _whole(d_logits, f32, (shape.T, shape.E), "d_logits", dev)
+    if topk_idx is not None:
+        _whole(topk_idx, torch.int32, (shape.T, kp), "topk_idx", dev)
+    for t, want, name in ((slope, (S, shape.E), "slope"), (d_loss, (1,), "d_loss"), (d_topk_w, (shape.T, kp), "d_topk_w")):
+        if t is not None:
+            _whole(t, f32, want, name, dev)
+    _check(load().moe_router_backward(ctypes.byref(shape), logits.data_ptr(), _ptr(topk_idx), _ptr(slope), _ptr(d_loss),
+                                      _ptr(seq_offset), S, _ptr(mask), _ptr(d_topk_w), d_logits.data_ptr(),
+                                      _stream_of(logits, stream)))
+
+
 def moe_pack_gate_up(shape, Wg, Wu, dst, n, src_stride, dst_stride, stream=None):
     _check(load().moe_pack_gate_up(ctypes.byref(shape), _ptr(Wg), _ptr(Wu), _ptr(dst), n,
                                    src_stride, dst_stride, _stream(stream)))
@@ -505,6 +742,15 @@ def alloc_decode_workspace(shape: moe_shape, device="cuda") -> torch.Tensor:
     ws = buf[off:off + n]
     moe_decode_workspace_init(shape, ws)
     return ws
+
+
+def alloc_balance_workspace(shape: moe_shape, S: int = 1, device="cuda") -> torch.Tensor:
+    n = moe_balance_workspace_bytes(shape, S)
+    if n == 0:
+        _check(MOE_ERR_INVALID_ARG)
+    buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + n]
 
 
 class Arena:

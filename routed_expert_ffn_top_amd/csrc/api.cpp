@@ -22,8 +22,10 @@
 
 #include "common.h"
 #include "decode.h"
+#include "fp8.h"
 #include "mxfp4.h"
 #include "residency.h"
+#include "train.h"
 
 using namespace moe;
 
@@ -845,6 +847,291 @@ moe_status moe_matmul_mxfp4(int32_t M, int32_t N, int32_t K, const void *A_codes
     a.c_bf16 = c_dtype == MOE_DT_BF16;
     a.ldc = ldc;
     HIP_TRY(launch_matmul_mxfp4(a, S(stream)), "matmul launch");
+    return MOE_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// fp8 operators
+
+namespace {
+
+moe_status check_fp8_values(const char *what, const void *v, int32_t dt, int64_t rows, int32_t K, int64_t ld,
+                            int32_t block_rows, const void *codes, const void *scales)
+{
+    if (dt != MOE_DT_F32 && dt != MOE_DT_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "%s: val_dtype must be MOE_DT_F32 or MOE_DT_BF16", what);
+    if (block_rows != 1 && block_rows != kFp8Block)
+        return fail(MOE_ERR_INVALID_ARG, "%s: block_rows must be 1 or 128", what);
+    if (rows < 0 || K <= 0 || ld < K) return fail(MOE_ERR_INVALID_ARG, "%s: bad sizes", what);
+    if (K % 64 != 0) return fail(MOE_ERR_UNSUPPORTED, "%s: K must be a multiple of 64", what);
+    // at most 2^32 - 1 threads a launch: 16 for each block of a row, 256 for each of a matrix
+    if (rows > ((int64_t)1 << 33) / K) return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^33 values", what);
+    if (rows > 0 && (!v || !codes || !scales)) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    const int esz = dt == MOE_DT_F32 ? 4 : 2;
+    if (!aligned(v, 16) || (ld * esz) % 16 != 0 || !aligned(codes, 16) || !aligned(scales, block_rows == 1 ? 1 : 4))
+        return fail(MOE_ERR_INVALID_ARG, "%s: values, their row stride and codes must be 16-byte aligned, fp32 scales "
+                                         "4-byte", what);
+    return MOE_OK;
+}
+
+// What the two products have in common; N: rows of a weight slice. With *work
+// false there is nothing to do.
+moe_status check_fp8_product(const char *what, int32_t M, int32_t N, int32_t K, const void *A, const void *As,
+                             int32_t A_rows, const int32_t *row_index, const int32_t *slot_offset, int32_t P,
+                             int64_t B_stride, int64_t Bs_stride, bool *work)
+{
+    *work = false;
+    if (M < 0 || N <= 0 || K <= 0 || A_rows < 0 || P < 1 || P > kMaxExp)
+        return fail(MOE_ERR_INVALID_ARG, "%s: bad sizes M=%d N=%d K=%d A_rows=%d P=%d", what, M, N, K, A_rows, P);
+    if (N % 64 != 0 || K % 64 != 0) return fail(MOE_ERR_UNSUPPORTED, "%s: the weights' sizes must be multiples of 64", what);
+    if (K > MOE_FP8_MAX_K) return fail(MOE_ERR_UNSUPPORTED, "%s: K above %d", what, MOE_FP8_MAX_K);
+    if (!slot_offset && P != 1) return fail(MOE_ERR_INVALID_ARG, "%s: slot_offset is required for P > 1", what);
+    if (M == 0) return MOE_OK;
+    if (A_rows < 1 || (!row_index && A_rows < M)) return fail(MOE_ERR_INVALID_ARG, "%s: A has too few rows", what);
+    if (!A || !As) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    if (!aligned(A, 16) || !aligned(As, 16)) return fail(MOE_ERR_INVALID_ARG, "%s: A and its scales must be 16-byte aligned", what);
+    if (P > 1 && (B_stride < (int64_t)N * K || B_stride % 16 != 0 || Bs_stride < fp8_blocks(N) * fp8_blocks(K)))
+        return fail(MOE_ERR_INVALID_ARG, "%s: the strides must hold a slice, that of the codes in whole 16 bytes", what);
+    // 1024 threads per 16 records x 128 units, at most 2^32 - 1 threads a launch
+    if (((int64_t)M / 16 + P + 1) * (N / 64) >= (1 << 22)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", what);
+    *work = true;
+    return MOE_OK;
+}
+
+Fp8Args fp8_args(int32_t M, int32_t N, int32_t K, const void *A, const void *As, int32_t A_rows, const int32_t *row_index,
+                 const int32_t *slot_offset, int32_t P, int64_t B_stride, int64_t Bs_stride)
+{
+    Fp8Args a{};
+    a.A = (const uint8_t *)A;
+    a.As = (const uint8_t *)As;
+    a.A_rows = A_rows;
+    a.row_index = row_index;
+    a.slot_offset = slot_offset;
+    a.P = P;
+    a.B_stride = P > 1 ? B_stride : 0;
+    a.Bs_stride = P > 1 ? Bs_stride : 0;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_quantize_fp8(const void *values, int32_t val_dtype, int64_t rows, int32_t K, int64_t ld,
+                            int32_t block_rows, void *codes, void *scales, moe_stream stream)
+{
+    MOE_TRY(check_fp8_values("quantize", values, val_dtype, rows, K, ld, block_rows, codes, scales));
+    HIP_TRY(launch_quantize_fp8(values, val_dtype == MOE_DT_BF16, rows, K, ld, block_rows, (uint8_t *)codes, scales,
+                                S(stream)),
+            "quantize launch");
+    return MOE_OK;
+}
+
+moe_status moe_dequantize_fp8(const void *codes, const void *scales, int64_t rows, int32_t K, int32_t block_rows,
+                              void *values, int32_t val_dtype, int64_t ld, moe_stream stream)
+{
+    MOE_TRY(check_fp8_values("dequantize", values, val_dtype, rows, K, ld, block_rows, codes, scales));
+    HIP_TRY(launch_dequantize_fp8((const uint8_t *)codes, scales, rows, K, block_rows, values, val_dtype == MOE_DT_BF16,
+                                  ld, S(stream)),
+            "dequantize launch");
+    return MOE_OK;
+}
+
+moe_status moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void *A_codes, const void *A_scales, int32_t A_rows,
+                          const int32_t *row_index, const int32_t *slot_offset, int32_t P, const void *B_codes,
+                          const float *B_scales, int64_t B_stride, int64_t B_scale_stride, void *C, int32_t c_dtype,
+                          int64_t ldc, moe_stream stream)
+{
+    if (c_dtype != MOE_DT_F32 && c_dtype != MOE_DT_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "matmul: c_dtype must be MOE_DT_F32 or MOE_DT_BF16");
+    if (ldc < N) return fail(MOE_ERR_INVALID_ARG, "matmul: ldc below N");
+    bool work;
+    MOE_TRY(check_fp8_product("matmul", M, N, K, A_codes, A_scales, A_rows, row_index, slot_offset, P, B_stride,
+                              B_scale_stride, &work));
+    if (!work) return MOE_OK;
+    if (!B_codes || !B_scales || !C) return fail(MOE_ERR_INVALID_ARG, "matmul: NULL pointer");
+    const int esz = c_dtype == MOE_DT_F32 ? 4 : 2;
+    if (!aligned(B_codes, 16) || !aligned(B_scales, 4) || !aligned(C, 16) || (ldc * esz) % 16 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "matmul: B, C and C's row stride must be 16-byte aligned");
+    // 256 rows of C are one buffer of the ring kernel
+    if (ldc > ((int64_t)1 << 31) / 256 / 4 - 1) return fail(MOE_ERR_UNSUPPORTED, "matmul: ldc too large");
+    Fp8Args a = fp8_args(M, N, K, A_codes, A_scales, A_rows, row_index, slot_offset, P, B_stride, B_scale_stride);
+    a.B[0] = a.B[1] = (const uint8_t *)B_codes;
+    a.Bs[0] = a.Bs[1] = B_scales;
+    a.C = C;
+    a.c_bf16 = c_dtype == MOE_DT_BF16;
+    a.ldc = ldc;
+    HIP_TRY(launch_matmul_fp8(a, S(stream)), "matmul launch");
+    return MOE_OK;
+}
+
+moe_status moe_gate_up_fp8(int32_t M, int32_t f, int32_t K, const void *A_codes, const void *A_scales, int32_t A_rows,
+                           const int32_t *row_index, const int32_t *slot_offset, int32_t P, const void *Wg_codes,
+                           const float *Wg_scales, const void *Wu_codes, const float *Wu_scales, int64_t W_stride,
+                           int64_t W_scale_stride, void *H_codes, void *H_scales, moe_stream stream)
+{
+    bool work;
+    MOE_TRY(check_fp8_product("gate/up", M, f, K, A_codes, A_scales, A_rows, row_index, slot_offset, P, W_stride,
+                              W_scale_stride, &work));
+    if (!work) return MOE_OK;
+    if (!Wg_codes || !Wg_scales || !Wu_codes || !Wu_scales || !H_codes || !H_scales)
+        return fail(MOE_ERR_INVALID_ARG, "gate/up: NULL pointer");
+    if (!aligned(Wg_codes, 16) || !aligned(Wu_codes, 16) || !aligned(Wg_scales, 4) || !aligned(Wu_scales, 4) ||
+        !aligned(H_codes, 16))
+        return fail(MOE_ERR_INVALID_ARG, "gate/up: the weights and H must be 16-byte aligned, the weights' scales 4-byte");
+    Fp8Args a = fp8_args(M, f, K, A_codes, A_scales, A_rows, row_index, slot_offset, P, W_stride, W_scale_stride);
+    a.B[0] = (const uint8_t *)Wg_codes;
+    a.B[1] = (const uint8_t *)Wu_codes;
+    a.Bs[0] = Wg_scales;
+    a.Bs[1] = Wu_scales;
+    a.C = H_codes;
+    a.Hs = (uint8_t *)H_scales;
+    HIP_TRY(launch_gate_up_fp8(a, S(stream)), "gate/up launch");
+    return MOE_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// the combine of record rows, the balance loss and the router's gradient
+
+namespace {
+
+moe_status check_combine(const char *what, int32_t T, int32_t d, int32_t kp, int32_t M, const void *C, int32_t c_dtype,
+                         int64_t ldc, const int32_t *route_pos, const float *topk_w, const float *Y, int64_t ldy,
+                         CombineArgs *a)
+{
+    if (T < 0 || d <= 0 || M < 0) return fail(MOE_ERR_INVALID_ARG, "%s: bad sizes T=%d d=%d M=%d", what, T, d, M);
+    if (kp < 1 || kp > 64) return fail(MOE_ERR_INVALID_ARG, "%s: need 1 <= K' <= 64", what);
+    if (c_dtype != MOE_DT_F32 && c_dtype != MOE_DT_BF16)
+        return fail(MOE_ERR_INVALID_ARG, "%s: c_dtype must be MOE_DT_F32 or MOE_DT_BF16", what);
+    if (d % 4 != 0 || d > MOE_COMBINE_MAX_D)
+        return fail(MOE_ERR_UNSUPPORTED, "%s: d must be a multiple of 4 and at most %d", what, MOE_COMBINE_MAX_D);
+    if (ldc < d || ldy < d || ldc % 4 != 0 || ldy % 4 != 0)
+        return fail(MOE_ERR_INVALID_ARG, "%s: row strides must be at least d and multiples of 4", what);
+    // a workgroup of 256 threads per token and 1024 columns, at most 2^32 - 1 threads a launch
+    if ((int64_t)T * ((d + 1023) / 1024) >= (1 << 24)) return fail(MOE_ERR_UNSUPPORTED, "%s: T * ceil(d / 1024) must be below 2^24", what);
+    if (T > 0 && (!route_pos || !topk_w || !Y || (M > 0 && !C))) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
+    if (!aligned(Y, 16) || !aligned(C, c_dtype == MOE_DT_F32 ? 16 : 8))
+        return fail(MOE_ERR_INVALID_ARG, "%s: Y and fp32 rows must be 16-byte aligned, bf16 rows 8-byte", what);
+    *a = CombineArgs{};
+    a->T = T;
+    a->d = d;
+    a->kp = kp;
+    a->M = M;
+    a->C = C;
+    a->c_bf16 = c_dtype == MOE_DT_BF16;
+    a->ldc = ldc;
+    a->route_pos = route_pos;
+    a->topk_w = topk_w;
+    a->ldy = ldy;
+    return MOE_OK;
+}
+
+moe_status check_sequences(const char *what, const int32_t *seq_offset, int32_t S)
+{
+    if (S < 1 || S > kMaxSeq) return fail(MOE_ERR_INVALID_ARG, "%s: need 1 <= S <= %d", what, kMaxSeq);
+    if (!seq_offset && S != 1) return fail(MOE_ERR_INVALID_ARG, "%s: seq_offset is required for S > 1", what);
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_combine(int32_t T, int32_t d, int32_t kp, int32_t M, const void *C, int32_t c_dtype, int64_t ldc,
+                       const int32_t *route_pos, const float *topk_w, float *Y, int64_t ldy, moe_stream stream)
+{
+    CombineArgs a;
+    MOE_TRY(check_combine("combine", T, d, kp, M, C, c_dtype, ldc, route_pos, topk_w, Y, ldy, &a));
+    a.Y = Y;
+    HIP_TRY(launch_combine_rows(a, S(stream)), "combine launch");
+    return MOE_OK;
+}
+
+moe_status moe_combine_backward(int32_t T, int32_t d, int32_t kp, int32_t M, const void *C, int32_t c_dtype, int64_t ldc,
+                                const int32_t *route_pos, const float *topk_w, const float *dY, int64_t ldy, void *dC,
+                                int64_t lddc, float *d_topk_w, moe_stream stream)
+{
+    CombineArgs a;
+    MOE_TRY(check_combine("combine backward", T, d, kp, M, C, c_dtype, ldc, route_pos, topk_w, dY, ldy, &a));
+    if (T > 0 && !d_topk_w) return fail(MOE_ERR_INVALID_ARG, "combine backward: NULL pointer");
+    if (dC && (lddc < d || lddc % 4 != 0 || !aligned(dC, c_dtype == MOE_DT_F32 ? 16 : 8)))
+        return fail(MOE_ERR_INVALID_ARG, "combine backward: dC needs rows as C's");
+    a.dY = dY;
+    a.dC = dC;
+    a.lddc = lddc;
+    a.dw = d_topk_w;
+    HIP_TRY(launch_combine_rows_backward(a, S(stream)), "combine backward launch");
+    return MOE_OK;
+}
+
+size_t moe_balance_workspace_bytes(const moe_shape *shape, int32_t S)
+{
+    if (check_shape(shape) != MOE_OK || check_sequences("balance", (const int32_t *)1, S) != MOE_OK) return 0;
+    return balance_layout(shape->T, shape->E, S).total;
+}
+
+moe_status moe_balance_loss(const moe_shape *shape, const float *logits, const int32_t *topk_idx,
+                            const int32_t *seq_offset, int32_t S_, const uint8_t *mask, float *loss, int32_t *counts,
+                            float *prob, float *slope, void *ws, size_t ws_bytes, moe_stream stream)
+{
+    MOE_TRY(check_shape(shape));
+    MOE_TRY(check_sequences("balance", seq_offset, S_));
+    if (!loss || !counts || !prob || !slope || (shape->T > 0 && (!logits || !topk_idx)))
+        return fail(MOE_ERR_INVALID_ARG, "balance: NULL pointer");
+    const BalanceLayout w = balance_layout(shape->T, shape->E, S_);
+    if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (!aligned(ws, 256)) return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < w.total) return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu < %zu", ws_bytes, w.total);
+    BalanceArgs a{};
+    a.T = shape->T;
+    a.E = shape->E;
+    a.k = shape->k;
+    a.kp = shape->k + shape->n_shared;
+    a.logits = logits;
+    a.idx = topk_idx;
+    a.seq_offset = seq_offset;
+    a.S = S_;
+    a.mask = mask;
+    a.loss = loss;
+    a.counts = counts;
+    a.prob = prob;
+    a.slope = slope;
+    HIP_TRY(launch_balance(a, w, ws, S(stream)), "balance launch");
+    return MOE_OK;
+}
+
+moe_status moe_router_backward(const moe_shape *shape, const float *logits, const int32_t *topk_idx, const float *slope,
+                               const float *d_loss, const int32_t *seq_offset, int32_t S_, const uint8_t *mask,
+                               const float *d_topk_w, float *d_logits, moe_stream stream)
+{
+    MOE_TRY(check_shape(shape));
+    MOE_TRY(check_sequences("router backward", seq_offset, S_));
+    if (!slope && !d_topk_w) return fail(MOE_ERR_INVALID_ARG, "router backward: give slope, d_topk_w or both");
+    if (shape->T > 0 && (!logits || !d_logits || (d_topk_w && !topk_idx)))
+        return fail(MOE_ERR_INVALID_ARG, "router backward: NULL pointer");
+    RouterBackArgs a{};
+    a.T = shape->T;
+    a.E = shape->E;
+    a.k = shape->k;
+    a.kp = shape->k + shape->n_shared;
+    a.renorm = shape->renorm;
+    a.logits = logits;
+    a.idx = topk_idx;
+    a.seq_offset = seq_offset;
+    a.S = S_;
+    a.mask = mask;
+    a.slope = slope;
+    a.d_loss = d_loss;
+    a.dw = d_topk_w;
+    a.dlogits = d_logits;
+    HIP_TRY(launch_router_backward(a, S(stream)), "router backward launch");
     return MOE_OK;
 }
 

@@ -1,0 +1,80 @@
+// Internal declarations: the combine of record rows with its gradients, the
+// balance loss and the gradient of the router's logits.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+
+struct CombineArgs {
+    int T, d, kp, M;
+    const void *C;               // rows in record order [M][ldc], bf16 or fp32
+    int c_bf16;
+    int64_t ldc;
+    const int32_t *route_pos;    // [T*kp]: record of a route, or outside [0, M)
+    const float *topk_w;         // [T*kp]
+    float *Y;                    // forward: [T][ldy], in place
+    const float *dY;             // backward
+    int64_t ldy;
+    void *dC;                    // backward: rows as C's, or null
+    int64_t lddc;
+    float *dw;                   // backward: [T*kp]
+};
+hipError_t launch_combine_rows(const CombineArgs &a, hipStream_t st);
+hipError_t launch_combine_rows_backward(const CombineArgs &a, hipStream_t st);
+
+constexpr int kMaxSeq = 4096;    // sequences of a balance call
+
+struct BalanceArgs {
+    int T, E, k, kp, renorm;
+    const float *logits;         // [T][E]
+    const int32_t *idx;          // [T][kp]
+    const int32_t *seq_offset;   // [S+1] or null (S == 1: every token)
+    int S;
+    const uint8_t *mask;         // [T] or null
+    float *loss;                 // [1]
+    int32_t *counts;             // [S][E]
+    float *prob, *slope;         // [S][E]
+};
+struct BalanceLayout {
+    size_t chunk;   // int32[V][2]: sequence of a chunk (-1: none), tokens counted
+    size_t count;   // int32[V][E]
+    size_t prob;    // float[V][E]
+    size_t part;    // double[S][ceil(E/32)]
+    size_t ticket;  // uint32
+    size_t total;
+    int ch, V;      // tokens a chunk, chunks at most
+};
+// Tokens a chunk: a chunk is what a workgroup sums, 4 waves of its tokens each.
+// 1024 chunks and more fill the GPU; the sums over the chunks follow.
+inline BalanceLayout balance_layout(int64_t T, int E, int S)
+{
+    BalanceLayout w{};
+    w.ch = T <= 16384 ? 16 : T <= 65536 ? 64 : 256;
+    w.V = (int)((T + w.ch - 1) / w.ch + S);
+    size_t o = 0;
+    w.chunk = o;  o = align_up(o + (size_t)w.V * 8, 256);
+    w.count = o;  o = align_up(o + (size_t)w.V * E * 4, 256);
+    w.prob = o;   o = align_up(o + (size_t)w.V * E * 4, 256);
+    w.part = o;   o = align_up(o + (size_t)S * ((E + 31) / 32) * 8, 256);
+    w.ticket = o; o = align_up(o + 4, 256);
+    w.total = o;
+    return w;
+}
+hipError_t launch_balance(const BalanceArgs &a, const BalanceLayout &w, void *ws, hipStream_t st);
+
+struct RouterBackArgs {
+    int T, E, k, kp, renorm;
+    const float *logits;
+    const int32_t *idx;
+    const int32_t *seq_offset;
+    int S;
+    const uint8_t *mask;
+    const float *slope;          // [S][E] or null
+    const float *d_loss;         // [1] or null (1)
+    const float *dw;             // [T][kp] or null
+    float *dlogits;              // [T][E]
+};
+hipError_t launch_router_backward(const RouterBackArgs &a, hipStream_t st);
+
+}  // namespace moe

@@ -12,6 +12,7 @@
 // is a normal fp32 number. A block that holds an infinity or a NaN gets the
 // scale NaN (byte 255) and codes 0.
 #include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "fp8.h"
@@ -38,6 +39,12 @@ __device__ __forceinline__ float block_unit(uint32_t byte)
 __device__ __forceinline__ float block_value(uint32_t byte)
 {
     return __uint_as_float(byte == 255 ? 0x7fc00000u : byte << 23);
+}
+
+// 2^(e - 127) of an exponent field; 0: 2^-127, 255: NaN.
+__device__ __forceinline__ float exponent_value(int e)
+{
+    return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7fc00000u : (uint32_t)e << 23);
 }
 
 // 8 consecutive values as fp32.
@@ -372,6 +379,407 @@ __global__ __launch_bounds__(1024) void k_gate_up_few(Fp8Args a)
     if (lane == 0) a.Hs[p * fp8_scale_bytes(a.N) + f0 / kFp8Block] = (uint8_t)byte;
 }
 
+// ---------------------------------------------------------------------------
+// Many records a slot: a persistent ring kernel. Tile 256 records x 256 weight
+// rows, one stage = 64 k: 256 rows of 64 code bytes of each side, copied straight
+// into LDS (16 bytes a lane), NS stages deep; 8 waves as 2 x 4. Wave row wm takes
+// the 32-record blocks wm, wm + 2, ..., so that a tile with fewer records takes
+// less time (MI blocks a wave, 1 to 4). Rows are stored with their 16-byte chunk c
+// at c ^ ((row >> 2) & 3), which keeps the fragment reads free of bank conflicts.
+// The scales come in panels of 2048 k: 16 bytes a record, 16 numbers for each of
+// the tile's two blocks of 128 weight rows.
+//
+// The records' scales, powers of two, are operands of the matrix instruction. So
+// are the powers of two of the weights' scales m 2^e, 1 <= |m| < 2; the m are
+// brought in by holding the sums in units of the current one: before the first
+// multiply of a block of k the sums are multiplied by m_last / m, at most 2 in
+// magnitude, so nothing overflows on the way, and at the end by the last m. Where
+// the weights' scales are powers of two there is nothing to multiply.
+//
+// EPI: STORE: C, rounded to its type. With DEC (fp32 C) the codes are decoded to
+// bf16 when they leave LDS. GATE_UP: the tile's weight rows are 128 of gate and
+// the 128 of up; the operands change places, so that a lane holds 16 units of one
+// record, H's blocks are the tile's 128 units, their maxima joined over the four
+// waves through LDS.
+constexpr int kXcd = 8;
+constexpr int kStream = 2;   // buffer stores of C, which is not read here: non-temporal
+enum { EPI_STORE = 0, EPI_GATE_UP = 1 };
+
+// A weight scale as m and the bits of 2^e; below 2^-126 as +-2^-127, NaN and infinity as NaN.
+__device__ __forceinline__ float scale_m(float s)
+{
+    const uint32_t u = __float_as_uint(s);
+    const uint32_t e = u & 0x7f800000u;
+    return __uint_as_float(e == 0 || e == 0x7f800000u ? (u & 0x80000000u) | 0x3f800000u : (u & 0x807fffffu) | 0x3f800000u);
+}
+__device__ __forceinline__ int scale_e(float s) { return (int)((__float_as_uint(s) >> 23) & 255u); }
+
+template <int EPI, bool DEC>
+__global__ __launch_bounds__(512) void k_ring(Fp8Args a)
+{
+    constexpr int BM = 256, NS = 4, WN = 4, NI = 2, MI = 4;
+    constexpr int CODES = 256 * 64, STAGE = 2 * CODES;   // bytes: one side, both
+    constexpr int LOADS = 4;                              // copies a wave and stage
+    constexpr int APANEL = BM * 16, BPANEL = 2 * 64, PANEL = APANEL + BPANEL;
+    __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE + 2 * PANEL];
+    __shared__ int32_t s_tpref[kMaxExp + 1], s_lo[kMaxExp], s_cnt[kMaxExp];
+    __shared__ int32_t s_rows[3][BM];   // the rows of A of three tiles' records, this one, the next and the one after it
+    __shared__ u32x4_t s_top[EPI == EPI_GATE_UP ? BM : 1];
+    char *const panels = lds + NS * STAGE;
+    const uint32_t lds_at = lds_address(lds), panels_at = lds_at + NS * STAGE, rows_at = lds_address(s_rows);
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN, half = lane >> 5;
+    const int K = a.K, N = a.N, P = a.P, KB = (K + kFp8Block - 1) / kFp8Block;
+    constexpr int BN = EPI == EPI_GATE_UP ? 128 : 256;
+    const int ntn = (N + BN - 1) / BN;
+    if (tid < 64) {
+        int run = 0;
+        for (int s0 = 0; s0 < P; s0 += 64) {
+            const int s = s0 + lane;
+            int lo = 0, hi = 0;
+            if (s < P) slot_range(a, s, &lo, &hi);
+            const int w = (hi - lo + BM - 1) / BM * ntn;
+            const int inc = run + wave_incl_scan(w, lane);
+            if (s < P) {
+                s_tpref[s] = inc - w;
+                s_lo[s] = lo;
+                s_cnt[s] = hi - lo;
+            }
+            run = __shfl(inc, 63, 64);
+        }
+        if (lane == 0) s_tpref[P] = run;
+    }
+    __syncthreads();
+    const int total = s_tpref[P];
+    const int xcd = blockIdx.x % kXcd, li = blockIdx.x / kXcd;
+    const int nwg = ((int)gridDim.x - xcd + kXcd - 1) / kXcd;
+    const int qx = total / kXcd, rx = total % kXcd;
+    const int cnt_x = qx + (xcd < rx ? 1 : 0), start_x = xcd * qx + min(xcd, rx);
+    if (li >= cnt_x) return;
+
+    struct Tile {
+        int slot, row0, rows, n0;
+    };
+    auto decode = [&](int L) -> Tile {
+        int lo = 0, hi = P - 1;   // last slot whose first tile is <= L (skips empty slots)
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_tpref[mid] <= L) lo = mid; else hi = mid - 1;
+        }
+        const int mt = (s_cnt[lo] + BM - 1) / BM, local = L - s_tpref[lo], ml = local % mt;
+        Tile t;   // the same in every lane
+        t.slot = __builtin_amdgcn_readfirstlane(lo);
+        t.row0 = __builtin_amdgcn_readfirstlane(s_lo[lo] + ml * BM);
+        t.rows = __builtin_amdgcn_readfirstlane(min(BM, s_cnt[lo] - ml * BM));
+        t.n0 = __builtin_amdgcn_readfirstlane((local / mt) * BN);
+        return t;
+    };
+
+    // Copies of this wave: rows 32 wave + 16 j .. +15 of both sides (lane: row + l/4,
+    // chunk position l % 4); of a panel, waves 0-3 the records 64 wave .. +63, wave 4
+    // the weights' scales.
+    const char *asrc[2], *bbase, *ssrc = nullptr;   // bbase: the same in every lane
+    uint32_t boff[2];
+    // A tile's rows to LDS. No register waits for them: a load into one
+    // would be waited for with everything requested after it.
+    auto fetch_rows = [&](const Tile &t, int buf) {
+        if (a.row_index && wave < BM / 64)
+            copy_to_lds<4>(a.row_index + t.row0 + min(wave * 64 + lane, t.rows - 1), rows_at + (buf * BM + wave * 64) * 4);
+    };
+    auto row_in = [&](const Tile &t, int buf, int i) {
+        const int r = min(i, t.rows - 1);
+        return a.row_index ? min(max(s_rows[buf][r], 0), a.A_rows - 1) : t.row0 + r;
+    };
+    auto set_sources = [&](const Tile &t, int buf) {
+        const int side = EPI == EPI_GATE_UP ? wave >> 2 : 0;
+        const int64_t first = EPI == EPI_GATE_UP ? t.n0 + (wave & 3) * 32 : t.n0 + wave * 32;
+        bbase = (const char *)a.B[side] + t.slot * a.B_stride;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = j * 16 + (lane >> 2), sw = ((lane & 3) ^ ((r >> 2) & 3)) * 16;
+            asrc[j] = (const char *)a.A + (int64_t)row_in(t, buf, wave * 32 + r) * K + sw;
+            boff[j] = (uint32_t)(min((int)first + r, N - 1) - t.n0) * (uint32_t)K + sw;
+        }
+        bbase += (int64_t)t.n0 * K;
+        if (wave < 4) {
+            ssrc = (const char *)a.As + row_in(t, buf, wave * 64 + lane) * fp8_scale_bytes(K);
+        } else if (wave == 4) {
+            const int b = (lane >> 4) & 1, nbs = (N + kFp8Block - 1) / kFp8Block;
+            const int nb = min(t.n0 / kFp8Block + (EPI == EPI_GATE_UP ? 0 : b), nbs - 1);
+            ssrc = (const char *)(a.Bs[EPI == EPI_GATE_UP ? b : 0] + t.slot * a.Bs_stride + (int64_t)nb * KB);
+        }
+    };
+    const int nk = K / 64;
+    auto issue_panel = [&](int pn) {
+        const uint32_t at = panels_at + (pn & 1) * PANEL;
+        if (wave < 4)
+            copy_to_lds<16>(ssrc + pn * 16, at + wave * 1024);
+        else if (wave == 4 && lane < 32)
+            copy_to_lds<4>(ssrc + 4 * min(pn * 16 + (lane & 15), KB - 1), at + APANEL);
+    };
+    auto issue = [&](int kt) {
+        const uint32_t st = lds_at + (kt % NS) * STAGE + wave * 2048;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) copy_to_lds<16>(asrc[j] + kt * 64, st + j * 1024);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) copy_to_lds(bbase + kt * 64, boff[j], st + CODES + j * 1024);
+        if ((kt & 31) == 16 && kt + 16 < nk) issue_panel(kt / 32 + 1);
+    };
+
+    const int sw = ((lane & 31) >> 2) & 3;
+    const int foff[2] = {(lane & 31) * 64 + ((2 * half) ^ sw) * 16, (lane & 31) * 64 + ((2 * half + 1) ^ sw) * 16};
+    auto cblock = [&](int j) { return EPI == EPI_GATE_UP ? wn + 4 * j : 2 * wn + j; };
+    f32x16_t acc[MI][NI];
+    i32x8_t af[2], bf[2][NI];   // records' blocks in turn, weights of this stage and the next
+    int sa[MI];                 // scale bytes of this lane's records, current block of k
+    float sm[NI];               // m of the weights' scales, current block of k
+    int se[NI];
+    auto frag = [&](const char *p) {
+        const u32x4_t lo = *(const u32x4_t *)(p + foff[0]), hi = *(const u32x4_t *)(p + foff[1]);
+        return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    };
+    auto a_frag = [&](int kt, int i) { return frag(lds + (kt % NS) * STAGE + (2 * i + wm) * 2048); };
+    auto b_frag = [&](int kt, int j) { return frag(lds + (kt % NS) * STAGE + CODES + cblock(j) * 2048); };
+    // scales of block kb of k; the factors that bring the sums into its units
+    auto read_scales = [&](auto mi, int kb, float (&ratio)[NI]) {
+        const char *p = panels + (kb / 16 & 1) * PANEL;
+#pragma unroll
+        for (int i = 0; i < decltype(mi)::value; ++i) sa[i] = *(const uint8_t *)(p + ((2 * i + wm) * 32 + (lane & 31)) * 16 + (kb & 15));
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            const float s = *(const float *)(p + APANEL + (EPI == EPI_GATE_UP ? j : wn >> 1) * 64 + (kb & 15) * 4);
+            const float m = scale_m(s);
+            ratio[j] = m == sm[j] ? 1.0f : sm[j] / m;
+            sm[j] = m;
+            se[j] = scale_e(s);
+        }
+    };
+    // One stage: block i's multiplies, and before them the reads of the next block.
+    auto stage = [&](auto mi, auto set_t, auto scaled, int kt, const float (&ratio)[NI]) {
+        constexpr int n = decltype(mi)::value, set = decltype(set_t)::value;
+        bf16x8_t Bv[DEC ? NI : 1][4];
+        if constexpr (DEC)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) decode32(bf[set][j], exponent_value(se[j]), Bv[j]);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const int cur = (n & 1 ? set + i : i) & 1;
+            if (i + 1 < n) {
+                af[cur ^ 1] = a_frag(kt, i + 1);
+            } else {   // past the last stage: a resident one, not used
+                af[cur ^ 1] = a_frag(kt + 1, 0);
+#pragma unroll
+                for (int j = 0; j < NI; ++j) bf[set ^ 1][j] = b_frag(kt + 1, j);
+            }
+            if constexpr (decltype(scaled)::value)
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][j][r] *= ratio[j];
+            if constexpr (DEC) {
+                bf16x8_t Av[4];
+                decode32(af[cur], block_value(sa[i]), Av);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(Av[t], Bv[j][t], acc[i][j], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+                    acc[i][j] = EPI == EPI_GATE_UP
+                                    ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[set][j], af[cur], acc[i][j], 0, 0, 0, se[j], 0, sa[i])
+                                    : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(af[cur], bf[set][j], acc[i][j], 0, 0, 0, sa[i], 0, se[j]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
+    // A tile's first requests: rows of the tile after it, the first panel, the
+    // first stages.
+    auto begin = [&](const Tile &after, int after_buf) {
+        fetch_rows(after, after_buf);
+        issue_panel(0);
+#pragma unroll
+        for (int p = 0; p < NS - 1; ++p)
+            if (p < nk) issue(p);
+    };
+
+    // At the top of step kt stage kt is visible to every wave, and this wave
+    // holds its fragments. Stage kt + 1 is made visible (own copies waited for,
+    // unless it is one of the first, then a barrier) and stage kt + NS - 1
+    // requested into the slot of stage kt - 1, which every wave finished before that
+    // barrier. Loads return in order: stage kt + 1 is there once no more than the
+    // copies of the next one are outstanding.
+    auto top = [&](int kt) {
+        if (kt + 1 < nk) {
+            if (kt + 1 >= NS - 1) wait_vmcnt_stages<LOADS, NS - 3>(min(NS - 3, nk - 2 - kt));
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");   // for the compiler: reads stay behind
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
+        if (kt + NS - 1 < nk) issue(kt + NS - 1);
+    };
+    auto tile_loop = [&](auto mi) {
+        constexpr int n = decltype(mi)::value;
+        if constexpr (n > 0) {
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NI; ++j) sm[j] = 1.0f;
+            af[0] = a_frag(0, 0);
+#pragma unroll
+            for (int j = 0; j < NI; ++j) bf[0][j] = b_frag(0, j);
+        }
+        // whole blocks of k, then half a one
+        float ratio[NI] = {1.0f, 1.0f};
+        const int whole = nk & ~1;
+        for (int kt = 0; kt < whole; kt += 2) {
+            top(kt);
+            if constexpr (n > 0) {
+                read_scales(mi, kt / 2, ratio);
+                stage(mi, std::integral_constant<int, 0>(), std::true_type(), kt, ratio);
+            }
+            top(kt + 1);
+            if constexpr (n > 0) stage(mi, std::integral_constant<int, 1>(), std::false_type(), kt + 1, ratio);
+        }
+        if (nk & 1) {
+            top(whole);
+            if constexpr (n > 0) {
+                read_scales(mi, whole / 2, ratio);
+                stage(mi, std::integral_constant<int, 0>(), std::true_type(), whole, ratio);
+            }
+        }
+    };
+
+    int tl = li, buf = 0;
+    Tile cur = decode(start_x + tl), nxt = tl + nwg < cnt_x ? decode(start_x + tl + nwg) : cur;
+    fetch_rows(cur, 0);
+    wait_vmcnt<0>();
+    __syncthreads();
+    set_sources(cur, 0);
+    begin(nxt, 1);
+    for (;;) {
+        const int tn = tl + nwg;
+        const bool has_next = tn < cnt_x;
+        const Tile after = tn + nwg < cnt_x ? decode(start_x + tn + nwg) : nxt;
+        const int mine = (cur.rows + 31) / 32 - wm + 1 >> 1;   // blocks of this wave
+        // The first stages, and the last tile's stores.
+        wait_vmcnt<0>();
+        lds_barrier();
+        if (mine > 2) tile_loop(std::integral_constant<int, 4>());
+        else if (mine > 0) tile_loop(std::integral_constant<int, 2>());
+        else tile_loop(std::integral_constant<int, 0>());
+        const Tile done = cur;
+        if (has_next) {
+            lds_barrier();   // nothing reads the ring any more
+            const int nb = buf == 2 ? 0 : buf + 1;
+            set_sources(nxt, nb);
+            begin(after, nb == 2 ? 0 : nb + 1);
+        }
+        if constexpr (EPI == EPI_GATE_UP) {
+            // register r of lane l: unit 32 wn + 8 (r / 4) + 4 (l / 32) + r % 4 of record l % 32 of the block
+            const bool in = done.n0 + wn * 32 < N;
+            uint32_t *tops = (uint32_t *)s_top;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                if (i >= mine) continue;
+                uint32_t t = 0;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float h = in ? swiglu(acc[i][0][r] * sm[0], acc[i][1][r] * sm[1]) : 0.0f;
+                    acc[i][0][r] = h;
+                    t = max(t, __float_as_uint(h) & 0x7fffffffu);
+                }
+                t = max(t, (uint32_t)__shfl_xor((int)t, 32, 64));
+                if (half == 0) tops[((2 * i + wm) * 32 + lane) * 4 + wn] = t;
+            }
+            lds_barrier();
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                if (i >= mine) continue;
+                const int m = (2 * i + wm) * 32 + (lane & 31);
+                const u32x4_t t = s_top[m];
+                const uint32_t byte = block_byte(max(max(t[0], t[1]), max(t[2], t[3])));
+                const float unit = block_unit(byte);
+                uint32_t q[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const f32x16_t &h = acc[i][0];
+                    int w = __builtin_amdgcn_cvt_pk_fp8_f32(h[4 * c] * unit, h[4 * c + 1] * unit, 0, false);
+                    w = __builtin_amdgcn_cvt_pk_fp8_f32(h[4 * c + 2] * unit, h[4 * c + 3] * unit, w, true);
+                    q[c] = byte == 255 ? 0u : (uint32_t)w;
+                }
+                // units 0-15 to the lower half, 16-31 to the upper
+                const uint32_t g0 = (uint32_t)__shfl_xor((int)(half ? q[0] : q[2]), 32, 64);
+                const uint32_t g1 = (uint32_t)__shfl_xor((int)(half ? q[1] : q[3]), 32, 64);
+                const u32x4_t o = half ? u32x4_t{g0, q[2], g1, q[3]} : u32x4_t{q[0], g0, q[1], g1};
+                if (in && m < done.rows) {
+                    *(u32x4_t *)((uint8_t *)a.C + (int64_t)(done.row0 + m) * N + done.n0 + wn * 32 + half * 16) = o;
+                    if (wn == 0 && half == 0) a.Hs[(int64_t)(done.row0 + m) * fp8_scale_bytes(N) + done.n0 / kFp8Block] = (uint8_t)byte;
+                }
+            }
+        } else if (mine > 0 && done.n0 + wn * 64 < N) {
+            // Register r of lane l holds record 8 (r / 4) + 4 (l / 32) + r % 4 and column
+            // l % 32 of its block. bf16: adjacent lanes swap a value of records R, R + 1,
+            // so that each stores two columns of one. The tile's rows of C are a
+            // buffer: stores to rows past its last one are dropped by its bounds
+            // check, so no store has a branch. A wave's 64 columns are all in N or
+            // all past it.
+            constexpr int esz = DEC ? 4 : 2;
+            char *base = (char *)a.C + ((int64_t)done.row0 * a.ldc + done.n0 + wn * 64) * esz;
+            // opaque, or the rows' offsets are computed before the tile loop and held through it
+            uint32_t ld = (uint32_t)a.ldc * esz;
+            asm volatile("" : "+s"(ld));
+            const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(base, 0, (int)(done.rows * ld), 0x00027000);
+            const uint32_t row = wm * 32 + 4 * half;
+            if constexpr (!DEC) {
+                const bool even = (lane & 1) == 0;
+                const uint32_t at = (row + (even ? 0 : 1)) * ld + (lane & 30) * 2;
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    if (i >= mine) continue;
+#pragma unroll
+                    for (int r = 0; r < 16; r += 2) {
+                        const uint32_t o = at + (uint32_t)(i * 64 + 8 * (r / 4) + (r & 3)) * ld;
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) {
+                            const float s0 = acc[i][j][r] * sm[j], s1 = acc[i][j][r + 1] * sm[j];
+                            const float y = __uint_as_float(dpp<0xB1>(__float_as_uint(even ? s1 : s0)));
+                            __builtin_amdgcn_raw_buffer_store_b32(even ? bf16_pair(s0, y) : bf16_pair(y, s1), out,
+                                                                  (int)(o + j * 64), 0, kStream);
+                        }
+                    }
+                }
+            } else {
+                const uint32_t at = row * ld + (lane & 31) * 4;
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    if (i >= mine) continue;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const uint32_t o = at + (uint32_t)(i * 64 + 8 * (r / 4) + (r & 3)) * ld;
+#pragma unroll
+                        for (int j = 0; j < NI; ++j)
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][r] * sm[j]), out, (int)(o + j * 128), 0,
+                                                                  kStream);
+                    }
+                }
+            }
+        }
+        if (!has_next) break;
+        cur = nxt;
+        nxt = after;
+        tl = tn;
+        buf = buf == 2 ? 0 : buf + 1;
+    }
+}
+
 }  // namespace
 
 hipError_t launch_quantize_fp8(const void *src, bool bf16, int64_t rows, int K, int64_t ld, int block_rows,
@@ -415,9 +823,21 @@ hipError_t launch_dequantize_fp8(const uint8_t *codes, const void *scales, int64
 // at most this many row tiles of R records: one partial tile per slot with records
 static int64_t row_tiles(const Fp8Args &a, int R) { return (int64_t)(a.M + R - 1) / R + std::min(a.P, a.M) - 1; }
 
+static bool ring_pays(const Fp8Args &a) { return a.M / std::min(a.P, a.M) >= 32; }
+
+template <int EPI, bool DEC>
+static hipError_t launch_ring(const Fp8Args &a, hipStream_t st)
+{
+    const int64_t cols = EPI == EPI_GATE_UP ? 128 : 256;
+    const unsigned grid = (unsigned)std::min<int64_t>(row_tiles(a, 256) * ((a.N + cols - 1) / cols), 256);   // a workgroup a CU
+    hipLaunchKernelGGL((k_ring<EPI, DEC>), dim3(grid), dim3(512), 0, st, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_matmul_fp8(const Fp8Args &a, hipStream_t st)
 {
     if (a.M == 0) return hipSuccess;
+    if (ring_pays(a)) return a.c_bf16 ? launch_ring<EPI_STORE, false>(a, st) : launch_ring<EPI_STORE, true>(a, st);
     const int64_t grid = row_tiles(a, 16) * (a.N / 64);
     hipLaunchKernelGGL((k_matmul_few<4, 4>), dim3((unsigned)grid), dim3(256), 0, st, a);
     return hipGetLastError();
@@ -426,6 +846,7 @@ hipError_t launch_matmul_fp8(const Fp8Args &a, hipStream_t st)
 hipError_t launch_gate_up_fp8(const Fp8Args &a, hipStream_t st)
 {
     if (a.M == 0) return hipSuccess;
+    if (ring_pays(a)) return launch_ring<EPI_GATE_UP, false>(a, st);
     const int64_t grid = row_tiles(a, 16) * fp8_blocks(a.N);
     hipLaunchKernelGGL(k_gate_up_few, dim3((unsigned)grid), dim3(1024), 0, st, a);
     return hipGetLastError();

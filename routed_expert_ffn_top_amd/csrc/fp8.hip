@@ -380,14 +380,14 @@ __global__ __launch_bounds__(1024) void k_gate_up_few(Fp8Args a)
 }
 
 // ---------------------------------------------------------------------------
-// Many records a slot: a persistent ring kernel. Tile 256 records x 256 weight
-// rows, one stage = 64 k: 256 rows of 64 code bytes of each side, copied straight
-// into LDS (16 bytes a lane), NS stages deep; 8 waves as 2 x 4. Wave row wm takes
-// the 32-record blocks wm, wm + 2, ..., so that a tile with fewer records takes
-// less time (MI blocks a wave, 1 to 4). Rows are stored with their 16-byte chunk c
-// at c ^ ((row >> 2) & 3), which keeps the fragment reads free of bank conflicts.
-// The scales come in panels of 2048 k: 16 bytes a record, 16 numbers for each of
-// the tile's two blocks of 128 weight rows.
+// Many records a slot: a persistent kernel. Tile 256 records x 256 weight rows,
+// one stage = 128 k: 256 rows of 128 code bytes, a whole line, of each side, copied
+// straight into LDS (16 bytes a lane), one stage in use and one on its way; 8 waves as
+// 2 x 4. Wave row wm takes the 32-record blocks wm, wm + 2, ..., so that a tile with
+// fewer records takes less time (2 or 4 blocks a wave). Rows are stored with their
+// 16-byte chunk c at c ^ ((row >> 1) & 7), which keeps the fragment reads free of
+// bank conflicts. The scales come in panels of 2048 k: 16 bytes a record, 16 numbers for
+// each of the tile's two blocks of 128 weight rows.
 //
 // The records' scales, powers of two, are operands of the matrix instruction. So
 // are the powers of two of the weights' scales m 2^e, 1 <= |m| < 2; the m are
@@ -414,15 +414,17 @@ __device__ __forceinline__ float scale_m(float s)
 }
 __device__ __forceinline__ int scale_e(float s) { return (int)((__float_as_uint(s) >> 23) & 255u); }
 
+__device__ __forceinline__ void opaque(f32x16_t &v) { asm volatile("" : "+v"(v)); }
+
 template <int EPI, bool DEC>
 __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
 {
-    constexpr int BM = 256, NS = 4, WN = 4, NI = 2, MI = 4;
-    constexpr int CODES = 256 * 64, STAGE = 2 * CODES;   // bytes: one side, both
-    constexpr int LOADS = 4;                              // copies a wave and stage
+    constexpr int BM = 256, NS = 2, WN = 4, NI = 2, MI = 4;
+    constexpr int CODES = 256 * kFp8Block, STAGE = 2 * CODES;   // bytes: one side, both
     constexpr int APANEL = BM * 16, BPANEL = 2 * 64, PANEL = APANEL + BPANEL;
     __shared__ __attribute__((aligned(1024))) char lds[NS * STAGE + 2 * PANEL];
     __shared__ int32_t s_tpref[kMaxExp + 1], s_lo[kMaxExp], s_cnt[kMaxExp];
+    __shared__ u32x4_t s_tiles[2][64];
     __shared__ int32_t s_rows[3][BM];   // the rows of A of three tiles' records, this one, the next and the one after it
     __shared__ u32x4_t s_top[EPI == EPI_GATE_UP ? BM : 1];
     char *const panels = lds + NS * STAGE;
@@ -460,168 +462,273 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
     if (li >= cnt_x) return;
 
     struct Tile {
-        int slot, row0, rows, n0;
+        int slot, row0, rows, n0;   // the same in every lane
     };
-    auto decode = [&](int L) -> Tile {
+    // Tiles 64 b .. + 63 of this workgroup, a lane each, to LDS. Groups of 8 row tiles, columns
+    // in turn within: what runs at the same time shares both sides' rows.
+    const int tiles = (cnt_x - li + nwg - 1) / nwg;
+    auto list = [&](int b) __attribute__((always_inline)) {
+        const int L = start_x + li + min(64 * b + lane, tiles - 1) * nwg;
         int lo = 0, hi = P - 1;   // last slot whose first tile is <= L (skips empty slots)
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (s_tpref[mid] <= L) lo = mid; else hi = mid - 1;
         }
-        const int mt = (s_cnt[lo] + BM - 1) / BM, local = L - s_tpref[lo], ml = local % mt;
-        Tile t;   // the same in every lane
-        t.slot = __builtin_amdgcn_readfirstlane(lo);
-        t.row0 = __builtin_amdgcn_readfirstlane(s_lo[lo] + ml * BM);
-        t.rows = __builtin_amdgcn_readfirstlane(min(BM, s_cnt[lo] - ml * BM));
-        t.n0 = __builtin_amdgcn_readfirstlane((local / mt) * BN);
-        return t;
+        const int cnt = s_cnt[lo], mt = (cnt + BM - 1) / BM, group = (L - s_tpref[lo]) / (8 * ntn);
+        const int local = (L - s_tpref[lo]) % (8 * ntn), high = min(8, mt - 8 * group), ml = 8 * group + local % high;
+        s_tiles[b & 1][lane] = u32x4_t{(uint32_t)lo, (uint32_t)(s_lo[lo] + ml * BM), (uint32_t)min(BM, cnt - ml * BM),
+                                       (uint32_t)(local / high * BN)};
     };
+    auto tile = [&](int i) __attribute__((always_inline)) {   // past the last one: that one
+        const u32x4_t t = s_tiles[min(i, tiles - 1) >> 6 & 1][min(i, tiles - 1) & 63];
+        return Tile{__builtin_amdgcn_readfirstlane((int)t[0]), __builtin_amdgcn_readfirstlane((int)t[1]),
+                    __builtin_amdgcn_readfirstlane((int)t[2]), __builtin_amdgcn_readfirstlane((int)t[3])};
+    };
+    if (wave == 0) list(0);
+    __syncthreads();
 
-    // Copies of this wave: rows 32 wave + 16 j .. +15 of both sides (lane: row + l/4,
-    // chunk position l % 4); of a panel, waves 0-3 the records 64 wave .. +63, wave 4
+    // Copies of this wave: rows 32 wave + 8 j .. +7 of both sides (lane: row + l/8,
+    // chunk position l % 8); of a panel, waves 0-3 the records 64 wave .. +63, wave 4
     // the weights' scales.
-    const char *asrc[2], *bbase, *ssrc = nullptr;   // bbase: the same in every lane
-    uint32_t boff[2];
+    const char *bbase;   // the same in every lane
+    uint32_t aoff[4], boff[4];   // aoff in 16 bytes
     // A tile's rows to LDS. No register waits for them: a load into one
     // would be waited for with everything requested after it.
-    auto fetch_rows = [&](const Tile &t, int buf) {
+    auto fetch_rows = [&](const Tile &t, int buf) __attribute__((always_inline)) {
         if (a.row_index && wave < BM / 64)
             copy_to_lds<4>(a.row_index + t.row0 + min(wave * 64 + lane, t.rows - 1), rows_at + (buf * BM + wave * 64) * 4);
     };
-    auto row_in = [&](const Tile &t, int buf, int i) {
+    auto row_in = [&](const Tile &t, int buf, int i) __attribute__((always_inline)) {
         const int r = min(i, t.rows - 1);
         return a.row_index ? min(max(s_rows[buf][r], 0), a.A_rows - 1) : t.row0 + r;
     };
-    auto set_sources = [&](const Tile &t, int buf) {
+    auto set_sources = [&](const Tile &t, int buf) __attribute__((always_inline)) {
         const int side = EPI == EPI_GATE_UP ? wave >> 2 : 0;
         const int64_t first = EPI == EPI_GATE_UP ? t.n0 + (wave & 3) * 32 : t.n0 + wave * 32;
         bbase = (const char *)a.B[side] + t.slot * a.B_stride;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = j * 16 + (lane >> 2), sw = ((lane & 3) ^ ((r >> 2) & 3)) * 16;
-            asrc[j] = (const char *)a.A + (int64_t)row_in(t, buf, wave * 32 + r) * K + sw;
+        for (int j = 0; j < 4; ++j) {
+            const int r = j * 8 + (lane >> 3), sw = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+            aoff[j] = (uint32_t)row_in(t, buf, wave * 32 + r) * (uint32_t)(K / 16) + sw / 16;
             boff[j] = (uint32_t)(min((int)first + r, N - 1) - t.n0) * (uint32_t)K + sw;
         }
         bbase += (int64_t)t.n0 * K;
+    };
+    // Where stages and panels of the current tile are: they go on from the last one's.
+    int par = 0, ppar = 0;
+    auto at_stage = [&](int kb) __attribute__((always_inline)) { return ((kb + par) & 1) * STAGE; };
+    auto at_panel = [&](int pn) __attribute__((always_inline)) { return ((pn + ppar) & 1) * PANEL; };
+    auto issue_panel = [&](const Tile &t, int buf, int pn, int place) __attribute__((always_inline)) {
+        const uint32_t at = panels_at + place;
         if (wave < 4) {
-            ssrc = (const char *)a.As + row_in(t, buf, wave * 64 + lane) * fp8_scale_bytes(K);
-        } else if (wave == 4) {
-            const int b = (lane >> 4) & 1, nbs = (N + kFp8Block - 1) / kFp8Block;
+            copy_to_lds<16>(a.As + row_in(t, buf, wave * 64 + lane) * fp8_scale_bytes(K) + pn * 16, at + wave * 1024);
+        } else if (wave == 4 && lane < 32) {
+            const int b = lane >> 4, nbs = (N + kFp8Block - 1) / kFp8Block;
             const int nb = min(t.n0 / kFp8Block + (EPI == EPI_GATE_UP ? 0 : b), nbs - 1);
-            ssrc = (const char *)(a.Bs[EPI == EPI_GATE_UP ? b : 0] + t.slot * a.Bs_stride + (int64_t)nb * KB);
+            copy_to_lds<4>(a.Bs[EPI == EPI_GATE_UP ? b : 0] + t.slot * a.Bs_stride + (int64_t)nb * KB + min(pn * 16 + (lane & 15), KB - 1),
+                           at + APANEL);
         }
     };
-    const int nk = K / 64;
-    auto issue_panel = [&](int pn) {
-        const uint32_t at = panels_at + (pn & 1) * PANEL;
-        if (wave < 4)
-            copy_to_lds<16>(ssrc + pn * 16, at + wave * 1024);
-        else if (wave == 4 && lane < 32)
-            copy_to_lds<4>(ssrc + 4 * min(pn * 16 + (lane & 15), KB - 1), at + APANEL);
-    };
-    auto issue = [&](int kt) {
-        const uint32_t st = lds_at + (kt % NS) * STAGE + wave * 2048;
+    const bool odd = (K & 64) != 0;   // the last stage has 64 k: chunks 4-7 are not copied, and not read
+    const bool first64 = (((lane & 7) ^ (lane >> 4)) & 4) == 0;   // this lane's chunk is below 4, of rows 8 j .. with even j; odd ones: is not
+    auto issue = [&](int kb, int side, int place) __attribute__((always_inline)) {
+        const uint32_t st = lds_at + place + side * CODES + wave * 4096;
+        const char *base = (side == 0 ? (const char *)a.A : bbase) + kb * kFp8Block;
+        auto copy = [&](int j) __attribute__((always_inline)) {
+            if (side == 0)
+                copy_to_lds<16>(base + (uint64_t)aoff[j] * 16, st + j * 1024);
+            else
+                copy_to_lds(base, boff[j], st + j * 1024);
+        };
+        if (!(odd && kb == KB - 1)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) copy_to_lds<16>(asrc[j] + kt * 64, st + j * 1024);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) copy_to_lds(bbase + kt * 64, boff[j], st + CODES + j * 1024);
-        if ((kt & 31) == 16 && kt + 16 < nk) issue_panel(kt / 32 + 1);
+            for (int j = 0; j < 4; ++j) copy(j);
+        } else if (first64) {
+            copy(0);
+            copy(2);
+        } else {
+            copy(1);
+            copy(3);
+        }
     };
 
-    const int sw = ((lane & 31) >> 2) & 3;
-    const int foff[2] = {(lane & 31) * 64 + ((2 * half) ^ sw) * 16, (lane & 31) * 64 + ((2 * half + 1) ^ sw) * 16};
-    auto cblock = [&](int j) { return EPI == EPI_GATE_UP ? wn + 4 * j : 2 * wn + j; };
+    const int sw = (lane >> 1) & 7, frow = (lane & 31) * kFp8Block;
+    auto cblock = [&](int j) __attribute__((always_inline)) { return EPI == EPI_GATE_UP ? wn + 4 * j : 2 * wn + j; };
     f32x16_t acc[MI][NI];
-    i32x8_t af[2], bf[2][NI];   // records' blocks in turn, weights of this stage and the next
-    int sa[MI];                 // scale bytes of this lane's records, current block of k
-    float sm[NI];               // m of the weights' scales, current block of k
+    i32x8_t af[2], bf[2][NI];   // records' blocks in turn, weights of this half stage and the next
+    int sa[MI];                 // scale bytes of this lane's records
+    // of the weights' scales of a panel, lane l: block l % 16 of k, (l / 16) % 2 of the tile's
+    // two blocks of rows: the bits of 2^e, the last m over this one
+    int se_panel;
+    float ratio_panel;
     int se[NI];
-    auto frag = [&](const char *p) {
-        const u32x4_t lo = *(const u32x4_t *)(p + foff[0]), hi = *(const u32x4_t *)(p + foff[1]);
+    float ratio[NI];
+    auto frag = [&](const char *p, int h) __attribute__((always_inline)) {
+        const u32x4_t lo = *(const u32x4_t *)(p + frow + ((4 * h + 2 * half) ^ sw) * 16);
+        const u32x4_t hi = *(const u32x4_t *)(p + frow + ((4 * h + 2 * half + 1) ^ sw) * 16);
         return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
     };
-    auto a_frag = [&](int kt, int i) { return frag(lds + (kt % NS) * STAGE + (2 * i + wm) * 2048); };
-    auto b_frag = [&](int kt, int j) { return frag(lds + (kt % NS) * STAGE + CODES + cblock(j) * 2048); };
-    // scales of block kb of k; the factors that bring the sums into its units
-    auto read_scales = [&](auto mi, int kb, float (&ratio)[NI]) {
-        const char *p = panels + (kb / 16 & 1) * PANEL;
-#pragma unroll
-        for (int i = 0; i < decltype(mi)::value; ++i) sa[i] = *(const uint8_t *)(p + ((2 * i + wm) * 32 + (lane & 31)) * 16 + (kb & 15));
-#pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const float s = *(const float *)(p + APANEL + (EPI == EPI_GATE_UP ? j : wn >> 1) * 64 + (kb & 15) * 4);
-            const float m = scale_m(s);
-            ratio[j] = m == sm[j] ? 1.0f : sm[j] / m;
-            sm[j] = m;
-            se[j] = scale_e(s);
-        }
+    auto a_frag = [&](int kb, int h, int i) __attribute__((always_inline)) { return frag(lds + at_stage(kb) + (2 * i + wm) * 4096, h); };
+    auto b_frag = [&](int kb, int h, int j) __attribute__((always_inline)) { return frag(lds + at_stage(kb) + CODES + cblock(j) * 4096, h); };
+    // scale of block kb of k in the tile's row block r, and of the one before
+    auto weight_scale = [&](int kb, int r) __attribute__((always_inline)) { return *(const float *)(panels + at_panel(kb / 16) + APANEL + r * 64 + (kb & 15) * 4); };
+    auto row_block = [&](int j) __attribute__((always_inline)) { return EPI == EPI_GATE_UP ? j : wn >> 1; };
+    auto read_panel = [&](int pn) __attribute__((always_inline)) {
+        const int kb = pn * 16 + (lane & 15), r = EPI == EPI_GATE_UP ? (lane >> 4) & 1 : wn >> 1;
+        const float s = weight_scale(min(kb, KB - 1), r), last = weight_scale(max(min(kb, KB) - 1, 0), r);
+        ratio_panel = scale_m(last) / scale_m(s);   // behind the last block: 1
+        se_panel = scale_e(s);
     };
-    // One stage: block i's multiplies, and before them the reads of the next block.
-    auto stage = [&](auto mi, auto set_t, auto scaled, int kt, const float (&ratio)[NI]) {
-        constexpr int n = decltype(mi)::value, set = decltype(set_t)::value;
-        bf16x8_t Bv[DEC ? NI : 1][4];
-        if constexpr (DEC)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) decode32(bf[set][j], exponent_value(se[j]), Bv[j]);
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const int cur = (n & 1 ? set + i : i) & 1;
-            if (i + 1 < n) {
-                af[cur ^ 1] = a_frag(kt, i + 1);
-            } else {   // past the last stage: a resident one, not used
-                af[cur ^ 1] = a_frag(kt + 1, 0);
-#pragma unroll
-                for (int j = 0; j < NI; ++j) bf[set ^ 1][j] = b_frag(kt + 1, j);
-            }
-            if constexpr (decltype(scaled)::value)
-#pragma unroll
-                for (int j = 0; j < NI; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][j][r] *= ratio[j];
-            if constexpr (DEC) {
-                bf16x8_t Av[4];
-                decode32(af[cur], block_value(sa[i]), Av);
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int j = 0; j < NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(Av[t], Bv[j][t], acc[i][j], 0, 0, 0);
-            } else {
-#pragma unroll
-                for (int j = 0; j < NI; ++j)
-                    acc[i][j] = EPI == EPI_GATE_UP
-                                    ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[set][j], af[cur], acc[i][j], 0, 0, 0, se[j], 0, sa[i])
-                                    : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(af[cur], bf[set][j], acc[i][j], 0, 0, 0, sa[i], 0, se[j]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
+    // scale byte of this lane's record of block i (behind the last block of k: anything)
+    auto row_scale = [&](int kb, int i) __attribute__((always_inline)) {
+        return *(const uint8_t *)(panels + at_panel(kb / 16) + ((2 * i + wm) * 32 + (lane & 31)) * 16 + (kb & 15));
     };
-
-    // A tile's first requests: rows of the tile after it, the first panel, the
-    // first stages.
-    auto begin = [&](const Tile &after, int after_buf) {
-        fetch_rows(after, after_buf);
-        issue_panel(0);
+    bool scaled = false;   // whether one of them is not 1
+    auto take_ratios = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
-        for (int p = 0; p < NS - 1; ++p)
-            if (p < nk) issue(p);
+        for (int j = 0; j < NI; ++j)
+            ratio[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ratio_panel), (EPI == EPI_GATE_UP ? j * 16 : 0) + (kb & 15)));
+        scaled = ratio[0] != 1.0f || ratio[1] != 1.0f;
     };
-
-    // At the top of step kt stage kt is visible to every wave, and this wave
-    // holds its fragments. Stage kt + 1 is made visible (own copies waited for,
-    // unless it is one of the first, then a barrier) and stage kt + NS - 1
-    // requested into the slot of stage kt - 1, which every wave finished before that
-    // barrier. Loads return in order: stage kt + 1 is there once no more than the
-    // copies of the next one are outstanding.
-    auto top = [&](int kt) {
-        if (kt + 1 < nk) {
-            if (kt + 1 >= NS - 1) wait_vmcnt_stages<LOADS, NS - 3>(min(NS - 3, nk - 2 - kt));
+    auto take_powers = [&](int kb) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NI; ++j) se[j] = __builtin_amdgcn_readlane(se_panel, (EPI == EPI_GATE_UP ? j * 16 : 0) + (kb & 15));
+    };
+    auto multiply = [&](int i, int j, int set, int cur) __attribute__((always_inline)) {
+        acc[i][j] = EPI == EPI_GATE_UP
+                        ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[set][j], af[cur], acc[i][j], 0, 0, 0, se[j], 0, sa[i])
+                        : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(af[cur], bf[set][j], acc[i][j], 0, 0, 0, sa[i], 0, se[j]);
+    };
+    auto rescale = [&](int i, int j) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] *= ratio[j];
+    };
+    // The stores of a tile are requested behind the first two stages' copies of the
+    // next one, and are not waited for with them: loads and stores return in order.
+    int stores = 0;   // of this wave, a multiple of 16
+    auto wait_behind = [&](int n) __attribute__((always_inline)) {
+        if (n >= 64) wait_vmcnt<63>();
+        else if (n == 48) wait_vmcnt<48>();
+        else if (n == 32) wait_vmcnt<32>();
+        else if (n == 16) wait_vmcnt<16>();
+        else wait_vmcnt<0>();
+    };
+    // The stage behind kb, the next tile's first one behind the last, is made visible: this
+    // wave's reads of stage kb are done, its copies have landed, and behind the barrier so
+    // have all waves'. Then stage kb's place is free, and `follow` requests the stage after that one
+    // into it, of this tile or the next.
+    Tile cur;
+    int o = 0;   // which of this workgroup's tiles it is
+    int buf = 0, buf1 = 1, buf2 = 2;   // of their rows
+    bool has_next, cross;
+    auto next_stage = [&](int kb) __attribute__((always_inline)) {
+        if (kb + 1 < KB || cross) {
+            if (kb == 0) wait_behind(stores); else wait_vmcnt<0>();
+            __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));   // lgkmcnt(0)
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");   // for the compiler: reads stay behind
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         }
-        if (kt + NS - 1 < nk) issue(kt + NS - 1);
     };
-    auto tile_loop = [&](auto mi) {
+    auto follow = [&](int kb, int side) __attribute__((always_inline)) {
+        const int place = at_stage(kb);
+        if (kb + 2 < KB) {
+            issue(kb + 2, side, place);
+            if (side == 1 && (kb & 15) == 6 && kb + 10 < KB) issue_panel(cur, buf, kb / 16 + 1, at_panel(kb / 16 + 1));
+        } else if (cross) {
+            if (side == 0 && kb + 2 == KB) {
+                const Tile nxt = tile(o + 1);
+                set_sources(nxt, buf1);
+                fetch_rows(tile(o + 2), buf2);
+                issue_panel(nxt, buf1, 0, at_panel((KB + 15) / 16));
+            }
+            issue(kb + 2 - KB, side, place);
+        }
+    };
+    // Half h of stage kb. While block i is multiplied, the next block's codes are read,
+    // and its sums brought into the current units (first half; block 0's at the end of
+    // the half before): what the scheduler is held from moving runs in the
+    // shadow of the matrix instructions. The next stage begins before the last block
+    // is multiplied, whose codes are in registers by then. The sums are opaque
+    // where there are branches: the compiler would move a stage's multiplies behind
+    // them, with all of its codes in registers until then.
+    int mine = 0;   // blocks of records of this wave, 0, 2 or 4 of them multiplied
+    bf16x8_t Bv[DEC ? NI : 1][4];   // the weights of a half stage, decoded
+    auto step = [&](auto half_t, auto block_t, int kb, bool last) __attribute__((always_inline)) {
+        constexpr int h = decltype(half_t)::value, i = decltype(block_t)::value, cur = i & 1;
+        const bool end = h == 1 && last;
+        if (end) next_stage(kb);
+        if (!last) {
+            af[cur ^ 1] = a_frag(kb, h, i + 1);
+        } else {   // past the last stage: a resident one, not used
+            af[cur ^ 1] = a_frag(kb + h, h ^ 1, 0);
+#pragma unroll
+            for (int j = 0; j < NI; ++j) bf[h ^ 1][j] = b_frag(kb + h, h ^ 1, j);
+        }
+        if (h == 1 && i == 0 && (kb & 15) == 15) read_panel(kb / 16 + 1);
+        if (end) take_ratios(kb + 1);
+        if constexpr (h == 1 && i > 0) sa[i - 1] = row_scale(kb + 1, i - 1);
+        __builtin_amdgcn_sched_barrier(0);
+        const int next = last ? 0 : i + 1;
+        const bool scales = h == 0 ? !last : last;
+        if constexpr (DEC) {
+            bf16x8_t Av[4];
+            decode32(af[cur], block_value(sa[i]), Av);
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(Av[c], Bv[j][c], acc[i][j], 0, 0, 0);
+                opaque(acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (end) follow(kb, j);
+                if (scales && scaled) {
+                    rescale(next, j);
+                    opaque(acc[next][j]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                multiply(i, j, h, cur);
+                opaque(acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (end) follow(kb, j);
+                if (scales && scaled) {
+                    rescale(next, j);
+                    opaque(acc[next][j]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+    auto half_stage = [&](auto mi, auto half_t, int kb) __attribute__((always_inline)) {
+        constexpr int n = decltype(mi)::value;
+        if constexpr (DEC)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) decode32(bf[decltype(half_t)::value][j], exponent_value(se[j]), Bv[j]);
+        step(half_t, std::integral_constant<int, 0>(), kb, false);
+        step(half_t, std::integral_constant<int, 1>(), kb, n == 2);
+        if constexpr (n == 4) {
+            step(half_t, std::integral_constant<int, 2>(), kb, false);
+            step(half_t, std::integral_constant<int, 3>(), kb, true);
+        }
+    };
+
+    // The first tile's first requests, and those of a tile behind one of a single stage.
+    auto begin = [&]() __attribute__((always_inline)) {
+        set_sources(cur, buf);
+        fetch_rows(tile(o + 1), buf1);
+        issue_panel(cur, buf, 0, at_panel(0));
+        issue(0, 0, at_stage(0));
+        issue(0, 1, at_stage(0));
+        if (KB > 1) {
+            issue(1, 0, at_stage(1));
+            issue(1, 1, at_stage(1));
+        }
+    };
+
+    auto tile_loop = [&](auto mi) __attribute__((always_inline)) {
         constexpr int n = decltype(mi)::value;
         if constexpr (n > 0) {
 #pragma unroll
@@ -630,58 +737,60 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
                 for (int j = 0; j < NI; ++j)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+            read_panel(0);
+            take_powers(0);
+            take_ratios(0);   // 1
 #pragma unroll
-            for (int j = 0; j < NI; ++j) sm[j] = 1.0f;
-            af[0] = a_frag(0, 0);
+            for (int i = 0; i < n; ++i) sa[i] = row_scale(0, i);
+            af[0] = a_frag(0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < NI; ++j) bf[0][j] = b_frag(0, j);
+            for (int j = 0; j < NI; ++j) bf[0][j] = b_frag(0, 0, j);
         }
-        // whole blocks of k, then half a one
-        float ratio[NI] = {1.0f, 1.0f};
-        const int whole = nk & ~1;
-        for (int kt = 0; kt < whole; kt += 2) {
-            top(kt);
+        const int whole = K / kFp8Block;   // stages, and half a one
+        for (int kb = 0; kb < whole; ++kb) {
             if constexpr (n > 0) {
-                read_scales(mi, kt / 2, ratio);
-                stage(mi, std::integral_constant<int, 0>(), std::true_type(), kt, ratio);
+                half_stage(mi, std::integral_constant<int, 0>(), kb);
+                half_stage(mi, std::integral_constant<int, 1>(), kb);
+                sa[n - 1] = row_scale(kb + 1, n - 1);
+                take_powers(kb + 1);
+            } else {
+                next_stage(kb);
+                follow(kb, 0);
+                follow(kb, 1);
             }
-            top(kt + 1);
-            if constexpr (n > 0) stage(mi, std::integral_constant<int, 1>(), std::false_type(), kt + 1, ratio);
         }
-        if (nk & 1) {
-            top(whole);
-            if constexpr (n > 0) {
-                read_scales(mi, whole / 2, ratio);
-                stage(mi, std::integral_constant<int, 0>(), std::true_type(), whole, ratio);
+        if (odd) {
+            if constexpr (n > 0) half_stage(mi, std::integral_constant<int, 0>(), whole);
+            if (cross) {
+                next_stage(whole);
+                follow(whole, 0);
+                follow(whole, 1);
             }
         }
     };
 
-    int tl = li, buf = 0;
-    Tile cur = decode(start_x + tl), nxt = tl + nwg < cnt_x ? decode(start_x + tl + nwg) : cur;
-    fetch_rows(cur, 0);
+    cur = tile(0);
+    fetch_rows(cur, buf);
     wait_vmcnt<0>();
     __syncthreads();
-    set_sources(cur, 0);
-    begin(nxt, 1);
+    begin();
     for (;;) {
-        const int tn = tl + nwg;
-        const bool has_next = tn < cnt_x;
-        const Tile after = tn + nwg < cnt_x ? decode(start_x + tn + nwg) : nxt;
-        const int mine = (cur.rows + 31) / 32 - wm + 1 >> 1;   // blocks of this wave
-        // The first stages, and the last tile's stores.
-        wait_vmcnt<0>();
-        lds_barrier();
+        has_next = o + 1 < tiles;
+        cross = has_next && KB > 1;
+        if (wave == 0 && (o & 63) == 32) list((o >> 6) + 1);   // read half a list later
+        mine = __builtin_amdgcn_readfirstlane(((cur.rows + 31) / 32 - wm + 1) >> 1);
+        if (o == 0 || KB == 1) {   // else the first stage is visible already
+            wait_behind(stores);
+            lds_barrier();
+        }
         if (mine > 2) tile_loop(std::integral_constant<int, 4>());
         else if (mine > 0) tile_loop(std::integral_constant<int, 2>());
         else tile_loop(std::integral_constant<int, 0>());
         const Tile done = cur;
-        if (has_next) {
-            lds_barrier();   // nothing reads the ring any more
-            const int nb = buf == 2 ? 0 : buf + 1;
-            set_sources(nxt, nb);
-            begin(after, nb == 2 ? 0 : nb + 1);
-        }
+        float sm[NI];   // the units that the sums are in
+#pragma unroll
+        for (int j = 0; j < NI; ++j) sm[j] = scale_m(weight_scale(KB - 1, row_block(j)));
+        stores = 0;
         if constexpr (EPI == EPI_GATE_UP) {
             // register r of lane l: unit 32 wn + 8 (r / 4) + 4 (l / 32) + r % 4 of record l % 32 of the block
             const bool in = done.n0 + wn * 32 < N;
@@ -689,12 +798,26 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 if (i >= mine) continue;
-                uint32_t t = 0;
+                f32x16_t &g = acc[i][0], &u = acc[i][1];
+                uint32_t least = 0, t = 0;   // of negative numbers the least has the largest bits
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const float h = in ? swiglu(acc[i][0][r] * sm[0], acc[i][1][r] * sm[1]) : 0.0f;
-                    acc[i][0][r] = h;
-                    t = max(t, __float_as_uint(h) & 0x7fffffffu);
+                    g[r] *= sm[0];
+                    u[r] *= sm[1];
+                    least = max(least, __float_as_uint(g[r]));
+                }
+                float h[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) h[r] = silu_mul(g[r], u[r]);
+                if (__any(least > __builtin_bit_cast(uint32_t, kSiluTail))) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (g[r] < kSiluTail) h[r] = silu_tail_mul(g[r], u[r]);
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    g[r] = in ? h[r] : 0.0f;
+                    t = max(t, __float_as_uint(g[r]) & 0x7fffffffu);
                 }
                 t = max(t, (uint32_t)__shfl_xor((int)t, 32, 64));
                 if (half == 0) tops[((2 * i + wm) * 32 + lane) * 4 + wn] = t;
@@ -725,6 +848,7 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
                 }
             }
         } else if (mine > 0 && done.n0 + wn * 64 < N) {
+            if (cross) stores = mine * (DEC ? 32 : 16);
             // Register r of lane l holds record 8 (r / 4) + 4 (l / 32) + r % 4 and column
             // l % 32 of its block. bf16: adjacent lanes swap a value of records R, R + 1,
             // so that each stores two columns of one. The tile's rows of C are a
@@ -773,10 +897,17 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
             }
         }
         if (!has_next) break;
-        cur = nxt;
-        nxt = after;
-        tl = tn;
-        buf = buf == 2 ? 0 : buf + 1;
+        cur = tile(++o);
+        const int b = buf;
+        buf = buf1;
+        buf1 = buf2;
+        buf2 = b;
+        par ^= KB & 1;
+        ppar ^= (KB + 15) / 16 & 1;
+        if (KB == 1) {
+            lds_barrier();   // nothing reads the stages any more
+            begin();
+        }
     }
 }
 

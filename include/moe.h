@@ -558,7 +558,11 @@ moe_status moe_dequantize_fp8(const void *codes, const void *scales,
  * A weight's scale may be any fp32 number; a NaN or an infinity makes NaN of
  * what it meets, one below 2^-126 in magnitude counts as 2^-126 or as itself. Rows and
  * offsets out of range are brought into it on the device.
- * MOE_ERR_UNSUPPORTED from (M / 16 + P + 1) * (N / 64) = 2^22 on.
+ * C in bf16 of many records a slot (and H below) is multiplied on the fp8 matrix
+ * instructions, which keep 14 bits of the products of 8 neighbouring k: 1.1e-5 of
+ * the norm of C for normally distributed operands. fp32 C keeps 24 bits.
+ * MOE_ERR_UNSUPPORTED from (M / 256 + P + 1) * (N / 64) = 2^30 and for A_rows * K
+ * above 2^36.
  */
 moe_status moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void *A_codes,
                           const void *A_scales, int32_t A_rows,
@@ -577,10 +581,15 @@ moe_status moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void *A_codes,
  *                tensors, or the halves of one of [P][2f][K])
  *   H_codes      device [M][f], 16-byte aligned
  *   H_scales     device [M][MOE_FP8_SCALE_BYTES(f)]
+ *   ws           at least moe_gate_up_fp8_workspace_bytes(M, f, K, P) bytes, 256-byte
+ *                aligned, of any contents; one call at a time. 0 bytes (NULL will
+ *                do) where many records a slot make one kernel of it, else 4 M f
  * The other arguments and the limits are those of moe_matmul_fp8, which takes
  * H for the down projection. SiLU(g) * u is within (|g| + 8) 2^-22 of its
  * value for the g and u of the fp32 sums, relative.
  */
+size_t moe_gate_up_fp8_workspace_bytes(int32_t M, int32_t f, int32_t K,
+                                       int32_t P);
 moe_status moe_gate_up_fp8(int32_t M, int32_t f, int32_t K, const void *A_codes,
                            const void *A_scales, int32_t A_rows,
                            const int32_t *row_index, const int32_t *slot_offset,
@@ -588,7 +597,8 @@ moe_status moe_gate_up_fp8(int32_t M, int32_t f, int32_t K, const void *A_codes,
                            const float *Wg_scales, const void *Wu_codes,
                            const float *Wu_scales, int64_t W_stride,
                            int64_t W_scale_stride, void *H_codes,
-                           void *H_scales, moe_stream stream);
+                           void *H_scales, void *ws, size_t ws_bytes,
+                           moe_stream stream);
 
 /*
  * Combine of rows in record order, as moe_matmul_fp8 and moe_matmul_mxfp4

@@ -103,8 +103,9 @@ _SIGS = {
     "moe_quantize_fp8": ([_VP, _I32, _I64, _I32, _I64, _I32, _VP, _VP, _VP], _I32),
     "moe_dequantize_fp8": ([_VP, _VP, _I64, _I32, _I32, _VP, _I32, _I64, _VP], _I32),
     "moe_matmul_fp8": ([_I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _VP, _I64, _I64, _VP, _I32, _I64, _VP], _I32),
-    "moe_gate_up_fp8": ([_I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _I64, _I64, _VP, _VP, _VP],
-                        _I32),
+    "moe_gate_up_fp8_workspace_bytes": ([_I32, _I32, _I32, _I32], _SZ),
+    "moe_gate_up_fp8": ([_I32, _I32, _I32, _VP, _VP, _I32, _VP, _VP, _I32, _VP, _VP, _VP, _VP, _I64, _I64, _VP, _VP, _VP,
+                         _SZ, _VP], _I32),
     "moe_combine": ([_I32, _I32, _I32, _I32, _VP, _I32, _I64, _VP, _VP, _VP, _I64, _VP], _I32),
     "moe_combine_backward": ([_I32, _I32, _I32, _I32, _VP, _I32, _I64, _VP, _VP, _VP, _I64, _VP, _I64, _VP, _VP], _I32),
     "moe_balance_workspace_bytes": ([_VP, _I32], _SZ),
@@ -510,10 +511,16 @@ def moe_matmul_fp8(A_codes, A_scales, B_codes, B_scales, C, slot_offset=None, ro
                                  C.data_ptr(), dtype, ldc, _stream_of(C, stream)))
 
 
+def moe_gate_up_fp8_workspace_bytes(M: int, f: int, K: int, P: int = 1) -> int:
+    return load().moe_gate_up_fp8_workspace_bytes(M, f, K, P)
+
+
 def moe_gate_up_fp8(A_codes, A_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales, H_codes, H_scales, slot_offset=None,
-                    row_index=None, stream=None):
+                    row_index=None, ws=None, stream=None):
     """H [M][f] = fp8 rows of SiLU(A Wg^T) * (A Wu^T); Wg_codes and Wu_codes
-    uint8 [P][f][K] (or one [f][K]), of the same strides."""
+    uint8 [P][f][K] (or one [f][K]), of the same strides. ws: see
+    ``moe_gate_up_fp8_workspace_bytes``; without it torch's allocator gives the
+    call one of its own, on its stream."""
     A_rows, K = _fp8_rows(A_codes, A_scales, "A")
     M, f = _fp8_rows(H_codes, H_scales, "H")
     gate, up = _fp8_slices(Wg_codes, Wg_scales, K, "Wg"), _fp8_slices(Wu_codes, Wu_scales, K, "Wu")
@@ -523,10 +530,16 @@ def moe_gate_up_fp8(A_codes, A_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales,
     dev = H_codes.get_device()
     _one_device(dev, A_codes, A_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales, H_scales)
     _groups(M, P, dev, slot_offset, row_index)
+    st, n = _stream_of(H_codes, stream), moe_gate_up_fp8_workspace_bytes(M, f, K, P)
+    if ws is None and n:
+        with on_stream(stream):   # its memory goes back to the pool of the stream that uses it
+            ws = torch.empty(n, dtype=torch.uint8, device=H_codes.device)
+    if ws is not None:
+        _one_device(dev, ws)
     _check(load().moe_gate_up_fp8(M, f, K, A_codes.data_ptr(), A_scales.data_ptr(), A_rows, _ptr(row_index),
                                   _ptr(slot_offset), P, Wg_codes.data_ptr(), Wg_scales.data_ptr(), Wu_codes.data_ptr(),
                                   Wu_scales.data_ptr(), w_stride, s_stride, H_codes.data_ptr(), H_scales.data_ptr(),
-                                  _stream_of(H_codes, stream)))
+                                  _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0, st))
 
 
 def _strided(t, name, cols=None):

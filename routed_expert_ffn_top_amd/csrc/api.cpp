@@ -894,8 +894,9 @@ moe_status check_fp8_product(const char *what, int32_t M, int32_t N, int32_t K, 
     if (!aligned(A, 16) || !aligned(As, 16)) return fail(MOE_ERR_INVALID_ARG, "%s: A and its scales must be 16-byte aligned", what);
     if (P > 1 && (B_stride < (int64_t)N * K || B_stride % 16 != 0 || Bs_stride < fp8_blocks(N) * fp8_blocks(K)))
         return fail(MOE_ERR_INVALID_ARG, "%s: the strides must hold a slice, that of the codes in whole 16 bytes", what);
-    // 1024 threads per 16 records x 128 units, at most 2^32 - 1 threads a launch
-    if (((int64_t)M / 16 + P + 1) * (N / 64) >= (1 << 22)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", what);
+    // tiles are counted in 32 bits, a row of A is addressed in 16 bytes and 32 bits
+    if (((int64_t)M / 256 + P + 1) * (N / 64) >= (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", what);
+    if ((int64_t)A_rows * K > (int64_t)1 << 36) return fail(MOE_ERR_UNSUPPORTED, "%s: A above 64 GiB", what);
     *work = true;
     return MOE_OK;
 }
@@ -970,10 +971,22 @@ moe_status moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void *A_codes, 
     return MOE_OK;
 }
 
+size_t moe_gate_up_fp8_workspace_bytes(int32_t M, int32_t f, int32_t K, int32_t P)
+{
+    if (M <= 0 || f <= 0 || K <= 0 || P < 1) return 0;
+    Fp8Args a{};
+    a.M = M;
+    a.N = f;
+    a.K = K;
+    a.P = P;
+    return gate_up_fp8_workspace(a);
+}
+
 moe_status moe_gate_up_fp8(int32_t M, int32_t f, int32_t K, const void *A_codes, const void *A_scales, int32_t A_rows,
                            const int32_t *row_index, const int32_t *slot_offset, int32_t P, const void *Wg_codes,
                            const float *Wg_scales, const void *Wu_codes, const float *Wu_scales, int64_t W_stride,
-                           int64_t W_scale_stride, void *H_codes, void *H_scales, moe_stream stream)
+                           int64_t W_scale_stride, void *H_codes, void *H_scales, void *ws, size_t ws_bytes,
+                           moe_stream stream)
 {
     bool work;
     MOE_TRY(check_fp8_product("gate/up", M, f, K, A_codes, A_scales, A_rows, row_index, slot_offset, P, W_stride,
@@ -991,7 +1004,11 @@ moe_status moe_gate_up_fp8(int32_t M, int32_t f, int32_t K, const void *A_codes,
     a.Bs[1] = Wu_scales;
     a.C = H_codes;
     a.Hs = (uint8_t *)H_scales;
-    HIP_TRY(launch_gate_up_fp8(a, S(stream)), "gate/up launch");
+    const size_t need = gate_up_fp8_workspace(a);
+    if (need > 0 && !ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (need > 0 && !aligned(ws, 256)) return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace too small: %zu < %zu", ws_bytes, need);
+    HIP_TRY(launch_gate_up_fp8(a, ws, S(stream)), "gate/up launch");
     return MOE_OK;
 }
 

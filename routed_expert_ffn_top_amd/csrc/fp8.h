@@ -37,6 +37,8 @@ struct Fp8Args {
     uint8_t *Hs;                 // the SwiGLU product: scale bytes of H [M][fp8_scale_bytes(N)]
 };
 hipError_t launch_matmul_fp8(const Fp8Args &a, hipStream_t st);
-hipError_t launch_gate_up_fp8(const Fp8Args &a, hipStream_t st);
+// Bytes of workspace the SwiGLU product takes (few records a slot: h in fp32).
+size_t gate_up_fp8_workspace(const Fp8Args &a);
+hipError_t launch_gate_up_fp8(const Fp8Args &a, void *ws, hipStream_t st);
 
 }  // namespace moe

@@ -103,13 +103,14 @@ __device__ __forceinline__ uint32_t max_over(uint32_t v)
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_quantize_rows(const void *__restrict__ src, int64_t blocks, int KB, int K,
                                                        int64_t ld, int64_t lds, uint8_t *__restrict__ codes,
-                                                       uint8_t *__restrict__ scales)
+                                                       uint8_t *__restrict__ scales,
+                                                       const int32_t *__restrict__ first, const int32_t *__restrict__ last)
 {
     const int64_t b = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
     const uint32_t row = (uint32_t)min(b, blocks - 1) / (uint32_t)KB;
     const int kb = (int)((uint32_t)min(b, blocks - 1) - row * (uint32_t)KB), k = kb * kFp8Block + (threadIdx.x & 15) * 8;
     uint32_t v[8] = {};
-    const bool in = b < blocks && k < K;
+    const bool in = b < blocks && k < K && (!first || ((int)row >= *first && (int)row < *last));
     if (in) load8<BF16>(src, row * ld + k, v);
     const uint32_t byte = block_byte(max_over<16>(largest(v)));
     if (in) *(u32x2_t *)(codes + (int64_t)row * K + k) = codes8(v, block_unit(byte), byte == 255);
@@ -264,14 +265,23 @@ __device__ __forceinline__ void step128(f32x4_t &acc, const bf16x8_t (&A)[4], co
     for (int r = 0; r < 4; ++r) acc[r] = fmaf(part[r], sb, acc[r]);
 }
 
-// Few records a slot: 16 records x 16 NT columns a workgroup, its W waves taking
-// steps of 128 k in turn, their sums joined in LDS in the order of the waves.
-template <int NT, int W>
-__global__ __launch_bounds__(64 * W) void k_matmul_few(Fp8Args a)
+__device__ __forceinline__ float swiglu(float g, float u) { return g < kSiluTail ? silu_tail_mul(g, u) : silu_mul(g, u); }
+
+// Few records a slot: 16 records x 16 NT weight rows a workgroup, its W waves taking
+// steps of 128 k in turn, U of them requested at a time, their sums joined in LDS in
+// the order of the waves. Bound by reading the weights, and for a record or
+// two by the chain slot - record - row. GATE_UP: half of the rows are gate, half up of the
+// same units; h goes to `hw` in fp32, and is quantised by the next launch: a
+// workgroup that held whole blocks of 128 units would leave most compute units idle,
+// and one alone reads 50 GB/s at most (one record of 2048 x 2048: 20 us).
+enum { EPI_STORE = 0, EPI_GATE_UP = 1 };
+template <int EPI, int NT, int W>
+__global__ __launch_bounds__(64 * W) void k_few(Fp8Args a, float *__restrict__ hw)
 {
+    constexpr int U = 4, G = EPI == EPI_GATE_UP ? 2 : 1, COLS = 16 * NT / G;
     __shared__ f32x4_t s_sum[W][NT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int ntn = (a.N + 16 * NT - 1) / (16 * NT), n0 = blockIdx.x % ntn * (16 * NT);
+    const int ntn = (a.N + COLS - 1) / COLS, n0 = blockIdx.x % ntn * COLS;
     int row0 = 0, cnt = 0;
     const int slot = find_tile<16>(a, blockIdx.x / ntn, lane, &row0, &cnt);
     if (slot < 0) return;
@@ -283,101 +293,83 @@ __global__ __launch_bounds__(64 * W) void k_matmul_few(Fp8Args a)
     const float *bs[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const int n = min(n0 + 16 * j + (lane & 15), a.N - 1);
-        bp[j] = a.B[0] + slot * a.B_stride + (int64_t)n * K + (lane >> 4) * 16;
-        bs[j] = a.Bs[0] + slot * a.Bs_stride + (int64_t)(n / kFp8Block) * KB;
+        const int c = n0 + 16 * (j / G), n = min(c + (lane & 15), a.N - 1);
+        bp[j] = a.B[j % G] + slot * a.B_stride + (int64_t)n * K + (lane >> 4) * 16;
+        bs[j] = a.Bs[j % G] + slot * a.Bs_stride + (int64_t)(min(c, a.N - 1) / kFp8Block) * KB;
     }
     f32x4_t acc[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kb = wave; kb < KB; kb += W) {
-        const bool half = (kb + 1) * kFp8Block > K;
-        i32x8_t A = codes32(ap + (int64_t)kb * kFp8Block, half);
-        if (half)
+    auto batch = [&](auto u_t, int k0) __attribute__((always_inline)) {
+        constexpr int n = decltype(u_t)::value;
+        i32x8_t A[n], Bv[n][NT];
+        int sa[n];
+        float sb[n][NT];
 #pragma unroll
-            for (int i = 4; i < 8; ++i) A[i] = 0;
-        bf16x8_t Av[4];
-        decode32(A, block_value(as[kb]), Av);
+        for (int u = 0; u < n; ++u) {
+            const int kb = k0 + u * W;
+            const bool half = (kb + 1) * kFp8Block > K;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) step128(acc[j], Av, codes32(bp[j] + (int64_t)kb * kFp8Block, half), bs[j][kb]);
+            for (int j = 0; j < NT; ++j) {
+                Bv[u][j] = codes32(bp[j] + (int64_t)kb * kFp8Block, half);
+                sb[u][j] = bs[j][kb];
+            }
+            A[u] = codes32(ap + (int64_t)kb * kFp8Block, half);
+            sa[u] = as[kb];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < n; ++u) {
+            if ((k0 + u * W + 1) * kFp8Block > K)
+#pragma unroll
+                for (int i = 4; i < 8; ++i) A[u][i] = 0;
+            bf16x8_t Av[4];
+            decode32(A[u], block_value(sa[u]), Av);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) step128(acc[j], Av, Bv[u][j], sb[u][j]);
+        }
+    };
+    int k0 = wave;
+    for (; k0 + (U - 1) * W < KB; k0 += W * U) batch(std::integral_constant<int, U>(), k0);
+    for (; k0 < KB; k0 += W) batch(std::integral_constant<int, 1>(), k0);
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s_sum[wave][j][lane] = acc[j];
+        __syncthreads();
     }
+    for (int q = wave; q < NT / G; q += W) {
+        f32x4_t s[G];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) s_sum[wave][j][lane] = acc[j];
-    __syncthreads();
-    for (int j = wave; j < NT; j += W) {
-        f32x4_t s = s_sum[0][j][lane];
+        for (int g = 0; g < G; ++g) {
+            if constexpr (W > 1) {
+                s[g] = s_sum[0][q * G + g][lane];
 #pragma unroll
-        for (int w = 1; w < W; ++w) s += s_sum[w][j][lane];
-        const int n = n0 + 16 * j + (lane & 15);
+                for (int w = 1; w < W; ++w) s[g] += s_sum[w][q * G + g][lane];
+            } else {
+#pragma unroll
+                for (int c = 0; c < NT / G; ++c)   // a register's index has to be known
+                    if (c == q) s[g] = acc[c * G + g];
+            }
+        }
+        const int n = n0 + 16 * q + (lane & 15);
         if (n >= a.N) continue;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int m = 4 * (lane >> 4) + r;
             if (m >= cnt) continue;
-            const int64_t at = (int64_t)(row0 + m) * a.ldc + n;
-            if (a.c_bf16)
-                ((uint16_t *)a.C)[at] = (uint16_t)bf16_pair(s[r], 0.0f);
-            else
-                ((float *)a.C)[at] = s[r];
+            if constexpr (EPI == EPI_GATE_UP) {
+                hw[(int64_t)(row0 + m) * a.N + n] = swiglu(s[0][r], s[G - 1][r]);
+            } else {
+                const int64_t at = (int64_t)(row0 + m) * a.ldc + n;
+                if (a.c_bf16)
+                    ((uint16_t *)a.C)[at] = (uint16_t)bf16_pair(s[0][r], 0.0f);
+                else
+                    ((float *)a.C)[at] = s[0][r];
+            }
         }
     }
 }
 
-__device__ __forceinline__ float swiglu(float g, float u) { return g < kSiluTail ? silu_tail_mul(g, u) : silu_mul(g, u); }
-
-// SiLU(g) u for few records a slot: 16 records x 128 units a workgroup, so that
-// the blocks of H are whole; wave w takes gate and up of units 16 (w % 8) .. +15
-// and every second step of 128 k. H passes through LDS to a wave a record.
-__global__ __launch_bounds__(1024) void k_gate_up_few(Fp8Args a)
-{
-    __shared__ f32x4_t s_sum[8][2][64];
-    __shared__ float s_h[16][kFp8Block + 4];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, cg = wave & 7;
-    const int fb = (a.N + kFp8Block - 1) / kFp8Block, f0 = blockIdx.x % fb * kFp8Block;
-    int row0 = 0, cnt = 0;
-    const int slot = find_tile<16>(a, blockIdx.x / fb, lane, &row0, &cnt);
-    if (slot < 0) return;   // the same in every wave
-    const int K = a.K, KB = (K + kFp8Block - 1) / kFp8Block;
-    const int rec = row_of(a, row0 + min(lane & 15, cnt - 1));
-    const uint8_t *ap = a.A + (int64_t)rec * K + (lane >> 4) * 16;
-    const uint8_t *as = a.As + rec * fp8_scale_bytes(K);
-    const int n = min(f0 + 16 * cg + (lane & 15), a.N - 1);
-    const int64_t at = slot * a.B_stride + (int64_t)n * K + (lane >> 4) * 16;
-    const int64_t sat = slot * a.Bs_stride + (int64_t)(f0 / kFp8Block) * KB;
-    f32x4_t acc[2] = {f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}};
-    for (int kb = wave >> 3; kb < KB; kb += 2) {
-        const bool half = (kb + 1) * kFp8Block > K;
-        i32x8_t A = codes32(ap + (int64_t)kb * kFp8Block, half);
-        if (half)
-#pragma unroll
-            for (int i = 4; i < 8; ++i) A[i] = 0;
-        bf16x8_t Av[4];
-        decode32(A, block_value(as[kb]), Av);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            step128(acc[j], Av, codes32(a.B[j] + at + (int64_t)kb * kFp8Block, half), a.Bs[j][sat + kb]);
-    }
-    if (wave >= 8) {
-        s_sum[cg][0][lane] = acc[0];
-        s_sum[cg][1][lane] = acc[1];
-    }
-    __syncthreads();
-    if (wave < 8) {
-        const f32x4_t g = acc[0] + s_sum[cg][0][lane], u = acc[1] + s_sum[cg][1][lane];
-        const bool in = f0 + 16 * cg + (lane & 15) < a.N;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s_h[4 * (lane >> 4) + r][16 * cg + (lane & 15)] = in ? swiglu(g[r], u[r]) : 0.0f;
-    }
-    __syncthreads();
-    if (wave >= cnt) return;
-    const float h0 = s_h[wave][2 * lane], h1 = s_h[wave][2 * lane + 1];
-    const uint32_t byte = block_byte(max_over<64>(max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu)));
-    const float unit = block_unit(byte);
-    const int q = __builtin_amdgcn_cvt_pk_fp8_f32(h0 * unit, h1 * unit, 0, false);
-    const int64_t p = row0 + wave;
-    if (f0 + 2 * lane < a.N) *(uint16_t *)((uint8_t *)a.C + p * a.N + f0 + 2 * lane) = byte == 255 ? 0 : (uint16_t)q;
-    if (lane == 0) a.Hs[p * fp8_scale_bytes(a.N) + f0 / kFp8Block] = (uint8_t)byte;
-}
 
 // ---------------------------------------------------------------------------
 // Many records a slot: a persistent kernel. Tile 256 records x 256 weight rows,
@@ -403,7 +395,6 @@ __global__ __launch_bounds__(1024) void k_gate_up_few(Fp8Args a)
 // waves through LDS.
 constexpr int kXcd = 8;
 constexpr int kStream = 2;   // buffer stores of C, which is not read here: non-temporal
-enum { EPI_STORE = 0, EPI_GATE_UP = 1 };
 
 // A weight scale as m and the bits of 2^e; below 2^-126 as +-2^-127, NaN and infinity as NaN.
 __device__ __forceinline__ float scale_m(float s)
@@ -913,18 +904,24 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
 
 }  // namespace
 
+// Rows [*first, *last), or with null pointers all of them.
+static void quantize_rows(const void *src, bool bf16, int64_t rows, int K, int64_t ld, uint8_t *codes, uint8_t *scales,
+                          const int32_t *first, const int32_t *last, hipStream_t st)
+{
+    const int KB = (int)fp8_blocks(K);
+    const int64_t blocks = rows * KB;
+    const auto kernel = bf16 ? k_quantize_rows<true> : k_quantize_rows<false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((blocks + 15) / 16)), dim3(256), 0, st, src, blocks, KB, K, ld, fp8_scale_bytes(K),
+                       codes, scales, first, last);
+}
+
 hipError_t launch_quantize_fp8(const void *src, bool bf16, int64_t rows, int K, int64_t ld, int block_rows,
                                uint8_t *codes, void *scales, hipStream_t st)
 {
     if (rows == 0) return hipSuccess;
     const int KB = (int)fp8_blocks(K);
     if (block_rows == 1) {
-        const int64_t blocks = rows * KB, lds = fp8_scale_bytes(K);
-        const dim3 grid((unsigned)((blocks + 15) / 16));
-        if (bf16)
-            hipLaunchKernelGGL(k_quantize_rows<true>, grid, dim3(256), 0, st, src, blocks, KB, K, ld, lds, codes, (uint8_t *)scales);
-        else
-            hipLaunchKernelGGL(k_quantize_rows<false>, grid, dim3(256), 0, st, src, blocks, KB, K, ld, lds, codes, (uint8_t *)scales);
+        quantize_rows(src, bf16, rows, K, ld, codes, (uint8_t *)scales, nullptr, nullptr, st);
     } else {
         const dim3 grid((unsigned)(fp8_blocks(rows) * KB));
         if (bf16)
@@ -954,7 +951,23 @@ hipError_t launch_dequantize_fp8(const uint8_t *codes, const void *scales, int64
 // at most this many row tiles of R records: one partial tile per slot with records
 static int64_t row_tiles(const Fp8Args &a, int R) { return (int64_t)(a.M + R - 1) / R + std::min(a.P, a.M) - 1; }
 
-static bool ring_pays(const Fp8Args &a) { return a.M / std::min(a.P, a.M) >= 32; }
+// Whether the persistent kernel is ahead, by what the two take (us; the rates are
+// those of single calls at sizes from 8 records of 2048 x 2048 to 16384 of 64 slices):
+// the few-records kernel 4 and 0.16 for each million of weights that a tile of 16
+// records meets, the persistent one a round of tiles of 5 and a time for each
+// stage, by whether a slot has more than 128 records (1.7, fp32 C 2.9) or not (0.85, 1.4). 64
+// slices of 2048 x 1024: 8 records each 27 against 29 us, 16 38 against 30, 64 100
+// against 36; one of 8192 x 2048: 64 records 14 against 22, 128 23 and 23, 256 42 against
+// 34; one of 1024 x 4096, where 4 tiles of the persistent kernel are all there are: 1024
+// records 45 against 60. Only the device knows the slots' records, the rule goes by the mean.
+static bool ring_pays(const Fp8Args &a, int sides, bool f32)
+{
+    const int64_t slots = std::min(a.P, a.M), rows = a.M / slots, cols = sides == 2 ? 128 : 256;
+    const double few = 4.0 + 0.16e-6 * ((double)a.M / 16 + slots / 2.0) * a.N * sides * a.K;
+    const int64_t tiles = slots * ((rows + 255) / 256) * ((a.N + cols - 1) / cols);
+    const double ring = (tiles + 255) / 256 * (5.0 + (double)fp8_blocks(a.K) * (rows > 128 ? (f32 ? 2.9 : 1.7) : (f32 ? 1.4 : 0.85)));
+    return ring < few || row_tiles(a, 16) * (a.N / 8 + 1) >= 1 << 22;   // a launch has fewer than 2^32 threads
+}
 
 template <int EPI, bool DEC>
 static hipError_t launch_ring(const Fp8Args &a, hipStream_t st)
@@ -965,21 +978,54 @@ static hipError_t launch_ring(const Fp8Args &a, hipStream_t st)
     return hipGetLastError();
 }
 
-hipError_t launch_matmul_fp8(const Fp8Args &a, hipStream_t st)
+// Weight rows a workgroup, 16 nt: 64 where that leaves 256 workgroups (64 records of 8
+// slices of 4096 x 14336: 77 us, 83 with 32 and 92 with 16), else 32, for one product only from 192 of
+// them on (one record of 7168 x 2048: 5.3 and 5.7 us), else 16 (4096 x 4096: 6.4, with 32 7.7).
+// Waves: as many as find a batch of 4 steps each (64 slices of 2048 x 512, 16 records: 6.1 us
+// with 1 and 13.6 with 4; of 2048 x 1024, 128 records: 22 with 2, 39 with 4), 8 only
+// where workgroups are few (one record of 2048 x 7168: 7.8, with 4 8.6; 64 of 8 slices
+// of 4096 x 14336 92 and 78).
+template <int EPI>
+static hipError_t launch_few(const Fp8Args &a, float *hw, hipStream_t st)
 {
-    if (a.M == 0) return hipSuccess;
-    if (ring_pays(a)) return a.c_bf16 ? launch_ring<EPI_STORE, false>(a, st) : launch_ring<EPI_STORE, true>(a, st);
-    const int64_t grid = row_tiles(a, 16) * (a.N / 64);
-    hipLaunchKernelGGL((k_matmul_few<4, 4>), dim3((unsigned)grid), dim3(256), 0, st, a);
+    constexpr int G = EPI == EPI_GATE_UP ? 2 : 1;
+    const int64_t tiles = row_tiles(a, 16), KB = fp8_blocks(a.K);
+    auto groups = [&](int nt) { return tiles * ((a.N + 16 * nt / G - 1) / (16 * nt / G)); };
+    const int nt = groups(4) >= 256 ? 4 : groups(2) >= 192 || G == 2 ? 2 : 1;
+    const int w = KB < 8 ? 1 : KB < 16 ? 2 : KB < 32 || groups(nt) >= 512 ? 4 : 8;
+    auto go = [&](auto nt_t, auto w_t) {
+        constexpr int NT = decltype(nt_t)::value, W = decltype(w_t)::value;
+        if constexpr (NT >= G)
+            hipLaunchKernelGGL((k_few<EPI, NT, W>), dim3((unsigned)groups(NT)), dim3(64 * W), 0, st, a, hw);
+    };
+    auto with = [&](auto nt_t) {
+        if (w == 1) go(nt_t, std::integral_constant<int, 1>());
+        else if (w == 2) go(nt_t, std::integral_constant<int, 2>());
+        else if (w == 4) go(nt_t, std::integral_constant<int, 4>());
+        else go(nt_t, std::integral_constant<int, 8>());
+    };
+    if (nt == 1) with(std::integral_constant<int, 1>());
+    else if (nt == 2) with(std::integral_constant<int, 2>());
+    else with(std::integral_constant<int, 4>());
     return hipGetLastError();
 }
 
-hipError_t launch_gate_up_fp8(const Fp8Args &a, hipStream_t st)
+hipError_t launch_matmul_fp8(const Fp8Args &a, hipStream_t st)
 {
     if (a.M == 0) return hipSuccess;
-    if (ring_pays(a)) return launch_ring<EPI_GATE_UP, false>(a, st);
-    const int64_t grid = row_tiles(a, 16) * fp8_blocks(a.N);
-    hipLaunchKernelGGL(k_gate_up_few, dim3((unsigned)grid), dim3(1024), 0, st, a);
+    if (ring_pays(a, 1, !a.c_bf16)) return a.c_bf16 ? launch_ring<EPI_STORE, false>(a, st) : launch_ring<EPI_STORE, true>(a, st);
+    return launch_few<EPI_STORE>(a, nullptr, st);
+}
+
+size_t gate_up_fp8_workspace(const Fp8Args &a) { return a.M == 0 || ring_pays(a, 2, false) ? 0 : (size_t)a.M * a.N * 4; }
+
+hipError_t launch_gate_up_fp8(const Fp8Args &a, void *ws, hipStream_t st)
+{
+    if (a.M == 0) return hipSuccess;
+    if (ring_pays(a, 2, false)) return launch_ring<EPI_GATE_UP, false>(a, st);
+    const hipError_t e = launch_few<EPI_GATE_UP>(a, (float *)ws, st);
+    if (e != hipSuccess) return e;
+    quantize_rows(ws, false, a.M, a.N, a.N, (uint8_t *)a.C, a.Hs, a.slot_offset, a.slot_offset ? a.slot_offset + a.P : nullptr, st);
     return hipGetLastError();
 }
 

@@ -37,7 +37,8 @@ BAD = (dict(M=-1), dict(N=0), dict(K=0), dict(rows=-1), dict(P=0), dict(P=513, o
        dict(rows=3), dict(rows=0, ri=0x10), dict(A=None), dict(As=None), dict(W=None), dict(Ws=None), dict(C=None), dict(A=0x1008),
        dict(As=0x2008), dict(W=0x4008), dict(Ws=0x5002), dict(C=0x8008), dict(P=2, off=0x10, stride=4095, sstride=1),
        dict(P=2, off=0x10, stride=4104, sstride=1), dict(P=2, off=0x10, stride=4096, sstride=0))
-UNSUPPORTED = (dict(N=96, ldc=96), dict(K=96), dict(K=(1 << 20) + 64), dict(M=1 << 30, rows=1 << 30))
+UNSUPPORTED = (dict(N=96, ldc=96), dict(K=96), dict(K=(1 << 20) + 64), dict(M=1 << 30, rows=1 << 30, N=1 << 15, ldc=1 << 15),
+               dict(rows=(1 << 30) + 1))
 
 
 def test_matmul_refusals():
@@ -54,17 +55,22 @@ def test_matmul_refusals():
 
 @pytest.mark.parametrize("which", ["Wg", "Wu"])
 def test_gate_up_refusals(which):
-    def status(Hs=0x9000, **kw):
+    def status(Hs=0x9000, ws=0xa0000, n=1 << 40, **kw):
         a = dict(PRODUCT, **kw)
         good = (PRODUCT["W"], PRODUCT["Ws"])
         g, u = ((a["W"], a["Ws"]), good) if which == "Wg" else (good, (a["W"], a["Ws"]))
         return L.moe_gate_up_fp8(a["M"], a["N"], a["K"], a["A"], a["As"], a["rows"], a["ri"], a["off"], a["P"], *g, *u, a["stride"],
-                                 a["sstride"], a["C"], Hs, None)
+                                 a["sstride"], a["C"], Hs, ws, n, None)
     assert status(M=0, A=None, As=None, W=None, Ws=None, C=None, rows=0) == B.MOE_OK
     for kw in BAD + (dict(Hs=None),):
         assert status(**kw) == INV, kw
     for kw in UNSUPPORTED:
         assert status(**kw) == UN, kw
+    need = B.moe_gate_up_fp8_workspace_bytes(4, 64, 64, 1)
+    assert need == 4 * 4 * 64 and B.moe_gate_up_fp8_workspace_bytes(0, 64, 64, 1) == 0
+    assert B.moe_gate_up_fp8_workspace_bytes(32768, 1024, 2048, 64) == 0      # many records a slot
+    for kw in (dict(ws=None), dict(ws=0xa0010), dict(n=need - 1)):
+        assert status(**kw) == WS, kw
 
 
 def test_combine_refusals():

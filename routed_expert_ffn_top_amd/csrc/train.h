@@ -2,6 +2,8 @@
 // balance loss and the gradient of the router's logits.
 #pragma once
 
+#include <algorithm>
+
 #include "common.h"
 
 namespace moe {
@@ -24,6 +26,7 @@ hipError_t launch_combine_rows(const CombineArgs &a, hipStream_t st);
 hipError_t launch_combine_rows_backward(const CombineArgs &a, hipStream_t st);
 
 constexpr int kMaxSeq = 4096;    // sequences of a balance call
+constexpr int kMaxChunk = 256;   // tokens of a chunk of it, 64 a wave
 
 struct BalanceArgs {
     int T, E, k, kp, renorm;
@@ -37,23 +40,25 @@ struct BalanceArgs {
     float *prob, *slope;         // [S][E]
 };
 struct BalanceLayout {
-    size_t chunk;   // int32[V][2]: sequence of a chunk (-1: none), tokens counted
+    size_t entry;   // int32[V][2]: sequence, tokens counted
     size_t count;   // int32[V][E]
     size_t prob;    // float[V][E]
     size_t part;    // double[S][ceil(E/32)]
     size_t ticket;  // uint32
     size_t total;
-    int ch, V;      // tokens a chunk, chunks at most
+    int ch, chunks, V;
 };
-// Tokens a chunk: a chunk is what a workgroup sums, 4 waves of its tokens each.
-// 1024 chunks and more fill the GPU; the sums over the chunks follow.
+// Tokens a chunk: what a workgroup sums, 4 waves of its tokens each, at most 64 a wave.
+// 1024 chunks and more fill the GPU; the sums over them follow. A chunk has an entry for each
+// sequence that it meets, one of them the one behind the last: V at most.
 inline BalanceLayout balance_layout(int64_t T, int E, int S)
 {
     BalanceLayout w{};
-    w.ch = T <= 16384 ? 16 : T <= 65536 ? 64 : 256;
-    w.V = (int)((T + w.ch - 1) / w.ch + S);
+    w.ch = T <= 16384 ? 16 : T <= 65536 ? 64 : kMaxChunk;
+    w.chunks = (int)std::max<int64_t>((T + w.ch - 1) / w.ch, 1);
+    w.V = w.chunks + S;
     size_t o = 0;
-    w.chunk = o;  o = align_up(o + (size_t)w.V * 8, 256);
+    w.entry = o;  o = align_up(o + (size_t)w.V * 8, 256);
     w.count = o;  o = align_up(o + (size_t)w.V * E * 4, 256);
     w.prob = o;   o = align_up(o + (size_t)w.V * E * 4, 256);
     w.part = o;   o = align_up(o + (size_t)S * ((E + 31) / 32) * 8, 256);

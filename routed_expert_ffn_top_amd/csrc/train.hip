@@ -2,6 +2,8 @@
 // router: the records' rows summed into their tokens and the gradients of that
 // sum, the load-balancing loss of a routing, and the gradient of the router's
 // logits.
+#include <initializer_list>
+
 #include "device.h"
 #include "train.h"
 
@@ -11,17 +13,26 @@ namespace {
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
+// Over a wave's 64 lanes, the same result in all of them: exchanges within rows of 16
+// as operands of the instructions, the four rows' results through scalar registers (a shuffle
+// through LDS takes some 100 cycles, and a token has three of these in a row).
+template <class F>
+__device__ __forceinline__ float wave_reduce(float v, F op)
+{
+    v = op(v, __uint_as_float(dpp<0xB1>(__float_as_uint(v))));    // lane ^ 1
+    v = op(v, __uint_as_float(dpp<0x4E>(__float_as_uint(v))));    // lane ^ 2
+    v = op(v, __uint_as_float(dpp<0x141>(__float_as_uint(v))));   // 7 - lane of 8
+    v = op(v, __uint_as_float(dpp<0x140>(__float_as_uint(v))));   // 15 - lane of 16
+    auto row = [&](int r) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane(__float_as_int(v), 16 * r)); };
+    return op(op(row(0), row(1)), op(row(2), row(3)));
+}
 __device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-    return v;
+    return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float wave_sum(float v)
 {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
+    return wave_reduce(v, [](float a, float b) { return a + b; });
 }
 
 // ---------------------------------------------------------------------------
@@ -158,258 +169,320 @@ __global__ __launch_bounds__(256) void k_combine_rows_backward(CombineArgs a)
 // all experts have in common, so what is kept for it is the same with c_e less
 // its mean, which the differences there do not lose in rounding.
 //
-// Three steps: chunks of up to w.ch tokens of one sequence, a workgroup each
-// (sums of at most w.ch / 4 terms a wave in fp32, then 4 waves); the chunks of
-// a sequence, 32 experts a workgroup, in fp64; the last of those workgroups
-// sums the loss. Every sum is in a fixed order.
+// Three steps: chunks of w.ch tokens, a workgroup each, which writes an entry for each
+// sequence that it meets (sums of at most w.ch / 4 terms a wave in fp32, then 4 waves);
+// the entries of a sequence, 32 experts at a time, in fp64; the last of those
+// workgroups sums the loss. Every sum is in a fixed order. Entry b + s is chunk b's of
+// sequence s: that is in ascending order of both, and every entry is written.
 
-// Softmax numerators of a token's logits, C a lane (expert lane + 64 c), and their sum.
+// C experts a lane: with V, C lane + c, read and written together (rows of whole 4 C bytes), else lane + 64 c.
+template <int C, bool V>
+__device__ __forceinline__ int expert(int lane, int c) { return V ? lane * C + c : lane + 64 * c; }
+template <int C, bool V>
+__device__ __forceinline__ int lane_of(int e) { return V ? e / C : e & 63; }
+template <int C, bool V>
+__device__ __forceinline__ int place_of(int e) { return V ? e % C : e >> 6; }
 template <int C>
-__device__ __forceinline__ float numerators(const float *L, int E, int lane, float (&z)[C])
+struct Row { typedef float type __attribute__((ext_vector_type(C))); };
+// A row's values, `none` past E.
+template <int C, bool V>
+__device__ __forceinline__ void load_experts(const float *L, int E, int lane, float (&v)[C], float none)
+{
+    if constexpr (V) {
+        const bool in = lane * C < E;
+        const typename Row<C>::type w = *(const typename Row<C>::type *)(L + (in ? lane * C : 0));
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = in ? w[c] : none;
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = lane + 64 * c < E ? L[lane + 64 * c] : none;
+    }
+}
+// Softmax numerators in place, and their sum.
+template <int C>
+__device__ __forceinline__ float numerators(float (&z)[C])
 {
     const float none = -__builtin_huge_valf();
-    float v[C], m = none, s = 0.0f;
+    float m = none, s = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int e = lane + 64 * c;
-        v[c] = e < E ? L[e] : none;
-        if (v[c] != v[c]) v[c] = none;
-        m = fmaxf(m, v[c]);
+        if (z[c] != z[c]) z[c] = none;
+        m = fmaxf(m, z[c]);
     }
     m = wave_max(m);
     if (m == none) m = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        z[c] = expf(v[c] - m);
+        z[c] = expf(z[c] - m);
         s += z[c];
     }
     return wave_sum(s);
 }
+// 1 / s, and 0 for a row without a finite logit.
+__device__ __forceinline__ float over(float s) { return s > 0.0f || s != s ? 1.0f / s : 0.0f; }
 
 __device__ __forceinline__ void seq_range(const int32_t *off, int T, int s, int *lo, int *hi)
 {
     *lo = off ? min(max(off[s], 0), T) : 0;
     *hi = off ? min(max(off[s + 1], *lo), T) : T;
 }
+// The last of offsets 0 .. S that is at most t, 64 of them at a time; -1 for none. Every lane.
+__device__ __forceinline__ int seq_at(const int32_t *off, int S, int64_t t, int lane)
+{
+    int first = 0, step = 1;
+    while (step * 64 < S + 1) step *= 64;
+    for (;; step /= 64) {
+        const int i = first + lane * step;
+        const int n = __popcll(__ballot(i <= S && off[min(i, S)] <= t));
+        if (n == 0) return -1;
+        first += (n - 1) * step;
+        if (step == 1) return min(first, S);
+    }
+}
 
 template <int C>
-__global__ __launch_bounds__(256) void k_balance_chunks(BalanceArgs a, int ch, int32_t *__restrict__ chunk,
+__global__ __launch_bounds__(256) void k_balance_chunks(BalanceArgs a, int ch, int32_t *__restrict__ entry,
                                                         int32_t *__restrict__ count, float *__restrict__ prob,
                                                         uint32_t *__restrict__ ticket)
 {
     __shared__ float s_p[4][64 * C];
-    __shared__ int32_t s_c[64 * C], s_n[4];
+    __shared__ int32_t s_c[64 * C], s_n[4], s_list[kMaxChunk], s_many;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b = blockIdx.x;
+    if (threadIdx.x == 0) s_many = 0;
     if (b == 0 && threadIdx.x == 0) *ticket = 0;   // for the next kernel
-    // the sequence whose chunk this is
-    int run = 0, seq = -1, t0 = 0, t1 = 0;
-    for (int q = 0; q < a.S && seq < 0; q += 64) {
-        int lo = 0, hi = 0;
-        if (q + lane < a.S) seq_range(a.seq_offset, a.T, q + lane, &lo, &hi);
-        const int n = (hi - lo + ch - 1) / ch, inc = run + wave_incl_scan(n, lane);
-        const uint64_t mine = __ballot(b < inc && b >= inc - n);
-        if (mine) {
-            const int l = __builtin_ctzll(mine);
-            seq = q + l;
-            t0 = __builtin_amdgcn_readlane(lo, l) + (b - (__builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(n, l))) * ch;
-            t1 = min(t0 + ch, __builtin_amdgcn_readlane(hi, l));
-        }
-        run = __builtin_amdgcn_readlane(inc, 63);
+    const int64_t t0 = (int64_t)b * ch, t1 = t0 + ch;
+    // the sequences that this chunk has entries of
+    int s0 = 0, s1 = 0;
+    if (a.seq_offset) {
+        s0 = b == 0 ? 0 : max(seq_at(a.seq_offset, a.S, t0, lane), 0);
+        s1 = max(seq_at(a.seq_offset, a.S, t1, lane), s0);
     }
-    if (seq < 0) {
-        if (threadIdx.x == 0) chunk[2 * b] = -1, chunk[2 * b + 1] = 0;
-        return;
-    }
-    for (int e = threadIdx.x; e < 64 * C; e += 256) s_c[e] = 0;
+    auto range = [&](int s, int *lo, int *hi) {
+        *lo = *hi = 0;
+        if (s < a.S) seq_range(a.seq_offset, a.T, s, lo, hi);
+        *lo = (int)max((int64_t)*lo, t0);
+        *hi = (int)min((int64_t)*hi, t1);
+    };
+    // those with tokens here, each with one of its own
     __syncthreads();
-    float p[C];
+    for (int s = s0 + (int)threadIdx.x; s <= s1; s += 256) {
+        int lo, hi;
+        range(s, &lo, &hi);
+        const int i = lo < hi ? atomicAdd(&s_many, 1) : kMaxChunk;
+        if (i < kMaxChunk)
+            s_list[i] = s;
+        else
+            entry[2 * ((int64_t)b + s)] = s, entry[2 * ((int64_t)b + s) + 1] = 0;
+    }
+    __syncthreads();
+    for (int i = 0; i < min(s_many, kMaxChunk); ++i) {
+        const int s = s_list[i];
+        int lo, hi;
+        range(s, &lo, &hi);
+        const int64_t at = (int64_t)b + s;
+        __syncthreads();   // of the entry before
+        for (int e = threadIdx.x; e < 64 * C; e += 256) s_c[e] = 0;
+        __syncthreads();
+        // this wave's tokens lo + wave + 4 i, those that count
+        const int mine = lo + wave + 4 * lane;
+        uint64_t live = __ballot(mine < hi && (!a.mask || a.mask[min(mine, hi - 1)] != 0));
+        const int n = __popcll(live);
+        float p[C], next[C];
+        int next_id = -1;
 #pragma unroll
-    for (int c = 0; c < C; ++c) p[c] = 0.0f;
-    int n = 0;
-    for (int t = t0 + wave; t < t1; t += 4) {
-        if (a.mask && a.mask[t] == 0) continue;
-        ++n;
-        float z[C];
-        const float s = numerators<C>(a.logits + (int64_t)t * a.E, a.E, lane, z);
-        const float r = s > 0.0f || s != s ? 1.0f / s : 0.0f;
+        for (int c = 0; c < C; ++c) p[c] = 0.0f;
+        auto ask = [&]() {   // the next token's logits and routes
+            const int64_t t = lo + wave + 4 * __builtin_ctzll(live);
+            load_experts<C, false>(a.logits + t * a.E, a.E, lane, next, -__builtin_huge_valf());
+            next_id = lane < a.k ? a.idx[t * a.kp + lane] : -1;
+        };
+        if (live) ask();
+        while (live) {
+            float z[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) p[c] = fmaf(z[c], r, p[c]);
-        if (lane < a.k) {
-            const int e = a.idx[(int64_t)t * a.kp + lane];
+            for (int c = 0; c < C; ++c) z[c] = next[c];
+            const int e = next_id;
+            live &= live - 1;
+            if (live) ask();
+            const float r = over(numerators<C>(z));
+#pragma unroll
+            for (int c = 0; c < C; ++c) p[c] = fmaf(z[c], r, p[c]);
             if (e >= 0 && e < a.E) atomicAdd(&s_c[e], 1);   // whole numbers: any order
         }
-    }
 #pragma unroll
-    for (int c = 0; c < C; ++c) s_p[wave][lane + 64 * c] = p[c];
-    if (lane == 0) s_n[wave] = n;
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += 256) {
-        prob[(int64_t)b * a.E + e] = (s_p[0][e] + s_p[1][e]) + (s_p[2][e] + s_p[3][e]);
-        count[(int64_t)b * a.E + e] = s_c[e];
+        for (int c = 0; c < C; ++c) s_p[wave][lane + 64 * c] = p[c];
+        if (lane == 0) s_n[wave] = n;
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += 256) {
+            prob[at * a.E + e] = (s_p[0][e] + s_p[1][e]) + (s_p[2][e] + s_p[3][e]);
+            count[at * a.E + e] = s_c[e];
+        }
+        if (threadIdx.x == 0) entry[2 * at] = s, entry[2 * at + 1] = s_n[0] + s_n[1] + s_n[2] + s_n[3];
     }
-    if (threadIdx.x == 0) chunk[2 * b] = seq, chunk[2 * b + 1] = s_n[0] + s_n[1] + s_n[2] + s_n[3];
 }
 
-// Workgroup (sequence, 32 experts): 32 lanes of experts x 32 shares of the chunks.
-__global__ __launch_bounds__(1024) void k_balance_sequences(BalanceArgs a, int V, const int32_t *__restrict__ chunk,
+// Workgroup (sequence, y): 32 experts at a time, 32 shares of the entries.
+__global__ __launch_bounds__(1024) void k_balance_sequences(BalanceArgs a, int ch, int V, const int32_t *__restrict__ entry,
                                                             const int32_t *__restrict__ count,
                                                             const float *__restrict__ prob, double *part,
                                                             uint32_t *ticket)
 {
     __shared__ uint32_t s_full[kMaxSeq / 32];   // sequences with counted tokens
-    __shared__ int32_t s_lo, s_hi, s_n, s_some, s_last;
-    __shared__ double s_p[32][33];
-    __shared__ int32_t s_c[32][33];
-    const int tid = threadIdx.x, seq = blockIdx.x, eb = blockIdx.y;
+    __shared__ int32_t s_n, s_some, s_last;
+    __shared__ double s_p[16][32];
+    __shared__ int32_t s_c[16][32];
+    const int tid = threadIdx.x, seq = blockIdx.x;
     for (int i = tid; i < kMaxSeq / 32; i += 1024) s_full[i] = 0;
-    if (tid == 0) s_lo = V, s_hi = 0, s_n = 0, s_some = 0;
+    if (tid == 0) s_n = 0, s_some = 0;
     __syncthreads();
     for (int v = tid; v < V; v += 1024) {
-        const int s = chunk[2 * v], n = chunk[2 * v + 1];
-        if (s < 0) continue;
-        if (n > 0) atomicOr(&s_full[s / 32], 1u << (s & 31));
-        if (s == seq) {
-            atomicMin(&s_lo, v);
-            atomicMax(&s_hi, v + 1);
-            atomicAdd(&s_n, n);
-        }
+        const int s = entry[2 * v], n = entry[2 * v + 1];
+        if (n <= 0 || (uint32_t)s >= (uint32_t)a.S) continue;
+        atomicOr(&s_full[s / 32], 1u << (s & 31));
+        if (s == seq) atomicAdd(&s_n, n);
     }
     __syncthreads();
     if (tid < kMaxSeq / 32 && s_full[tid]) atomicAdd(&s_some, __popc(s_full[tid]));
-    const int el = tid & 31, share = tid >> 5, e = eb * 32 + el;
-    double p = 0.0;
-    int c = 0;
-    if (e < a.E)
-        for (int v = s_lo + share; v < s_hi; v += 32) {
-            p += (double)prob[(int64_t)v * a.E + e];
-            c += count[(int64_t)v * a.E + e];
-        }
-    s_p[share][el] = p;
-    s_c[share][el] = c;
-    __syncthreads();
-    const double n = s_n, some = s_some;
-    if (tid < 32) {
+    int lo, hi;
+    seq_range(a.seq_offset, a.T, seq, &lo, &hi);
+    const int b0 = lo / ch, b1 = hi > lo ? (hi - 1) / ch + 1 : b0;   // the chunks that have tokens of it
+    const int el = tid & 31, share = tid >> 5;
+    double loss = 0.0;
+    for (int eb = blockIdx.y; eb * 32 < a.E; eb += gridDim.y) {
+        const int e = eb * 32 + el;
+        double p = 0.0;
+        int c = 0;
+        if (e < a.E)
+            for (int b = b0 + share; b < b1; b += 32) {
+                const int64_t at = ((int64_t)b + seq) * a.E + e;
+                p += (double)prob[at];
+                c += count[at];
+            }
+        p += __shfl_xor(p, 32, 64);
+        c += __shfl_xor(c, 32, 64);
+        __syncthreads();
+        if ((tid & 32) == 0) s_p[share / 2][el] = p, s_c[share / 2][el] = c;
+        __syncthreads();
+        if (tid >= 32) continue;
         p = 0.0;
         c = 0;
-        for (int q = 0; q < 32; ++q) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
             p += s_p[q][el];
             c += s_c[q][el];
         }
-        double l = 0.0;
         if (e < a.E) {
+            const double n = s_n, some = s_some;
             const int64_t at = (int64_t)seq * a.E + e;
             const double per = n > 0.0 ? a.E / (a.k * n) : 0.0, mean = a.k * n / a.E;
             p = n > 0.0 ? p / n : 0.0;
             a.counts[at] = c;
             a.prob[at] = (float)p;
             a.slope[at] = n > 0.0 ? (float)(per / (n * some) * (c - mean)) : 0.0f;
-            l = some > 0.0 ? per / some * c * p : 0.0;
+            loss += some > 0.0 ? per / some * c * p : 0.0;
         }
-        s_p[0][el] = l;   // the same wave's
     }
-    __syncthreads();
     const int blocks = gridDim.x * gridDim.y;
-    if (tid == 0) {
-        double l = 0.0;
-        for (int q = 0; q < 32; ++q) l += s_p[0][q];
-        __hip_atomic_store(&part[seq * gridDim.y + eb], l, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)blocks - 1;
+    if (tid < 32) {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) loss += __shfl_xor(loss, o, 64);
+        if (tid == 0) {
+            __hip_atomic_store(&part[seq * gridDim.y + blockIdx.y], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)blocks - 1;
+        }
     }
     __syncthreads();
-    if (!s_last) return;
-    double l = 0.0;
-    for (int i = tid; i < blocks; i += 1024) l += __hip_atomic_load(&part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_p[tid >> 5][tid & 31] = l;
-    __syncthreads();
-    if (tid == 0) {
-        l = 0.0;
-        for (int i = 0; i < 1024; ++i) l += s_p[i >> 5][i & 31];
-        *a.loss = (float)l;
-    }
+    if (!s_last || tid >= 64) return;
+    loss = 0.0;
+    for (int i = tid; i < blocks; i += 64) loss += __hip_atomic_load(&part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) loss += __shfl_xor(loss, o, 64);
+    if (tid == 0) *a.loss = (float)loss;
 }
 
 // dL = p (u - sum u p) with u = d_loss slope (counted tokens) and, for route
 // weights that are not renormalised, their gradients; renormalised ones, a
-// softmax over the chosen, add w (dw - sum w dw). A wave a token.
-template <int C>
+// softmax over the chosen, add w (dw - sum w dw). A wave a token; lane j holds route j's
+// id and gradient, which pass to the others through scalar registers.
+template <int C, bool V>
 __global__ __launch_bounds__(256) void k_router_backward(RouterBackArgs a)
 {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (t >= a.T) return;
     float z[C], u[C], x[C];
-    const float s = numerators<C>(a.logits + t * a.E, a.E, lane, z);
-    const float r = s > 0.0f || s != s ? 1.0f / s : 0.0f;
+    load_experts<C, V>(a.logits + t * a.E, a.E, lane, z, -__builtin_huge_valf());
+    int id = -1;
+    float dw = 0.0f;
+    if (a.dw && lane < a.k) {
+        id = a.idx[t * a.kp + lane];
+        if (id >= a.E) id = -1;
+        if (id >= 0) dw = a.dw[t * a.kp + lane];
+    }
 #pragma unroll
     for (int c = 0; c < C; ++c) u[c] = x[c] = 0.0f;
     if (a.slope && (!a.mask || a.mask[t] != 0)) {
-        int seq = 0;
-        bool in = true;
-        if (a.seq_offset) {   // the last sequence that starts at or before t, 64 offsets at a time
-            int first = 0, many = a.S + 1, step = 1;
-            while (step * 64 < many) step *= 64;
-            for (;; step /= 64) {
-                const int i = first + lane * step;
-                const bool le = i <= a.S && a.seq_offset[min(i, a.S)] <= t;
-                const int n = __popcll(__ballot(le));
-                if (n == 0) {
-                    in = false;
-                    break;
-                }
-                first += (n - 1) * step;
-                if (step == 1) break;
-            }
-            seq = first;
-            in = in && seq < a.S;
-        }
-        if (in) {
+        const int seq = a.seq_offset ? seq_at(a.seq_offset, a.S, t, lane) : 0;
+        if (seq >= 0 && seq < a.S) {
             const float g = a.d_loss ? *a.d_loss : 1.0f;
+            load_experts<C, V>(a.slope + (int64_t)seq * a.E, a.E, lane, u, 0.0f);
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (lane + 64 * c < a.E) u[c] = g * a.slope[(int64_t)seq * a.E + lane + 64 * c];
+            for (int c = 0; c < C; ++c) u[c] *= g;
         }
     }
+    const float r = over(numerators<C>(z));
     if (a.dw) {
-        const int32_t *id = a.idx + t * a.kp;
-        const float *dw = a.dw + t * a.kp;
+        auto id_of = [&](int j) { return __builtin_amdgcn_readlane(id, j); };
+        auto of = [&](float v, int j) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j)); };
         if (a.renorm) {
-            // sums over the routes: lane j holds route j's
-            float zj = 0.0f, den = 0.0f, dot = 0.0f;
+            float zj = 0.0f;   // lane j: the numerator of route j
             for (int j = 0; j < a.k; ++j) {
-                const int e = id[j];
-                const int c = e >> 6;
-                float v = 0.0f;
+                const int e = id_of(j);
+                if (e < 0) continue;
+                float v = z[0];
 #pragma unroll
-                for (int q = 0; q < C; ++q)
-                    if (q == c) v = z[q];
-                v = e >= 0 && e < a.E ? __shfl(v, e & 63, 64) : 0.0f;
-                den += v;
-                dot = fmaf(v, dw[j], dot);
+                for (int q = 1; q < C; ++q)
+                    if (place_of<C, V>(e) == q) v = z[q];
+                v = of(v, lane_of<C, V>(e));
                 if (lane == j) zj = v;
             }
-            const float rd = den > 0.0f || den != den ? 1.0f / den : 0.0f;
-            const float mine = lane < a.k ? zj * rd * (dw[lane] - dot * rd) : 0.0f;
+            const float rd = over(wave_sum(zj)), w = zj * rd;
+            const float dot = wave_sum(w * dw), mine = w * (dw - dot);
             for (int j = 0; j < a.k; ++j) {
-                const float v = __shfl(mine, j, 64);
-                const int e = id[j];
+                const int e = id_of(j);
+                const float v = of(mine, j);
 #pragma unroll
                 for (int q = 0; q < C; ++q)
-                    if (e == lane + 64 * q) x[q] += v;
+                    if (e == expert<C, V>(lane, q)) x[q] += v;
             }
         } else {
-            for (int j = 0; j < a.k; ++j)
+            for (int j = 0; j < a.k; ++j) {
+                const int e = id_of(j);
+                const float v = of(dw, j);
 #pragma unroll
                 for (int q = 0; q < C; ++q)
-                    if (id[j] == lane + 64 * q && id[j] < a.E) u[q] += dw[j];
+                    if (e == expert<C, V>(lane, q)) u[q] += v;
+            }
         }
     }
     float dot = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) dot = fmaf(u[c], z[c] * r, dot);
+    for (int c = 0; c < C; ++c) {
+        z[c] *= r;
+        dot = fmaf(u[c], z[c], dot);
+    }
     dot = wave_sum(dot);
+    float *out = a.dlogits + t * a.E;
+    if constexpr (V) {
+        typename Row<C>::type w;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (lane + 64 * c < a.E) a.dlogits[t * a.E + lane + 64 * c] = fmaf(z[c] * r, u[c] - dot, x[c]);
+        for (int c = 0; c < C; ++c) w[c] = fmaf(z[c], u[c] - dot, x[c]);
+        if (lane * C < a.E) *(typename Row<C>::type *)(out + lane * C) = w;
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (lane + 64 * c < a.E) out[lane + 64 * c] = fmaf(z[c], u[c] - dot, x[c]);
+    }
 }
 
 }  // namespace
@@ -454,23 +527,37 @@ hipError_t launch_combine_rows_backward(const CombineArgs &a, hipStream_t st)
 hipError_t launch_balance(const BalanceArgs &a, const BalanceLayout &w, void *ws, hipStream_t st)
 {
     char *p = (char *)ws;
-    int32_t *chunk = (int32_t *)(p + w.chunk), *count = (int32_t *)(p + w.count);
+    int32_t *entry = (int32_t *)(p + w.entry), *count = (int32_t *)(p + w.count);
     float *prob = (float *)(p + w.prob);
     uint32_t *ticket = (uint32_t *)(p + w.ticket);
     const auto kernel = a.E <= 64 ? k_balance_chunks<1> : a.E <= 128 ? k_balance_chunks<2> : k_balance_chunks<4>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)w.V), dim3(256), 0, st, a, w.ch, chunk, count, prob, ticket);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)w.chunks), dim3(256), 0, st, a, w.ch, entry, count, prob, ticket);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_balance_sequences, dim3((unsigned)a.S, (unsigned)((a.E + 31) / 32)), dim3(1024), 0, st, a, w.V, chunk,
-                       count, prob, (double *)(p + w.part), ticket);
+    // the experts over several workgroups where sequences are few and long
+    const unsigned y = a.S >= 256 ? 1 : (unsigned)((a.E + 31) / 32);
+    hipLaunchKernelGGL(k_balance_sequences, dim3((unsigned)a.S, y), dim3(1024), 0, st, a, w.ch, a.seq_offset ? w.V : w.chunks,
+                       entry, count, prob, (double *)(p + w.part), ticket);
     return hipGetLastError();
+}
+
+// Whether every row of E fp32 values of these arrays can be read C values at a time
+// (65536 rows of 256 backward: 43 us, 46 a value at a time; the forward pass gains nothing by it, 21 and 22).
+static bool together(int E, int C, std::initializer_list<const void *> rows)
+{
+    bool yes = E % C == 0;
+    for (const void *p : rows) yes = yes && ((uintptr_t)p & (4 * C - 1)) == 0;
+    return yes;
 }
 
 hipError_t launch_router_backward(const RouterBackArgs &a, hipStream_t st)
 {
     if (a.T == 0) return hipSuccess;
     const dim3 grid((unsigned)(((int64_t)a.T + 3) / 4));
-    const auto kernel = a.E <= 64 ? k_router_backward<1> : a.E <= 128 ? k_router_backward<2> : k_router_backward<4>;
+    const auto kernel =
+        a.E <= 64 ? k_router_backward<1, false>
+        : a.E <= 128 ? (together(a.E, 2, {a.logits, a.slope, a.dlogits}) ? k_router_backward<2, true> : k_router_backward<2, false>)
+                     : (together(a.E, 4, {a.logits, a.slope, a.dlogits}) ? k_router_backward<4, true> : k_router_backward<4, false>);
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, a);
     return hipGetLastError();
 }

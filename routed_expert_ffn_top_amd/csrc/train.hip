@@ -430,48 +430,57 @@ __global__ __launch_bounds__(256) void k_router_backward(RouterBackArgs a)
             for (int c = 0; c < C; ++c) u[c] *= g;
         }
     }
-    const float r = over(numerators<C>(z));
-    if (a.dw) {
-        auto id_of = [&](int j) { return __builtin_amdgcn_readlane(id, j); };
-        auto of = [&](float v, int j) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j)); };
-        if (a.renorm) {
-            float zj = 0.0f;   // lane j: the numerator of route j
-            for (int j = 0; j < a.k; ++j) {
-                const int e = id_of(j);
-                if (e < 0) continue;
-                float v = z[0];
+    auto id_of = [&](int j) { return __builtin_amdgcn_readlane(id, j); };
+    auto of = [&](float v, int j) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j)); };
+    if (a.dw && !a.renorm) {
+        for (int j = 0; j < a.k; ++j) {
+            const int e = id_of(j);
+            const float v = of(dw, j);
 #pragma unroll
-                for (int q = 1; q < C; ++q)
-                    if (place_of<C, V>(e) == q) v = z[q];
-                v = of(v, lane_of<C, V>(e));
-                if (lane == j) zj = v;
-            }
-            const float rd = over(wave_sum(zj)), w = zj * rd;
-            const float dot = wave_sum(w * dw), mine = w * (dw - dot);
-            for (int j = 0; j < a.k; ++j) {
-                const int e = id_of(j);
-                const float v = of(mine, j);
-#pragma unroll
-                for (int q = 0; q < C; ++q)
-                    if (e == expert<C, V>(lane, q)) x[q] += v;
-            }
-        } else {
-            for (int j = 0; j < a.k; ++j) {
-                const int e = id_of(j);
-                const float v = of(dw, j);
-#pragma unroll
-                for (int q = 0; q < C; ++q)
-                    if (e == expert<C, V>(lane, q)) u[q] += v;
-            }
+            for (int q = 0; q < C; ++q)
+                if (e == expert<C, V>(lane, q)) u[q] += v;
         }
     }
-    float dot = 0.0f;
+    // With nothing to pass on the row is 0 whatever its logits hold: padding may hold anything.
+    bool mine = false;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        z[c] *= r;
-        dot = fmaf(u[c], z[c], dot);
+    for (int c = 0; c < C; ++c) mine = mine || u[c] != 0.0f;
+    const bool some = __any(mine), chosen = a.dw && a.renorm && __any(dw != 0.0f);
+    float r = 0.0f, dot = 0.0f;
+    if (some || chosen) r = over(numerators<C>(z));
+    if (chosen) {
+        float zj = 0.0f;   // lane j: the numerator of route j
+        for (int j = 0; j < a.k; ++j) {
+            const int e = id_of(j);
+            if (e < 0) continue;
+            float v = z[0];
+#pragma unroll
+            for (int q = 1; q < C; ++q)
+                if (place_of<C, V>(e) == q) v = z[q];
+            v = of(v, lane_of<C, V>(e));
+            if (lane == j) zj = v;
+        }
+        const float rd = over(wave_sum(zj)), w = zj * rd;
+        const float mean = wave_sum(w * dw), part = w * (dw - mean);
+        for (int j = 0; j < a.k; ++j) {
+            const int e = id_of(j);
+            const float v = of(part, j);
+#pragma unroll
+            for (int q = 0; q < C; ++q)
+                if (e == expert<C, V>(lane, q)) x[q] += v;
+        }
     }
-    dot = wave_sum(dot);
+    if (some) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            z[c] *= r;
+            dot = fmaf(u[c], z[c], dot);
+        }
+        dot = wave_sum(dot);
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) z[c] = 0.0f;
+    }
     float *out = a.dlogits + t * a.E;
     if constexpr (V) {
         typename Row<C>::type w;

@@ -306,6 +306,57 @@ def test_balance_nothing_counted():
     B.moe_router_backward(none, L[:0], idx[:0], L[:0], slope=o["slope"])
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_padding_may_hold_anything(renorm, bad):
+    """Tokens that are not counted and whose weights have no gradient: 0, and nothing of theirs anywhere."""
+    T, E, k = 40, 100, 3
+    g = torch.Generator().manual_seed(11)
+    L, dw = torch.randn(T, E, generator=g), torch.randn(T, k, generator=g)
+    idx, mask = choice(L, k, 0, E), (torch.arange(T) % 3 != 0).to(torch.uint8)
+    dw[mask == 0] = 0.0
+    shape = B.make_shape(T, 64, 64, E, k, renorm=renorm)
+    got = []
+    for logits in (L, torch.where((mask == 0)[:, None] & (torch.arange(E) % 2 == 0), bad, L)):
+        o = run_balance(shape, logits.cuda(), idx.cuda(), 1, None, mask.cuda())
+        out = torch.full((T, E), 9.0, device="cuda")
+        B.moe_router_backward(shape, logits.cuda(), idx.cuda(), out, slope=o["slope"], d_topk_w=dw.cuda(), mask=mask.cuda())
+        got.append((o["loss"], o["prob"], out))
+    assert all(torch.equal(x, y) for x, y in zip(*got)) and bool((got[1][2][(mask == 0).cuda()] == 0).all())
+
+
+@pytest.mark.parametrize("E", [126, 128, 252, 256])
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_router_rows_of_every_alignment(E, at):
+    """Logits and gradients that begin at any multiple of 4 bytes: whether rows are read in pieces or not."""
+    T, k = 37, 4
+    g = torch.Generator().manual_seed(E)
+    L, dw = torch.randn(T, E, generator=g), torch.randn(T, k, generator=g).cuda()
+    idx = choice(L, k, 0, E).cuda()
+    for renorm in (True, False):
+        shape = B.make_shape(T, 64, 64, E, k, renorm=renorm)
+        outs = []
+        for shift in (0, at):
+            place = lambda: torch.empty(T * E + 4, device="cuda")[shift:shift + T * E].view(T, E)
+            logits, out = place(), place()
+            logits.copy_(L)
+            o = run_balance(shape, logits, idx, 1, None, None)
+            B.moe_router_backward(shape, logits, idx, out, slope=o["slope"], d_topk_w=dw)
+            outs.append((o["loss"], o["slope"], out.cpu().double()))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+        # another distribution of experts over lanes, another order of the same sums: twice their bound at worst
+        p = torch.softmax(L.double(), -1)
+        u = outs[0][1].cpu().double() + (0 if renorm else torch.zeros_like(p).scatter_add(1, idx.cpu().long(), dw.cpu().double()))
+        R = float(L.max() - L.min())
+        lim = 2 * (2 * (R + 18) + 16 + k) * U * p * (u.abs() + (u.abs() * p).sum(-1, keepdim=True)) + 2 * U * outs[0][2].abs()
+        if renorm:
+            c = idx.cpu().long()
+            w = torch.softmax(L.double().gather(1, c), -1)
+            d = dw.cpu().double().abs()
+            lim = lim.scatter_add(1, c, 2 * (2 * (R + 18) + 2 * k + 8) * U * w * (d + (w * d).sum(-1, keepdim=True)))
+        assert bool(((outs[0][2] - outs[1][2]).abs() <= lim + 1e-37).all())
+
+
 def test_balance_uniform_is_one():
     """Uniform routing and probabilities: the loss is 1 and its gradient 0."""
     T, E, k = 64, 8, 2

@@ -555,9 +555,9 @@ moe_status moe_dequantize_fp8(const void *codes, const void *scales,
  *                are not used with P = 1; P <= 512
  *   C            device [M][ldc] of c_dtype (MOE_DT_F32 or MOE_DT_BF16), N <=
  *                ldc < 2^21; C and its row stride 16-byte aligned
- * A weight's scale may be any fp32 number; a NaN or an infinity makes NaN of
- * what it meets, one below 2^-126 in magnitude counts as 2^-126 or as itself. Rows and
- * offsets out of range are brought into it on the device.
+ * A weight's scale may be any fp32 number; a NaN makes NaN of what it meets, an
+ * infinity NaN or infinity, and one below 2^-126 in magnitude counts as itself or
+ * as 0. Rows and offsets out of range are brought into it on the device.
  * C in bf16 of many records a slot (and H below) is multiplied on the fp8 matrix
  * instructions, which keep 14 bits of the products of 8 neighbouring k: 1.1e-5 of
  * the norm of C for normally distributed operands. fp32 C keeps 24 bits.

@@ -396,7 +396,8 @@ __global__ __launch_bounds__(64 * W) void k_few(Fp8Args a, float *__restrict__ h
 constexpr int kXcd = 8;
 constexpr int kStream = 2;   // buffer stores of C, which is not read here: non-temporal
 
-// A weight scale as m and the bits of 2^e; below 2^-126 as +-2^-127, NaN and infinity as NaN.
+// A weight scale as m and the bits of 2^e; NaN and infinity as NaN. What is below 2^-126 in
+// magnitude, which e cannot hold, counts as 0: its block's codes do, those of NaN aside.
 __device__ __forceinline__ float scale_m(float s)
 {
     const uint32_t u = __float_as_uint(s);
@@ -604,6 +605,28 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
         else if (n == 16) wait_vmcnt<16>();
         else wait_vmcnt<0>();
     };
+    // Scales that count as 0: a bit for each of a panel's 16 blocks of k and the tile's two row
+    // blocks. Such a block's codes are blanked in LDS, NaN left, before any wave reads them.
+    uint32_t zeros = 0;
+    auto read_zeros = [&](int pn) __attribute__((always_inline)) {
+        const float s = weight_scale(min(pn * 16 + (lane & 15), KB - 1), (lane >> 4) & 1);
+        zeros = (uint32_t)__ballot(fabsf(s) < 0x1p-126f);
+    };
+    auto blank = [&](int kb) __attribute__((always_inline)) {
+        const uint32_t here = zeros >> (kb & 15) & 0x10001u;
+        if (__builtin_expect(here == 0, 1)) return;
+        if (here >> (16 * (tid >> 8)) & 1)
+            for (int q = 0; q < 4; ++q) {
+                u32x4_t *p = (u32x4_t *)(lds + at_stage(kb) + CODES + tid * 64 + q * 16);
+                u32x4_t v = *p;
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t nan = ((v[c] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                    v[c] = nan - (nan >> 7);
+                }
+                *p = v;
+            }
+        lds_barrier();
+    };
     // The stage behind kb, the next tile's first one behind the last, is made visible: this
     // wave's reads of stage kb are done, its copies have landed, and behind the barrier so
     // have all waves'. Then stage kb's place is free, and `follow` requests the stage after that one
@@ -619,6 +642,10 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");   // for the compiler: reads stay behind
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        }
+        if (kb + 1 < KB) {
+            if ((kb & 15) == 15) read_zeros(kb / 16 + 1);
+            blank(kb + 1);
         }
     };
     auto follow = [&](int kb, int side) __attribute__((always_inline)) {
@@ -774,6 +801,8 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
             wait_behind(stores);
             lds_barrier();
         }
+        read_zeros(0);
+        blank(0);
         if (mine > 2) tile_loop(std::integral_constant<int, 4>());
         else if (mine > 0) tile_loop(std::integral_constant<int, 2>());
         else tile_loop(std::integral_constant<int, 0>());

@@ -215,10 +215,7 @@ SHAPES = [(1, 64, 64, 1), (1, 2048, 1024, 1), (3, 64, 128, 2), (8, 192, 192, 16)
           (2500, 640, 128, 2), (1537, 448, 64, 3), (40, 128, 4160, 2)]
 
 
-@pytest.mark.parametrize("M,N,K,P", SHAPES)
-@pytest.mark.parametrize("kind,scale", [("even", "any"), ("short", "pow2"), ("one", "signs")])
-@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
-def test_matmul(M, N, K, P, kind, scale, out):
+def check_matmul(M, N, K, P, kind, scale, out):
     g = torch.Generator().manual_seed(M + N + K + P)
     gather = kind != "one"
     rows = max(1, M // 3) if gather else M
@@ -243,14 +240,73 @@ def test_matmul(M, N, K, P, kind, scale, out):
         av = r64[lo:hi] if take is None else r64[take[lo:hi].long()]
         wv = weights64(w[s], ws[s])
         want = av @ wv.t()
-        lim = bound(av, wv, K, out is torch.bfloat16) + 1e-30
+        lim = bound(av, wv, K, out is torch.bfloat16) + 1e-37
         if out is torch.bfloat16:
             lim = lim + 2.0 ** -8 * (want.abs() + lim)
         err = (got[lo:hi, :N] - want).abs()
         assert bool((err <= lim).all()), f"slot {s}: {float((err / lim).max()):.3g} of the bound"
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 64, 192), (2100, 512, 320)])
+@pytest.mark.parametrize("M,N,K,P", SHAPES)
+@pytest.mark.parametrize("kind,scale", [("even", "any"), ("short", "pow2"), ("one", "signs")])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_matmul(M, N, K, P, kind, scale, out):
+    check_matmul(M, N, K, P, kind, scale, out)
+
+
+# Few records a slot at every number of weight rows and waves a workgroup
+FEW = [(640, 512, 1088, 8), (400, 320, 2112, 9), (300, 576, 4160, 4), (700, 768, 4160, 16), (260, 1024, 4160, 3), (1, 64, 4160, 1),
+       (5, 4096, 64, 2), (33, 8192, 2048, 1)]
+
+
+@pytest.mark.parametrize("M,N,K,P", FEW)
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_matmul_few(M, N, K, P, out):
+    check_matmul(M, N, K, P, "even", "any", out)
+
+
+# Many records a slot: one, two, several and many blocks of k, the last of 64 or 128; panels of 16 of them; tiles of 1 to
+# 256 records; slots without any; widths that end inside a tile
+MANY = [(4096, 1600, 64, 1), (4500, 2048, 64, 6), (4000, 1600, 128, 2), (4000, 1600, 192, 3), (3001, 1088, 448, 2), (2500, 1344, 576, 3),
+        (3000, 832, 2112, 1), (3000, 832, 4160, 2), (2100, 832, 2048, 1), (1600, 1024, 704, 40), (6000, 512, 1024, 300)]
+
+
+@pytest.mark.parametrize("M,N,K,P", MANY)
+@pytest.mark.parametrize("kind,scale", [("even", "any"), ("short", "pow2"), ("one", "signs")])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_matmul_many(M, N, K, P, kind, scale, out):
+    check_matmul(M, N, K, P, kind, scale, out)
+
+
+def test_matmul_most_slices():
+    check_matmul(9000, 512, 1088, 512, "even", "any", torch.bfloat16)
+
+
+@pytest.mark.parametrize("K", [64, 192])
+@pytest.mark.parametrize("gate_up", [False, True])
+def test_thousands_of_tiles(K, gate_up):
+    """Rows that recur with every tile: so must the results, over more tiles than a workgroup lists at once."""
+    g = torch.Generator().manual_seed(K)
+    N, R = 2048, 256 * 2200
+    a, as_ = quantise(torch.randn(256, K, generator=g).cuda())
+    w, ws = weights(g, 1, N, K, "any")
+    take = torch.arange(256, dtype=torch.int32, device="cuda").repeat(R // 256)
+    if gate_up:
+        assert B.moe_gate_up_fp8_workspace_bytes(R, N, K) == 0
+        H = torch.empty((R, N), dtype=torch.uint8, device="cuda")
+        Hs = torch.zeros((R, B.fp8_scale_bytes(N)), dtype=torch.uint8, device="cuda")
+        B.moe_gate_up_fp8(a, as_, w[0], ws[0] * 0.01, w[0], ws[0] * 0.01, H, Hs, row_index=take)
+        assert bool((H.view(-1, 256, N) == H[:256]).all()) and bool((Hs.view(-1, 256, Hs.shape[1]) == Hs[:256]).all())
+    else:
+        C = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
+        B.moe_matmul_fp8(a, as_, w[0], ws[0], C, row_index=take)
+        assert bool((C.view(-1, 256, N) == C[:256]).all())
+        av, wv = rows64(a, as_), weights64(w[0], ws[0])
+        want, lim = av @ wv.t(), bound(av, wv, K, True)
+        assert bool(((C[:256].cpu().double() - want).abs() <= lim + 2.0 ** -8 * (want.abs() + lim)).all())
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 64, 192), (2100, 512, 320), (4000, 1600, 320)])
 def test_matmul_nan_stays_where_it_is(M, N, K):
     """A NaN row makes its record NaN and no other; a NaN or infinite weight scale its 128 columns."""
     g = torch.Generator().manual_seed(1)
@@ -275,7 +331,7 @@ def test_matmul_nan_stays_where_it_is(M, N, K):
         assert bool(bad[:, 128:256].all()) and int(bad.any(0).sum()) == 128
 
 
-@pytest.mark.parametrize("M", [1, 40, 3000])
+@pytest.mark.parametrize("M", [1, 40, 3000, 20000])
 def test_matmul_scales_far_apart(M):
     """Weight scales over the whole range of fp32, next to each other: no partial sum may overflow."""
     g = torch.Generator().manual_seed(M)
@@ -290,9 +346,34 @@ def test_matmul_scales_far_apart(M):
     assert bool((err <= lim).all())
 
 
+@pytest.mark.parametrize("M", [5, 4000])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_matmul_scale_zero(M, out):
+    """A block whose scale is 0 adds nothing, however large the rows are that meet it; its NaN stay NaN."""
+    g = torch.Generator().manual_seed(M)
+    N, K = 1600, 384
+    x = torch.randn(M, K, generator=g)
+    x[:, 128:256] *= 2.0 ** 110
+    a, as_ = quantise(x.cuda())
+    w, ws = weights(g, 1, N, K, "any")
+    ws[0, :, 1] = 0.0
+    w[0, 70, 130] = 0xFF
+    C = torch.empty((M, N), device="cuda", dtype=out)
+    B.moe_matmul_fp8(a, as_, w[0], ws[0], C)
+    got = C.cpu().double()
+    assert bool(got[:, 70].isnan().all())
+    keep = torch.arange(N) != 70
+    k = torch.cat([torch.arange(128), torch.arange(256, 384)])
+    av, wv = rows64(a, as_)[:, k], weights64(w[0], ws[0])[:, k][keep]
+    want, lim = av @ wv.t(), bound(av, wv, K, out is torch.bfloat16)
+    if out is torch.bfloat16:
+        lim = lim + 2.0 ** -8 * (want.abs() + lim)
+    assert bool(((got[:, keep] - want).abs() <= lim).all())
+
+
 def test_matmul_stored_values_are_exact():
     """Small whole numbers: every sum is exact, in whatever order."""
-    for M, N, K, P in ((1, 64, 128, 1), (33, 320, 448, 4), (2600, 512, 1024, 3)):
+    for M, N, K, P in ((1, 64, 128, 1), (33, 320, 448, 4), (2600, 512, 1024, 3), (2600, 2048, 1024, 3)):
         g = torch.Generator().manual_seed(M)
         x = torch.randint(-8, 9, (M, K), generator=g).float()
         x[:, ::128] = 8.0
@@ -401,13 +482,44 @@ def test_gate_up(M, f, K, P, kind, scale):
     check_gate_up(M, f, K, P, kind, scale, gather=kind != "one")
 
 
-@pytest.mark.parametrize("M", [7, 2048])
+GATE_FEW = [(640, 256, 1088, 8), (300, 192, 4160, 2), (64, 64, 2048, 3), (700, 320, 4160, 16), (9, 2048, 64, 2)]
+GATE_MANY = [(4096, 832, 64, 1), (4500, 1088, 64, 6), (4000, 832, 128, 2), (3000, 832, 192, 3), (3001, 576, 448, 2), (1500, 704, 2112, 1),
+             (1500, 704, 4160, 2), (1600, 512, 704, 40), (2100, 2112, 320, 1)]
+
+
+@pytest.mark.parametrize("M,f,K,P", GATE_FEW + GATE_MANY)
+@pytest.mark.parametrize("kind,scale", [("even", "any"), ("short", "pow2"), ("one", "signs")])
+def test_gate_up_either_way(M, f, K, P, kind, scale):
+    n = B.moe_gate_up_fp8_workspace_bytes(M, f, K, P)
+    assert n == (4 * M * f if (M, f, K, P) in GATE_FEW else 0)
+    check_gate_up(M, f, K, P, kind, scale, gather=kind != "one")
+
+
+def test_gate_up_workspace():
+    """A workspace of the caller's: the bits of a call without; nothing behind it is written."""
+    g = torch.Generator().manual_seed(2)
+    M, f, K = 20, 192, 256
+    a, as_ = quantise(torch.randn(M, K, generator=g).cuda())
+    (wg, sg), (wu, su) = weights(g, 1, f, K, "any"), weights(g, 1, f, K, "any")
+    n, out = B.moe_gate_up_fp8_workspace_bytes(M, f, K), []
+    buf = torch.full((n + 512,), 0xA7, dtype=torch.uint8, device="cuda")
+    for ws in (None, buf[:n]):
+        H = torch.empty((M, f), dtype=torch.uint8, device="cuda")
+        Hs = torch.zeros((M, B.fp8_scale_bytes(f)), dtype=torch.uint8, device="cuda")
+        B.moe_gate_up_fp8(a, as_, wg[0], sg[0], wu[0], su[0], H, Hs, ws=ws)
+        out.append((H, Hs))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1]) and bool((buf[n:] == 0xA7).all())
+    with pytest.raises(B.MoEError):
+        B.moe_gate_up_fp8(a, as_, wg[0], sg[0], wu[0], su[0], H, Hs, ws=buf[:n - 1])
+
+
+@pytest.mark.parametrize("M", [7, 2048, 8000])
 def test_gate_up_far_gates(M):
     """Gates of hundreds: SiLU's tail, where exp(-g) leaves fp32, and its other end."""
     check_gate_up(M, 256, 256, 1, "even", "any", std=300.0)
 
 
-@pytest.mark.parametrize("M", [20, 1500])
+@pytest.mark.parametrize("M", [20, 1500, 12000])
 def test_gate_up_nan(M):
     g = torch.Generator().manual_seed(4)
     f, K = 256, 128
@@ -425,7 +537,7 @@ def test_gate_up_nan(M):
     assert bool((H[3] == 0).all()) and bool((H[:, 128:] == 0).all())
 
 
-@pytest.mark.parametrize("M,P", [(6, 2), (2100, 2)])
+@pytest.mark.parametrize("M,P", [(6, 2), (2100, 2), (12000, 3)])
 def test_streams_and_graphs(M, P):
     """Calls on two streams at once, and captured and replayed on new inputs: the bits of a call alone."""
     g = torch.Generator().manual_seed(M)

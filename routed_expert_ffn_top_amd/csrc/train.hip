@@ -198,6 +198,16 @@ __device__ __forceinline__ void load_experts(const float *L, int E, int lane, fl
         for (int c = 0; c < C; ++c) v[c] = lane + 64 * c < E ? L[lane + 64 * c] : none;
     }
 }
+// exp(x) for x <= 0, within 3 2^-24: 2^y by the instruction (1 unit in the last place) with y = x log2(e)
+// rounded, and what the rounding left, d, by 1 + d ln(2). Below 2^-126 it is 0. NaN stays. 8
+// instructions where expf has 15, and both kernels are bound by how many they issue.
+__device__ __forceinline__ float exp_down(float x)
+{
+    const float log2e = 0x1.715476p+0f, rest = 0x1.4ae0cp-26f;   // log2(e) in two pieces
+    x = x < -120.0f ? -120.0f : x;
+    const float y = x * log2e, d = fmaf(x, rest, fmaf(x, log2e, -y)), p = __builtin_amdgcn_exp2f(y);
+    return fmaf(p, d * 0x1.62e43p-1f, p);
+}
 // Softmax numerators in place, and their sum.
 template <int C>
 __device__ __forceinline__ float numerators(float (&z)[C])
@@ -213,7 +223,7 @@ __device__ __forceinline__ float numerators(float (&z)[C])
     if (m == none) m = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        z[c] = expf(z[c] - m);
+        z[c] = exp_down(z[c] - m);
         s += z[c];
     }
     return wave_sum(s);
@@ -416,19 +426,19 @@ __global__ __launch_bounds__(256) void k_router_backward(RouterBackArgs a)
     float dw = 0.0f;
     if (a.dw && lane < a.k) {
         id = a.idx[t * a.kp + lane];
-        if (id >= a.E) id = -1;
-        if (id >= 0) dw = a.dw[t * a.kp + lane];
+        dw = a.dw[t * a.kp + lane];
+        if ((uint32_t)id >= (uint32_t)a.E) id = -1, dw = 0.0f;
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) u[c] = x[c] = 0.0f;
-    if (a.slope && (!a.mask || a.mask[t] != 0)) {
+    if (a.slope) {   // all loads at once, the mask's too, but that of the sequence before its slope's
+        const int on = a.mask ? a.mask[t] : 1;
+        const float g = a.d_loss ? *a.d_loss : 1.0f;
         const int seq = a.seq_offset ? seq_at(a.seq_offset, a.S, t, lane) : 0;
-        if (seq >= 0 && seq < a.S) {
-            const float g = a.d_loss ? *a.d_loss : 1.0f;
-            load_experts<C, V>(a.slope + (int64_t)seq * a.E, a.E, lane, u, 0.0f);
+        load_experts<C, V>(a.slope + (int64_t)min(max(seq, 0), a.S - 1) * a.E, a.E, lane, u, 0.0f);
+        const bool counts = on != 0 && seq >= 0 && seq < a.S;
 #pragma unroll
-            for (int c = 0; c < C; ++c) u[c] *= g;
-        }
+        for (int c = 0; c < C; ++c) u[c] = counts ? u[c] * g : 0.0f;
     }
     auto id_of = [&](int j) { return __builtin_amdgcn_readlane(id, j); };
     auto of = [&](float v, int j) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), j)); };
@@ -551,7 +561,7 @@ hipError_t launch_balance(const BalanceArgs &a, const BalanceLayout &w, void *ws
 }
 
 // Whether every row of E fp32 values of these arrays can be read C values at a time
-// (65536 rows of 256 backward: 43 us, 46 a value at a time; the forward pass gains nothing by it, 21 and 22).
+// (65536 rows of 256 backward: 3 of 44 us; the forward pass gains nothing by it).
 static bool together(int E, int C, std::initializer_list<const void *> rows)
 {
     bool yes = E % C == 0;

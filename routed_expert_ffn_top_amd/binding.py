@@ -474,17 +474,19 @@ def _fp8_slices(codes, scales, K, name):
     if len(shape) not in (2, 3) or codes.dtype is not torch.uint8 or shape[-1] != K or stride[-1] != 1 or stride[-2] != K:
         raise ValueError(f"{name}: need uint8 codes [P][N][{K}], a slice contiguous")
     N, KB, P = shape[-2], -(-K // 128), shape[0] if len(shape) == 3 else 1
-    want, s_stride = (-(-N // 128), KB), scales.stride()
-    if (scales.dtype is not torch.float32 or tuple(scales.shape) != tuple(shape[:-2]) + want
-            or KB > 1 and s_stride[-1] != 1 or want[0] > 1 and s_stride[-2] != KB):
+    NB, s_stride = -(-N // 128), scales.stride()
+    if (scales.dtype is not torch.float32 or scales.shape != ((P, NB, KB) if len(shape) == 3 else (NB, KB))
+            or KB > 1 and s_stride[-1] != 1 or NB > 1 and s_stride[-2] != KB):
         raise ValueError(f"{name}: need float32 scales [P][ceil(N / 128)][ceil(K / 128)], a slice's contiguous")
     return P, N, stride[0] if P > 1 else N * K, s_stride[0] if P > 1 else 0
 
 
-def _groups(M, P, dev, slot_offset, row_index):
-    for t, n, name in ((slot_offset, P + 1, "slot_offset"), (row_index, M, "row_index")):
-        if t is not None and (t.dtype != torch.int32 or t.numel() < n or not t.is_contiguous() or t.get_device() != dev):
-            raise ValueError(f"{name}: need int32 [{n}]")
+def _list_of(t, n, dev, name):
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: need int32 [{n}]")
+    return t.data_ptr()
 
 
 def _one_device(dev, *tensors):
@@ -505,9 +507,8 @@ def moe_matmul_fp8(A_codes, A_scales, B_codes, B_scales, C, slot_offset=None, ro
     if dtype is None or C.shape[1] != N or step != 1 or ldc < N:
         raise ValueError(f"C must be float32 or bfloat16 [M][{N}] with contiguous rows")
     _one_device(dev, A_codes, A_scales, B_codes, B_scales)
-    _groups(M, P, dev, slot_offset, row_index)
-    _check(load().moe_matmul_fp8(M, N, K, A_codes.data_ptr(), A_scales.data_ptr(), A_rows, _ptr(row_index),
-                                 _ptr(slot_offset), P, B_codes.data_ptr(), B_scales.data_ptr(), b_stride, s_stride,
+    take, offset = _list_of(row_index, M, dev, "row_index"), _list_of(slot_offset, P + 1, dev, "slot_offset")
+    _check(load().moe_matmul_fp8(M, N, K, A_codes.data_ptr(), A_scales.data_ptr(), A_rows, take, offset, P, B_codes.data_ptr(), B_scales.data_ptr(), b_stride, s_stride,
                                  C.data_ptr(), dtype, ldc, _stream_of(C, stream)))
 
 
@@ -529,39 +530,43 @@ def moe_gate_up_fp8(A_codes, A_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales,
     P, _, w_stride, s_stride = gate
     dev = H_codes.get_device()
     _one_device(dev, A_codes, A_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales, H_scales)
-    _groups(M, P, dev, slot_offset, row_index)
-    st, n = _stream_of(H_codes, stream), moe_gate_up_fp8_workspace_bytes(M, f, K, P)
-    if ws is None and n:
-        with on_stream(stream):   # its memory goes back to the pool of the stream that uses it
-            ws = torch.empty(n, dtype=torch.uint8, device=H_codes.device)
+    take, offset = _list_of(row_index, M, dev, "row_index"), _list_of(slot_offset, P + 1, dev, "slot_offset")
+    st, n = _stream_of(H_codes, stream), 0
     if ws is not None:
         _one_device(dev, ws)
-    _check(load().moe_gate_up_fp8(M, f, K, A_codes.data_ptr(), A_scales.data_ptr(), A_rows, _ptr(row_index),
-                                  _ptr(slot_offset), P, Wg_codes.data_ptr(), Wg_scales.data_ptr(), Wu_codes.data_ptr(),
+        n = ws.numel() * ws.element_size()
+    else:
+        n = load().moe_gate_up_fp8_workspace_bytes(M, f, K, P)
+        if n:
+            with on_stream(stream):   # its memory goes back to the pool of the stream that uses it
+                ws = torch.empty(n, dtype=torch.uint8, device=H_codes.device)
+    _check(load().moe_gate_up_fp8(M, f, K, A_codes.data_ptr(), A_scales.data_ptr(), A_rows, take, offset, P, Wg_codes.data_ptr(), Wg_scales.data_ptr(), Wu_codes.data_ptr(),
                                   Wu_scales.data_ptr(), w_stride, s_stride, H_codes.data_ptr(), H_scales.data_ptr(),
-                                  _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0, st))
+                                  _ptr(ws), n, st))
 
 
-def _strided(t, name, cols=None):
+def _strided(t, name, cols):
     """Row stride of a matrix with contiguous rows that do not overlap."""
-    if t.dim() != 2 or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name}: need a matrix" + (f" of {cols} columns" if cols is not None else ""))
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != cols:
+        raise ValueError(f"{name}: need a matrix of {cols} columns")
+    if cols > 1 and stride[1] != 1 or shape[0] > 1 and stride[0] < cols:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap")
-    return row_stride(t)
+    return stride[0] if shape[0] > 1 else (cols + 7) // 8 * 8   # one row: any aligned stride does
 
 
 def _combine_args(C, route_pos, topk_w, Y, name):
     T, d = Y.shape
-    dtype, kp = _VAL_DTYPE.get(C.dtype), topk_w.shape[-1]
+    dtype, kp, dev = _VAL_DTYPE.get(C.dtype), topk_w.shape[-1], Y.get_device()
     if dtype is None or Y.dtype is not torch.float32:
         raise ValueError(f"C must be float32 or bfloat16 and {name} float32")
-    ldc, ldy = _strided(C, "C", d), _strided(Y, name)
-    if topk_w.dtype is not torch.float32 or tuple(topk_w.shape) != (T, kp) or not topk_w.is_contiguous():
+    ldc, ldy = _strided(C, "C", d), _strided(Y, name, d)
+    if topk_w.dtype is not torch.float32 or topk_w.shape != (T, kp) or not topk_w.is_contiguous():
         raise ValueError(f"topk_w: need contiguous float32 [{T}][K']")
     if route_pos.dtype is not torch.int32 or route_pos.numel() != T * kp or not route_pos.is_contiguous():
         raise ValueError(f"route_pos: need contiguous int32 [{T * kp}]")
-    _one_device(Y.get_device(), C, route_pos, topk_w)
+    if C.get_device() != dev or route_pos.get_device() != dev or topk_w.get_device() != dev:
+        raise ValueError("the operands must be on one device")
     return T, d, kp, C.shape[0], C.data_ptr(), dtype, ldc, route_pos.data_ptr(), topk_w.data_ptr(), Y.data_ptr(), ldy
 
 
@@ -577,7 +582,7 @@ def moe_combine_backward(C, route_pos, topk_w, dY, dC, d_topk_w, stream=None):
     if dC is not None:
         if dC.dtype is not C.dtype or dC.shape != C.shape:
             raise ValueError("dC: need C's shape and type")
-        lddc = _strided(dC, "dC")
+        lddc = _strided(dC, "dC", args[1])
         _one_device(dY.get_device(), dC)
     if d_topk_w.dtype is not torch.float32 or d_topk_w.shape != topk_w.shape or not d_topk_w.is_contiguous():
         raise ValueError("d_topk_w: need topk_w's shape, contiguous float32")
@@ -590,9 +595,8 @@ def moe_balance_workspace_bytes(shape: moe_shape, S: int = 1) -> int:
 
 
 def _whole(t, dtype, shape, name, dev):
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: need contiguous {dtype} {list(shape)}")
-    _one_device(dev, t)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: need contiguous {dtype} {list(shape)} on the operands' device")
 
 
 def _sequences(shape, seq_offset, mask, dev):

@@ -664,6 +664,9 @@ moe_status moe_combine_backward(int32_t T, int32_t d, int32_t kp, int32_t M,
  *                slope: without the loss); d_loss device [1] fp32 (NULL: 1)
  *   d_topk_w     device [T][K'] fp32 or NULL; the shared ranks' are not used,
  *                nor those of ids outside [0, E). With it, topk_idx is required
+ * T < 2^26 for this call. A token without a gradient (not counted, and its
+ * d_topk_w 0 or not given) gets 0 whatever its logits hold; otherwise a logit of
+ * +infinity makes NaN of its row here, and of the loss above.
  */
 size_t moe_balance_workspace_bytes(const moe_shape *shape, int32_t S);
 moe_status moe_balance_loss(const moe_shape *shape, const float *logits,

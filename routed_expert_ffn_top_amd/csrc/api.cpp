@@ -1131,6 +1131,8 @@ moe_status moe_router_backward(const moe_shape *shape, const float *logits, cons
     MOE_TRY(check_shape(shape));
     MOE_TRY(check_sequences("router backward", seq_offset, S_));
     if (!slope && !d_topk_w) return fail(MOE_ERR_INVALID_ARG, "router backward: give slope, d_topk_w or both");
+    if (shape->T >= 1 << 26)   // a wave a token, fewer than 2^32 threads a launch
+        return fail(MOE_ERR_UNSUPPORTED, "router backward: T must be below 2^26");
     if (shape->T > 0 && (!logits || !d_logits || (d_topk_w && !topk_idx)))
         return fail(MOE_ERR_INVALID_ARG, "router backward: NULL pointer");
     RouterBackArgs a{};

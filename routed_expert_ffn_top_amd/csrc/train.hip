@@ -71,7 +71,9 @@ __device__ __forceinline__ void store_row(void *C, int64_t at, const float *v)
 constexpr int kRoutes = 8;   // routes whose rows are asked for together
 
 // Y[t] += sum over the token's routes, ascending, of weight times row: one
-// fused multiply-add each, in fp32. Bound by HBM: every row read once.
+// fused multiply-add each, in fp32. The rows of 8 routes are requested together, their
+// positions before them. Bound by HBM: every row read once; 4096 tokens of 8 routes, 2048
+// bf16 columns: 48 us, 4.2 TB/s.
 template <bool BF16, int V>
 __global__ __launch_bounds__(256) void k_combine_rows(CombineArgs a, int blocks_x)
 {
@@ -109,7 +111,8 @@ __global__ __launch_bounds__(256) void k_combine_rows(CombineArgs a, int blocks_
 }
 
 // A workgroup a token: dC[pos] = w dY[t], dw = <dY[t], C[pos]>, the sums over a
-// thread's columns ascending, then over the lanes and the waves in a fixed order.
+// thread's columns ascending, then over the lanes and the waves in a fixed order. dY is read
+// once for 8 routes. Bound by HBM: rows read and written once; the same sizes 66 us, 4.6 TB/s.
 template <bool BF16, int V>
 __global__ __launch_bounds__(256) void k_combine_rows_backward(CombineArgs a)
 {
@@ -174,6 +177,11 @@ __global__ __launch_bounds__(256) void k_combine_rows_backward(CombineArgs a)
 // the entries of a sequence, 32 experts at a time, in fp64; the last of those
 // workgroups sums the loss. Every sum is in a fixed order. Entry b + s is chunk b's of
 // sequence s: that is in ascending order of both, and every entry is written.
+//
+// Bound by instructions issued, not by the logits read (67 MB, 13 us): 65536 tokens of 256
+// experts in 16 sequences 20.5 us and 9.8 for the second step, 16 tokens of 8 experts 3.6 and 4.3, all
+// latency. A chunk of 64 tokens there leaves 1024 workgroups; of 16, the sums over the chunks
+// take longer than the chunks.
 
 // C experts a lane: with V, C lane + c, read and written together (rows of whole 4 C bytes), else lane + 64 c.
 template <int C, bool V>
@@ -413,7 +421,9 @@ __global__ __launch_bounds__(1024) void k_balance_sequences(BalanceArgs a, int c
 // dL = p (u - sum u p) with u = d_loss slope (counted tokens) and, for route
 // weights that are not renormalised, their gradients; renormalised ones, a
 // softmax over the chosen, add w (dw - sum w dw). A wave a token; lane j holds route j's
-// id and gradient, which pass to the others through scalar registers.
+// id and gradient, which pass to the others through scalar registers. Bound by instructions
+// issued: 65536 tokens of 256 experts, 8 routes, 41 us (its 136 MB take 27); two tokens a wave with
+// their loads together 43.6, four 46.6.
 template <int C, bool V>
 __global__ __launch_bounds__(256) void k_router_backward(RouterBackArgs a)
 {

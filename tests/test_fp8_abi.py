@@ -120,6 +120,11 @@ def test_balance_refusals():
     assert back(shape=none, L_=None, idx=None, out=None) == B.MOE_OK
 
 
+def test_router_backward_refuses_more_tokens_than_a_launch_has_waves():
+    shape = B.make_shape(1 << 26, 64, 64, 1, 1)
+    assert L.moe_router_backward(ctypes.byref(shape), 0x1000, 0x2000, 0x3000, None, None, 1, None, None, 0x4000, None) == UN
+
+
 def u8(*s):
     return torch.zeros(s, dtype=torch.uint8)
 

@@ -49,7 +49,8 @@ struct BalanceLayout {
     int ch, chunks, V;
 };
 // Tokens a chunk: what a workgroup sums, 4 waves of its tokens each, at most 64 a wave.
-// 1024 chunks and more fill the GPU; the sums over them follow. A chunk has an entry for each
+// 1024 chunks and more fill the GPU, more than that lengthen the sums over them (65536
+// tokens of 256 experts: 1024 chunks 30 us for both steps, 4096 40, 256 48). A chunk has an entry for each
 // sequence that it meets, one of them the one behind the last: V at most.
 inline BalanceLayout balance_layout(int64_t T, int E, int S)
 {

@@ -152,7 +152,8 @@ __global__ __launch_bounds__(256) void k_quantize_blocks(const void *__restrict_
 
 // 8 values a lane: code value times scale in fp32, rounded once more to bf16
 // (exact in both for scales that are powers of two, unless the result leaves the
-// normal numbers). Bound by HBM: 65536 x 2048 to bf16 73 us, 5.5 TB/s.
+// normal numbers). Bound by HBM: 65536 x 2048 to bf16 59.5 us, 6.8 TB/s; 75.5 with stores that
+// go through the caches, where nothing reads the values again before they leave them.
 template <bool BF16, bool ROWS>
 __global__ __launch_bounds__(256) void k_dequantize(const uint8_t *__restrict__ codes, const void *__restrict__ scales,
                                                     int64_t n8, int K8, int64_t lds, void *__restrict__ dst, int64_t ld)
@@ -178,10 +179,10 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint8_t *__restrict__ 
         u32x4_t o;
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[c] = bf16_pair(v[2 * c], v[2 * c + 1]);
-        *(u32x4_t *)((uint16_t *)dst + at) = o;
+        __builtin_nontemporal_store(o, (u32x4_t *)((uint16_t *)dst + at));
     } else {
-        *(f32x4_t *)((float *)dst + at) = f32x4_t{v[0], v[1], v[2], v[3]};
-        *(f32x4_t *)((float *)dst + at + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+        __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (f32x4_t *)((float *)dst + at));
+        __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, (f32x4_t *)((float *)dst + at + 4));
     }
 }
 

@@ -60,11 +60,12 @@ template <bool BF16, int V>
 __device__ __forceinline__ void store_row(void *C, int64_t at, const float *v)
 {
     if constexpr (!BF16) {
-        *(f32x4_t *)((float *)C + at) = f32x4_t{v[0], v[1], v[2], v[3]};
+        __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (f32x4_t *)((float *)C + at));
     } else if constexpr (V == 8) {
-        *(u32x4_t *)((uint16_t *)C + at) = u32x4_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+        __builtin_nontemporal_store(u32x4_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])},
+                                    (u32x4_t *)((uint16_t *)C + at));
     } else {
-        *(u32x2_t *)((uint16_t *)C + at) = u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+        __builtin_nontemporal_store(u32x2_t{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}, (u32x2_t *)((uint16_t *)C + at));
     }
 }
 
@@ -73,7 +74,7 @@ constexpr int kRoutes = 8;   // routes whose rows are asked for together
 // Y[t] += sum over the token's routes, ascending, of weight times row: one
 // fused multiply-add each, in fp32. The rows of 8 routes are requested together, their
 // positions before them. Bound by HBM: every row read once; 4096 tokens of 8 routes, 2048
-// bf16 columns: 48 us, 4.2 TB/s.
+// bf16 columns: 41 us, 4.9 TB/s.
 template <bool BF16, int V>
 __global__ __launch_bounds__(256) void k_combine_rows(CombineArgs a, int blocks_x)
 {
@@ -112,7 +113,9 @@ __global__ __launch_bounds__(256) void k_combine_rows(CombineArgs a, int blocks_
 
 // A workgroup a token: dC[pos] = w dY[t], dw = <dY[t], C[pos]>, the sums over a
 // thread's columns ascending, then over the lanes and the waves in a fixed order. dY is read
-// once for 8 routes. Bound by HBM: rows read and written once; the same sizes 66 us, 4.6 TB/s.
+// once for 8 routes. Bound by HBM: rows read and written once; the same sizes 64 us behind the forward
+// pass on the same rows, 4.7 TB/s, 74 alone. Stores past the caches: 8 us less for both passes, 5 for
+// this one alone; loads past them gain 5 forward and cost 12 here, whose rows may still be there.
 template <bool BF16, int V>
 __global__ __launch_bounds__(256) void k_combine_rows_backward(CombineArgs a)
 {
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(256) void k_combine_rows_backward(CombineArgs a)
 // sequence s: that is in ascending order of both, and every entry is written.
 //
 // Bound by instructions issued, not by the logits read (67 MB, 13 us): 65536 tokens of 256
-// experts in 16 sequences 20.5 us and 9.8 for the second step, 16 tokens of 8 experts 3.6 and 4.3, all
+// experts in 16 sequences 18.5 us and 9.8 for the second step, 16 tokens of 8 experts 3.6 and 4.3, all
 // latency. Chunks of 16, 64, 256 tokens there: 22.6 + 17.9, 20.5 + 9.8, 41.0 + 7.4.
 
 // C experts a lane: with V, C lane + c, read and written together (rows of whole 4 C bytes), else lane + 64 c.
@@ -421,8 +424,8 @@ __global__ __launch_bounds__(1024) void k_balance_sequences(BalanceArgs a, int c
 // weights that are not renormalised, their gradients; renormalised ones, a
 // softmax over the chosen, add w (dw - sum w dw). A wave a token; lane j holds route j's
 // id and gradient, which pass to the others through scalar registers. Bound by instructions
-// issued: 65536 tokens of 256 experts, 8 routes, 41 us (its 136 MB take 27); two tokens a wave with
-// their loads together 43.6, four 46.6.
+// issued: 65536 tokens of 256 experts, 8 routes, 37 us (its 136 MB take 27), 41 with stores through the
+// caches; then two tokens a wave with their loads together 43.6, four 46.6.
 template <int C, bool V>
 __global__ __launch_bounds__(256) void k_router_backward(RouterBackArgs a)
 {
@@ -505,11 +508,11 @@ __global__ __launch_bounds__(256) void k_router_backward(RouterBackArgs a)
         typename Row<C>::type w;
 #pragma unroll
         for (int c = 0; c < C; ++c) w[c] = fmaf(z[c], u[c] - dot, x[c]);
-        if (lane * C < a.E) *(typename Row<C>::type *)(out + lane * C) = w;
+        if (lane * C < a.E) __builtin_nontemporal_store(w, (typename Row<C>::type *)(out + lane * C));
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (lane + 64 * c < a.E) out[lane + 64 * c] = fmaf(z[c], u[c] - dot, x[c]);
+            if (lane + 64 * c < a.E) __builtin_nontemporal_store(fmaf(z[c], u[c] - dot, x[c]), out + lane + 64 * c);
     }
 }
 

@@ -524,8 +524,8 @@ def moe_gate_up_fp8(A_codes, A_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales,
     call one of its own, on its stream."""
     A_rows, K = _fp8_rows(A_codes, A_scales, "A")
     M, f = _fp8_rows(H_codes, H_scales, "H")
-    gate, up = _fp8_slices(Wg_codes, Wg_scales, K, "Wg"), _fp8_slices(Wu_codes, Wu_scales, K, "Wu")
-    if gate != up or gate[1] != f:
+    gate = _fp8_slices(Wg_codes, Wg_scales, K, "Wg")
+    if gate[1] != f or gate != _fp8_slices(Wu_codes, Wu_scales, K, "Wu"):
         raise ValueError(f"Wg and Wu need the same shapes and strides, {f} rows a slice")
     P, _, w_stride, s_stride = gate
     dev = H_codes.get_device()
@@ -537,9 +537,11 @@ def moe_gate_up_fp8(A_codes, A_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales,
         n = ws.numel() * ws.element_size()
     else:
         n = load().moe_gate_up_fp8_workspace_bytes(M, f, K, P)
-        if n:
+        if n and stream is None:
+            ws = H_codes.new_empty(n)
+        elif n:
             with on_stream(stream):   # its memory goes back to the pool of the stream that uses it
-                ws = torch.empty(n, dtype=torch.uint8, device=H_codes.device)
+                ws = H_codes.new_empty(n)
     _check(load().moe_gate_up_fp8(M, f, K, A_codes.data_ptr(), A_scales.data_ptr(), A_rows, take, offset, P, Wg_codes.data_ptr(), Wg_scales.data_ptr(), Wu_codes.data_ptr(),
                                   Wu_scales.data_ptr(), w_stride, s_stride, H_codes.data_ptr(), H_scales.data_ptr(),
                                   _ptr(ws), n, st))

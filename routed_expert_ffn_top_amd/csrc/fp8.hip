@@ -163,7 +163,7 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint8_t *__restrict__ 
     const uint32_t row = (uint32_t)i / (uint32_t)K8;
     const int k = (int)((uint32_t)i - row * (uint32_t)K8) * 8;
     const u32x2_t q = *(const u32x2_t *)(codes + i * 8);
-    const float s = ROWS ? block_value(((const uint8_t *)scales)[row * lds + k / kFp8Block])
+    const float s = ROWS ? exponent_value(((const uint8_t *)scales)[row * lds + k / kFp8Block])
                          : ((const float *)scales)[(row / kFp8Block) * lds + k / kFp8Block];
     float v[8];
 #pragma unroll

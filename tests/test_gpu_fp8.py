@@ -167,6 +167,20 @@ def test_dequantise_any_scale():
         assert torch.equal(out.cpu().isnan(), want.isnan()) and torch.equal(out.cpu().nan_to_num(1.0), want.nan_to_num(1.0)), s
 
 
+def test_dequantize_any_byte():
+    """Every scale byte, those too that the quantiser never writes (0: 2^-127; from 248 on products may leave fp32)."""
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).repeat(128, 1).reshape(256, 128).cuda()
+    scales = torch.full((256, 16), 0xEE, dtype=torch.uint8)
+    scales[:, 0] = torch.arange(256, dtype=torch.int32).to(torch.uint8)
+    for half in range(2):   # each byte meets every code
+        c = codes.roll(half, 0)
+        out = torch.empty((256, 128), device="cuda")
+        B.moe_dequantize_fp8(c, scales.cuda(), out)
+        want = (decode(c) * unit64(scales[:, :1])).float()
+        got = out.cpu()
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(1.0), want.nan_to_num(1.0))
+
+
 def weights(g, P, N, K, kind):
     """Codes [P][N][K] and scales: powers of two, or any."""
     codes = torch.randint(0, 256, (P, N, K), generator=g, dtype=torch.int32)

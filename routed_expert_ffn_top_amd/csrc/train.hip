@@ -182,7 +182,7 @@ __global__ __launch_bounds__(256) void k_combine_rows_backward(CombineArgs a)
 // sequence s: that is in ascending order of both, and every entry is written.
 //
 // Bound by instructions issued, not by the logits read (67 MB, 13 us): 65536 tokens of 256
-// experts in 16 sequences 18.5 us and 9.8 for the second step, 16 tokens of 8 experts 3.6 and 4.3, all
+// experts in 16 sequences 18.1 us and 8.5 for the second step, 16 tokens of 8 experts 3.6 and 4.3, all
 // latency. Chunks of 16, 64, 256 tokens there: 22.6 + 17.9, 20.5 + 9.8, 41.0 + 7.4.
 
 // C experts a lane: with V, C lane + c, read and written together (rows of whole 4 C bytes), else lane + 64 c.
@@ -407,8 +407,10 @@ __global__ __launch_bounds__(1024) void k_balance_sequences(BalanceArgs a, int c
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) loss += __shfl_xor(loss, o, 64);
         if (tid == 0) {
+            // past the L2, as the reads below: once it has arrived there (a release would write the L2 back)
             __hip_atomic_store(&part[seq * gridDim.y + blockIdx.y], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)blocks - 1;
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)blocks - 1;
         }
     }
     __syncthreads();

@@ -243,7 +243,7 @@ __device__ __forceinline__ i32x8_t codes32(const uint8_t *p, bool half)
     return i32x8_t{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
-// 32 codes times scale (a power of two) as four operands of 8 bf16.
+// 32 codes times scale (a power of two) as four operands of 8 bf16; exact with scale 1.
 __device__ __forceinline__ void decode32(const i32x8_t &q, float scale, bf16x8_t (&v)[4])
 {
 #pragma unroll
@@ -259,16 +259,27 @@ __device__ __forceinline__ void decode32(const i32x8_t &q, float scale, bf16x8_t
         }
     }
 }
-// acc += sb times the product of 128 k (16 x 16).
-__device__ __forceinline__ void step128(f32x4_t &acc, const bf16x8_t (&A)[4], const i32x8_t &q, float sb)
+// acc += the product of 128 k (16 weight rows x 16 records) times the row's scale, a power of two, and
+// the block's. The codes are multiplied as they are, so that nothing leaves fp32 before the scales are there:
+// of the two, one at or above 1 and one below are joined first, others follow each other, and each
+// time what lies between is no further from 1 than the result or one of them.
+struct Factors {
+    float p, q;
+};
+__device__ __forceinline__ Factors factors(float row, float block)
 {
-    bf16x8_t Bv[4];
-    decode32(q, 1.0f, Bv);
+    const bool join = (row >= 1.0f) != (fabsf(block) >= 1.0f);
+    return {join ? 1.0f : row, join ? row * block : block};
+}
+__device__ __forceinline__ void step128(f32x4_t &acc, const i32x8_t &w, const bf16x8_t (&A)[4], Factors s)
+{
+    bf16x8_t W[4];
+    decode32(w, 1.0f, W);
     f32x4_t part = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[i], Bv[i], part, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(W[i], A[i], part, 0, 0, 0);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] = fmaf(part[r], sb, acc[r]);
+    for (int r = 0; r < 4; ++r) acc[r] = fmaf(part[r] * s.p, s.q, acc[r]);
 }
 
 __device__ __forceinline__ float swiglu(float g, float u) { return g < kSiluTail ? silu_tail_mul(g, u) : silu_mul(g, u); }
@@ -287,7 +298,7 @@ __device__ __forceinline__ float swiglu(float g, float u) { return g < kSiluTail
 // (offsets, row index, codes, and the join) with a launch.
 enum { EPI_STORE = 0, EPI_GATE_UP = 1 };
 template <int EPI, int NT, int W>
-__global__ __launch_bounds__(64 * W) void k_few(Fp8Args a, float *__restrict__ hw)
+__global__ __launch_bounds__(64 * W, NT == 4 ? 2 : NT == 2 ? 3 : 4) void k_few(Fp8Args a, float *__restrict__ hw)
 {
     constexpr int U = 4, G = EPI == EPI_GATE_UP ? 2 : 1, COLS = 16 * NT / G;
     __shared__ f32x4_t s_sum[W][NT][64];
@@ -301,13 +312,14 @@ __global__ __launch_bounds__(64 * W) void k_few(Fp8Args a, float *__restrict__ h
     const uint8_t *ap = a.A + (int64_t)rec * K + (lane >> 4) * 16;
     const uint8_t *as = a.As + rec * fp8_scale_bytes(K);
     const uint8_t *bp[NT];
-    const float *bs[NT];
+    const float *bs[G];   // the workgroup's columns lie within a block
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const int c = n0 + 16 * (j / G), n = min(c + (lane & 15), a.N - 1);
+        const int n = min(n0 + 16 * (j / G) + (lane & 15), a.N - 1);
         bp[j] = a.B[j % G] + slot * a.B_stride + (int64_t)n * K + (lane >> 4) * 16;
-        bs[j] = a.Bs[j % G] + slot * a.Bs_stride + (int64_t)(min(c, a.N - 1) / kFp8Block) * KB;
     }
+#pragma unroll
+    for (int g = 0; g < G; ++g) bs[g] = a.Bs[g] + slot * a.Bs_stride + (int64_t)(n0 / kFp8Block) * KB;
     f32x4_t acc[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -315,16 +327,15 @@ __global__ __launch_bounds__(64 * W) void k_few(Fp8Args a, float *__restrict__ h
         constexpr int n = decltype(u_t)::value;
         i32x8_t A[n], Bv[n][NT];
         int sa[n];
-        float sb[n][NT];
+        float sb[n][G];
 #pragma unroll
         for (int u = 0; u < n; ++u) {
             const int kb = k0 + u * W;
             const bool half = (kb + 1) * kFp8Block > K;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                Bv[u][j] = codes32(bp[j] + (int64_t)kb * kFp8Block, half);
-                sb[u][j] = bs[j][kb];
-            }
+            for (int j = 0; j < NT; ++j) Bv[u][j] = codes32(bp[j] + (int64_t)kb * kFp8Block, half);
+#pragma unroll
+            for (int g = 0; g < G; ++g) sb[u][g] = bs[g][kb];
             A[u] = codes32(ap + (int64_t)kb * kFp8Block, half);
             sa[u] = as[kb];
         }
@@ -335,9 +346,12 @@ __global__ __launch_bounds__(64 * W) void k_few(Fp8Args a, float *__restrict__ h
 #pragma unroll
                 for (int i = 4; i < 8; ++i) A[u][i] = 0;
             bf16x8_t Av[4];
-            decode32(A[u], block_value(sa[u]), Av);
+            decode32(A[u], 1.0f, Av);
+            Factors s[G];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) step128(acc[j], Av, Bv[u][j], sb[u][j]);
+            for (int g = 0; g < G; ++g) s[g] = factors(exponent_value(sa[u]), sb[u][g]);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) step128(acc[j], Bv[u][j], Av, s[j % G]);
         }
     };
     int k0 = wave;
@@ -362,21 +376,20 @@ __global__ __launch_bounds__(64 * W) void k_few(Fp8Args a, float *__restrict__ h
                     if (c == q) s[g] = acc[c * G + g];
             }
         }
-        const int n = n0 + 16 * q + (lane & 15);
-        if (n >= a.N) continue;
+        // register r: column 4 (lane / 16) + r of record lane % 16
+        const int n = n0 + 16 * q + 4 * (lane >> 4), m = lane & 15;
+        if (n >= a.N || m >= cnt) continue;
+        if constexpr (EPI == EPI_GATE_UP) {
+            f32x4_t h;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int m = 4 * (lane >> 4) + r;
-            if (m >= cnt) continue;
-            if constexpr (EPI == EPI_GATE_UP) {
-                hw[(int64_t)(row0 + m) * a.N + n] = swiglu(s[0][r], s[G - 1][r]);
-            } else {
-                const int64_t at = (int64_t)(row0 + m) * a.ldc + n;
-                if (a.c_bf16)
-                    ((uint16_t *)a.C)[at] = (uint16_t)bf16_pair(s[0][r], 0.0f);
-                else
-                    ((float *)a.C)[at] = s[0][r];
-            }
+            for (int r = 0; r < 4; ++r) h[r] = swiglu(s[0][r], s[G - 1][r]);
+            *(f32x4_t *)(hw + (int64_t)(row0 + m) * a.N + n) = h;
+        } else {
+            const int64_t at = (int64_t)(row0 + m) * a.ldc + n;
+            if (a.c_bf16)
+                *(u32x2_t *)((uint16_t *)a.C + at) = u32x2_t{bf16_pair(s[0][0], s[0][1]), bf16_pair(s[0][2], s[0][3])};
+            else
+                *(f32x4_t *)((float *)a.C + at) = s[0];
         }
     }
 }

@@ -560,7 +560,9 @@ moe_status moe_dequantize_fp8(const void *codes, const void *scales,
  * as 0. Rows and offsets out of range are brought into it on the device.
  * C in bf16 of many records a slot (and H below) is multiplied on the fp8 matrix
  * instructions, which keep 14 bits of the products of 8 neighbouring k: 1.1e-5 of
- * the norm of C for normally distributed operands. fp32 C keeps 24 bits.
+ * the norm of C for normally distributed operands. fp32 C keeps 24 bits; values of A
+ * below 2^-126 count to within 2^-133 there. A's scale bytes are those that
+ * moe_quantize_fp8 writes, 1 to 247 and 255; others make numbers of no meaning.
  * MOE_ERR_UNSUPPORTED from (M / 256 + P + 1) * (N / 64) = 2^30 and for A_rows * K
  * above 2^36.
  */

@@ -406,10 +406,10 @@ __global__ __launch_bounds__(64 * W, NT == 4 ? 2 : NT == 2 ? 3 : 4) void k_few(F
 // each of the tile's two blocks of 128 weight rows.
 //
 // The records' scales, powers of two, are operands of the matrix instruction. So
-// are the powers of two of the weights' scales m 2^e, 1 <= |m| < 2; the m are
+// are the powers of two of the weights' scales m 2^e; the m are
 // brought in by holding the sums in units of the current one: before the first
-// multiply of a block of k the sums are multiplied by m_last / m, at most 2 in
-// magnitude, so nothing overflows on the way, and at the end by the last m. Where
+// multiply of a block of k the sums are multiplied by m_last / m, and at the end by the last m. |m| >= 1,
+// so that sums in units of it are no larger than the sums, and nothing overflows on the way. Where
 // the weights' scales are powers of two there is nothing to multiply.
 //
 // Bound by the matrix instructions and the LDS reads that feed them: a stage of 128 k takes 1.1
@@ -431,15 +431,27 @@ __global__ __launch_bounds__(64 * W, NT == 4 ? 2 : NT == 2 ? 3 : 4) void k_few(F
 constexpr int kXcd = 8;
 constexpr int kStream = 2;   // buffer stores of C, which is not read here: non-temporal
 
-// A weight scale as m and the bits of 2^e; NaN and infinity as NaN. What is below 2^-126 in
-// magnitude, which e cannot hold, counts as 0: its block's codes do, those of NaN aside.
+// A weight scale as m 2^e, e in -126 .. 118, m of magnitude 1 up to 2, from 2^119 on up to 2^10; NaN and
+// infinity as NaN. What is below 2^-126 in magnitude, which e cannot hold, counts as 0: its block's
+// codes do, those of NaN aside.
+constexpr int kMaxField = 118 + 127;
 __device__ __forceinline__ float scale_m(float s)
 {
     const uint32_t u = __float_as_uint(s);
-    const uint32_t e = u & 0x7f800000u;
-    return __uint_as_float(e == 0 || e == 0x7f800000u ? (u & 0x80000000u) | 0x3f800000u : (u & 0x807fffffu) | 0x3f800000u);
+    const int e = (int)((u >> 23) & 255u);
+    return __uint_as_float(e == 0 || e == 255 ? (u & 0x80000000u) | 0x3f800000u
+                                              : (u & 0x807fffffu) | (uint32_t)(127 + max(e - kMaxField, 0)) << 23);
 }
-__device__ __forceinline__ int scale_e(float s) { return (int)((__float_as_uint(s) >> 23) & 255u); }
+__device__ __forceinline__ int scale_e(float s)
+{
+    const int e = (int)((__float_as_uint(s) >> 23) & 255u);
+    return e == 255 ? 255 : min(e, kMaxField);
+}
+// Codes decoded to bf16 (DEC) carry their scales: a record's halved, the weights' 2^e doubled, so that
+// neither side's largest code, 448, leaves bf16 (2^119 448 < 2^128), for row bytes up to 247. A row's byte 1 to 3
+// takes small codes below bf16's smallest number, 2^-133.
+__device__ __forceinline__ float decoded_row(int byte) { return exponent_value(byte == 255 ? 255 : max(byte - 1, 0)); }
+__device__ __forceinline__ float decoded_weight(int e) { return exponent_value(e == 255 ? 255 : e + 1); }
 
 __device__ __forceinline__ void opaque(f32x16_t &v) { asm volatile("" : "+v"(v)); }
 
@@ -726,7 +738,7 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
         const bool scales = h == 0 ? !last : last;
         if constexpr (DEC) {
             bf16x8_t Av[4];
-            decode32(af[cur], block_value(sa[i]), Av);
+            decode32(af[cur], decoded_row(sa[i]), Av);
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
 #pragma unroll
@@ -759,7 +771,7 @@ __global__ __launch_bounds__(512) void k_ring(Fp8Args a)
         constexpr int n = decltype(mi)::value;
         if constexpr (DEC)
 #pragma unroll
-            for (int j = 0; j < NI; ++j) decode32(bf[decltype(half_t)::value][j], exponent_value(se[j]), Bv[j]);
+            for (int j = 0; j < NI; ++j) decode32(bf[decltype(half_t)::value][j], decoded_weight(se[j]), Bv[j]);
         step(half_t, std::integral_constant<int, 0>(), kb, false);
         step(half_t, std::integral_constant<int, 1>(), kb, n == 2);
         if constexpr (n == 4) {

@@ -1,0 +1,72 @@
+"""fp8 products of whole numbers, to the last bit: sums that are exact in whatever order and on either kind of matrix
+instruction. Rows hold -8 .. 8, weights -4 .. 4, so that of 8 neighbouring products the smallest, 1, lies 5 binary
+places below the largest, 32, where the fp8 instructions cut 13 below it; block scales are 3/8 times 1, 2 or 4, a
+factor that every sum has. Sums stay below 2^24 of their smallest unit: 32 x 2112 x 4 x 3 < 2^20."""
+import pytest
+import torch
+
+from routed_expert_ffn_top_amd import binding as B
+from test_gpu_fp8 import FEW, GATE_FEW, GATE_MANY, MANY, decode, quantise, sizes, spread, unit64
+
+pytestmark = pytest.mark.gpu
+
+
+def rows(g, M, K):
+    x = torch.randint(-8, 9, (M, K), generator=g).float()
+    x[:, ::128] = 8.0
+    return x
+
+
+def slices(g, P, N, K):
+    """Codes and scales on the GPU, their values in 64 bits."""
+    v = torch.randint(-4, 5, (P, N, K), generator=g).float()
+    s = 2.0 ** torch.randint(0, 3, (P, -(-N // 128), -(-K // 128)), generator=g) * 0.375
+    d = torch.stack([v[p].double() * spread(s[p].double(), 128, N, K) for p in range(P)])
+    return v.cuda().to(torch.float8_e4m3fn).view(torch.uint8), s.cuda(), d
+
+
+SHAPES = [(5, 192, 448, 2), (130, 128, 2048, 1)] + [s for s in FEW + MANY if s[0] <= 4500 and s[2] <= 2112 and s[3] <= 40]
+
+
+@pytest.mark.parametrize("M,N,K,P", SHAPES)
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_products_of_whole_numbers(M, N, K, P, out):
+    g = torch.Generator().manual_seed(M + N + K)
+    x = rows(g, M, K)
+    a, as_ = quantise(x.cuda())
+    w, ws, d = slices(g, P, N, K)
+    off = sizes(g, M, P, "even")
+    C = torch.empty((M, N), device="cuda", dtype=out)
+    B.moe_matmul_fp8(a, as_, w, ws, C, slot_offset=off.int().cuda())
+    got = C.cpu()
+    for p in range(P):
+        r = slice(int(off[p]), int(off[p + 1]))
+        assert torch.equal(got[r], (x[r].double() @ d[p].t()).float().to(out)), f"slot {p}"
+
+
+GATE = [(5, 192, 448, 2)] + [s for s in GATE_FEW + GATE_MANY if s[2] <= 2112 and s[3] <= 40]
+
+
+@pytest.mark.parametrize("M,f,K,P", GATE)
+def test_hidden_of_whole_numbers(M, f, K, P):
+    """g and u are exact, so that H = SiLU(g) u is off by (|g| + 8) 2^-22 of its value and by half a step of its
+    code: 2^-4 of the value, or 2^-10 of the scale where the step is the smallest."""
+    g = torch.Generator().manual_seed(M + f + K)
+    x = rows(g, M, K)
+    a, as_ = quantise(x.cuda())
+    (wg, sg, dg), (wu, su, du) = slices(g, P, f, K), slices(g, P, f, K)
+    off = sizes(g, M, P, "even")
+    H = torch.empty((M, f), dtype=torch.uint8, device="cuda")
+    Hs = torch.zeros((M, B.fp8_scale_bytes(f)), dtype=torch.uint8, device="cuda")
+    # gates of a few units: 2^-8 of the sums, which lie near 2^9
+    B.moe_gate_up_fp8(a, as_, wg, sg * 2.0 ** -8, wu, su, H, Hs, slot_offset=off.int().cuda())
+    unit = spread(unit64(Hs.cpu()[:, :-(-f // 128)]), 1, M, f)
+    got = decode(H) * unit
+    for p in range(P):
+        r = slice(int(off[p]), int(off[p + 1]))
+        gate, up = x[r].double() @ dg[p].t() * 2.0 ** -8, x[r].double() @ du[p].t()
+        h = gate * torch.sigmoid(gate) * up
+        err = (gate.abs() + 8) * 2.0 ** -22 * h.abs()
+        lim = err + torch.maximum(2.0 ** -4 * (h.abs() + err), 2.0 ** -10 * unit[r])
+        off_by = (got[r] - h).abs()
+        assert bool((off_by <= lim).all()), f"slot {p}: {float((off_by / lim).max()):.3g} of the bound"

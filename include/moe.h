@@ -558,11 +558,15 @@ moe_status moe_dequantize_fp8(const void *codes, const void *scales,
  * A weight's scale may be any fp32 number; a NaN makes NaN of what it meets, an
  * infinity NaN or infinity, and one below 2^-126 in magnitude counts as itself or
  * as 0. Rows and offsets out of range are brought into it on the device.
- * C in bf16 of many records a slot (and H below) is multiplied on the fp8 matrix
- * instructions, which keep 14 bits of the products of 8 neighbouring k: 1.1e-5 of
- * the norm of C for normally distributed operands. fp32 C keeps 24 bits; values of A
- * below 2^-126 count to within 2^-133 there. A's scale bytes are those that
- * moe_quantize_fp8 writes, 1 to 247 and 255; others make numbers of no meaning.
+ * How C is summed goes by M, N, K, P and c_dtype alone, not by what the operands
+ * hold: a call of other sizes may give a record other roundings. fp32 C, and all of
+ * few records a slot, keeps 24 bits. C in bf16 (and H below) of many records a
+ * slot, M / P, is multiplied on the fp8 matrix instructions, which keep 14 bits of
+ * the products of 8 neighbouring k: within 2^-10 of sum_k |a b|, 1.1e-5 of the norm
+ * of C for normally distributed operands. fp32 C asks for 24 bits in any case.
+ * In fp32 C values of A below 2^-126 count to within 2^-133. A's scale bytes are
+ * those that moe_quantize_fp8 writes, 1 to 247 and 255; others make numbers of no
+ * meaning.
  * MOE_ERR_UNSUPPORTED from (M / 256 + P + 1) * (N / 64) = 2^30 and for A_rows * K
  * above 2^36.
  */
@@ -588,7 +592,10 @@ moe_status moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void *A_codes,
  *                do) where many records a slot make one kernel of it, else 4 M f
  * The other arguments and the limits are those of moe_matmul_fp8, which takes
  * H for the down projection. SiLU(g) * u is within (|g| + 8) 2^-22 of its
- * value for the g and u of the fp32 sums, relative.
+ * value for the g and u of the fp32 sums, relative. Sums that are off as C's in
+ * bf16 are move a value that lies near the middle between two codes to the other
+ * one (0.16 % of them for normally distributed operands); for H of sums of 24 bits
+ * take g and u as fp32 C of moe_matmul_fp8 and quantise SiLU(g) * u.
  */
 size_t moe_gate_up_fp8_workspace_bytes(int32_t M, int32_t f, int32_t K,
                                        int32_t P);

@@ -191,10 +191,13 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint8_t *__restrict__ 
 //  - the fp8 matrix instructions, at twice the rate of bf16. They align the
 //    products of 8 neighbouring k and cut what lies more than 13 bits below the
 //    largest one's exponent (measured with one large and one small product at
-//    every distance; across the groups of 8 sums keep 24 bits): 1.1e-5 of the
-//    norm of C for normally distributed operands, whatever K. That is a 350th of a
-//    rounding to bf16 and less yet of one to 8 bits, so C in bf16 and H of many
-//    records go this way.
+//    every distance, the same in all of their shapes; across the groups of 8 sums keep 24 bits): 1.1e-5
+//    of the norm of C for normally distributed operands, whatever K, and at most 2^-10 of sum |a b|. C in bf16
+//    and H of many records go this way. bf16 C: 1.655e-3 from the 64-bit result with the cut and without (32768 x
+//    2048 x 1408). H: 0.16 % of its codes come out a step away, where h lies that near the middle
+//    between two codes; either is as far from h (2.65e-2 of H's norm as before), but they differ from what
+//    sums of 24 bits give: an expert FFN of 4096 tokens on 64 experts is 1.99e-3 from the 64-bit
+//    one, with 24 bits 1.68e-3. On decoded codes gate/up of that FFN takes 309 us instead of 187.
 //  - codes decoded to bf16, which is exact, on the bf16 instructions, whose sums
 //    keep 24 bits (2e-8): fp32 C, and few records a slot, where the time goes into
 //    reading the weights and the decoding is free.

@@ -275,7 +275,8 @@ __global__ __launch_bounds__(256) void k_balance_chunks(BalanceArgs a, int ch, i
     int s0 = 0, s1 = 0;
     if (a.seq_offset) {
         s0 = b == 0 ? 0 : max(seq_at(a.seq_offset, a.S, t0, lane), 0);
-        s1 = max(seq_at(a.seq_offset, a.S, t1, lane), s0);
+        // the last chunk's go on to the end, also where offsets lie behind it: no entry keeps what was there
+        s1 = b == (int)gridDim.x - 1 ? a.S : max(seq_at(a.seq_offset, a.S, t1, lane), s0);
     }
     auto range = [&](int s, int *lo, int *hi) {
         *lo = *hi = 0;

@@ -661,8 +661,10 @@ moe_status moe_combine_backward(int32_t T, int32_t d, int32_t kp, int32_t M,
  *   mask         device [T] bytes, 0: the token is not counted; or NULL
  *   loss         device [1] fp32; counts device [S][E] int32 (c_se); prob device
  *                [S][E] fp32 (P_se)
- *   slope        device [S][E] fp32: d loss / d p_te of a counted token less its
- *                mean over the experts, which a softmax's gradient drops
+ *   slope        device [S][E] fp32: d loss / d p_te of a counted token with
+ *                c_se - k n_s / E in c_se's place (a softmax's gradient drops what
+ *                all experts have alike); where no id of its routes lies outside
+ *                [0, E) that is less its mean over the experts
  *   ws           at least moe_balance_workspace_bytes(shape, S) bytes, 256-byte
  *                aligned, of any contents; one call at a time
  * The sums are in a fixed order, so results are bitwise run-to-run identical.

@@ -173,7 +173,7 @@ __global__ __launch_bounds__(256) void k_combine_rows_backward(CombineArgs a)
 // loss = the mean of loss_s over the sequences that have tokens. Its gradient
 // with respect to p_te is E / (k n^2 S+) c_e; a softmax's backward drops what
 // all experts have in common, so what is kept for it is the same with c_e less
-// its mean, which the differences there do not lose in rounding.
+// k n / E, its mean if every route counts, which the differences there do not lose in rounding.
 //
 // Three steps: chunks of w.ch tokens, a workgroup each, which writes an entry for each
 // sequence that it meets (sums of at most w.ch / 4 terms a wave in fp32, then 4 waves);

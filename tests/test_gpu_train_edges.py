@@ -31,3 +31,28 @@ def test_offsets_past_the_tokens(T):
         clean.fill_(0xEE)
         got, want = balance(shape, L, idx, far, ws), balance(shape, L, idx, [min(o, T) for o in far], clean)
         assert all(torch.equal(x, y) for x, y in zip(got, want)), far
+
+
+def test_slope_with_ids_out_of_range():
+    """slope = E / (k n^2 S+) (c - k n / E) whether or not every route counts, one rounding to fp32 off; and its
+    gradient is that of the loss, from which a constant over the experts drops out."""
+    T, E, k = 60, 10, 3
+    g = torch.Generator().manual_seed(2)
+    L, idx = torch.randn(T, E, generator=g), torch.randint(-4, E + 4, (T, k), generator=g).int()
+    shape = B.make_shape(T, 64, 64, E, k)
+    loss, counts, prob, slope = balance(shape, L.cuda(), idx.cuda(), [0, T], B.alloc_balance_workspace(shape, 1))
+    c = torch.bincount(idx[(idx >= 0) & (idx < E)].long(), minlength=E).double()
+    assert torch.equal(counts.cpu()[0].double(), c) and float(c.sum()) < k * T
+    want = E / (k * T * T) * (c - k * T / E)
+    assert bool(((slope.cpu()[0].double() - want).abs() <= 1.01 * 2.0 ** -24 * want.abs()).all())
+    assert abs(float((slope.cpu()[0].double() + 1 / T).mean()) - E / (k * T * T) * float(c.mean())) <= 2.0 ** -23 / T
+    # the gradient of the loss as it is defined: p (u - sum u p) with u = E / (k n^2) c
+    out = torch.empty((T, E), device="cuda")
+    B.moe_router_backward(shape, L.cuda(), idx.cuda(), out, slope=slope)
+    p, u = torch.softmax(L.double(), -1), E / (k * T * T) * c
+    R = float(L.max() - L.min())
+    shifted = (slope.cpu()[0].double().abs()).expand(T, E)
+    lim = (2 * (R + 18) + 16) * 2.0 ** -24 * p * (shifted + (shifted * p).sum(-1, keepdim=True))
+    grad = p * (u - (u * p).sum(-1, keepdim=True))
+    # 2^-50: this formula's own differences, of numbers below 1, in 64 bits
+    assert bool(((out.cpu().double() - grad).abs() <= lim + 2.0 ** -24 * grad.abs() + 2.0 ** -50).all())

@@ -567,8 +567,8 @@ moe_status moe_dequantize_fp8(const void *codes, const void *scales,
  * In fp32 C values of A below 2^-126 count to within 2^-133. A's scale bytes are
  * those that moe_quantize_fp8 writes, 1 to 247 and 255; others make numbers of no
  * meaning.
- * MOE_ERR_UNSUPPORTED from (M / 256 + P + 1) * (N / 64) = 2^30 and for A_rows * K
- * above 2^36.
+ * MOE_ERR_UNSUPPORTED from (M / 256 + P + 1) * (N / 64) = 2^30, for A_rows * K
+ * above 2^36 and for M above 2^31 - 256.
  */
 moe_status moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void *A_codes,
                           const void *A_scales, int32_t A_rows,

@@ -894,6 +894,8 @@ moe_status check_fp8_product(const char *what, int32_t M, int32_t N, int32_t K, 
     if (!aligned(A, 16) || !aligned(As, 16)) return fail(MOE_ERR_INVALID_ARG, "%s: A and its scales must be 16-byte aligned", what);
     if (P > 1 && (B_stride < (int64_t)N * K || B_stride % 16 != 0 || Bs_stride < fp8_blocks(N) * fp8_blocks(K)))
         return fail(MOE_ERR_INVALID_ARG, "%s: the strides must hold a slice, that of the codes in whole 16 bytes", what);
+    // a slot's records are rounded up to whole tiles in 32 bits
+    if (M > INT32_MAX - 255) return fail(MOE_ERR_UNSUPPORTED, "%s: M above 2^31 - 256", what);
     // tiles are counted in 32 bits, a row of A is addressed in 16 bytes and 32 bits
     if (((int64_t)M / 256 + P + 1) * (N / 64) >= (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "%s: too many tiles", what);
     if ((int64_t)A_rows * K > (int64_t)1 << 36) return fail(MOE_ERR_UNSUPPORTED, "%s: A above 64 GiB", what);
@@ -973,7 +975,7 @@ moe_status moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void *A_codes, 
 
 size_t moe_gate_up_fp8_workspace_bytes(int32_t M, int32_t f, int32_t K, int32_t P)
 {
-    if (M <= 0 || f <= 0 || K <= 0 || P < 1) return 0;
+    if (M <= 0 || M > INT32_MAX - 255 || f <= 0 || K <= 0 || P < 1) return 0;
     Fp8Args a{};
     a.M = M;
     a.N = f;

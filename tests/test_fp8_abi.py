@@ -184,3 +184,12 @@ def test_binding_refuses_other_rows_and_routings():
     # host tensors
     with pytest.raises(ValueError):
         B.moe_router_backward(s, **ok)
+
+
+def test_products_refuse_more_records_than_tiles_are_counted_of():
+    """A slot's records are rounded up to whole tiles of 256 in 32 bits."""
+    for M in (2 ** 31 - 1, 2 ** 31 - 255):
+        p = (M, 64, 64, 0x1000, 0x2000, 1, 0x10, None, 1)
+        assert L.moe_matmul_fp8(*p, 0x4000, 0x5000, 0, 0, 0x8000, B.MOE_DT_BF16, 64, None) == UN
+        assert L.moe_gate_up_fp8(*p, 0x4000, 0x5000, 0x6000, 0x7000, 0, 0, 0x8000, 0x9000, 0xa0000, 1 << 40, None) == UN
+        assert B.moe_gate_up_fp8_workspace_bytes(M, 64, 64) == 0

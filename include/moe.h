@@ -512,7 +512,8 @@ moe_status moe_matmul_mxfp4(int32_t M, int32_t N, int32_t K,
  *     whose linear weights come with an inverse scale for each 128 x 128)
  *   values   device [rows][ld] of val_dtype (MOE_DT_F32 or MOE_DT_BF16), K of
  *            each row used, K a multiple of 64, rows >= 0, ld >= K; the pointer
- *            and the row stride 16-byte aligned; at most 2^33 values a call
+ *            and the row stride 16-byte aligned; at most 2^33 values a call, and
+ *            to quantise fewer than 2^24 blocks of 128 x 128
  *   codes    device [rows][K], 16-byte aligned
  * moe_quantize_fp8: a block's scale is the least power of two in 2^-126 ..
  * 2^120 with max |value| <= 448 scale; each value over it, which is exact, is

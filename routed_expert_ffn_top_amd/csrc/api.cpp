@@ -866,7 +866,7 @@ moe_status check_fp8_values(const char *what, const void *v, int32_t dt, int64_t
         return fail(MOE_ERR_INVALID_ARG, "%s: block_rows must be 1 or 128", what);
     if (rows < 0 || K <= 0 || ld < K) return fail(MOE_ERR_INVALID_ARG, "%s: bad sizes", what);
     if (K % 64 != 0) return fail(MOE_ERR_UNSUPPORTED, "%s: K must be a multiple of 64", what);
-    // at most 2^32 - 1 threads a launch: 16 for each block of a row, 256 for each of a matrix
+    // at most 2^32 - 1 threads a launch: 16 for each block of a row, one for 8 values read back
     if (rows > ((int64_t)1 << 33) / K) return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^33 values", what);
     if (rows > 0 && (!v || !codes || !scales)) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer", what);
     const int esz = dt == MOE_DT_F32 ? 4 : 2;
@@ -929,6 +929,9 @@ moe_status moe_quantize_fp8(const void *values, int32_t val_dtype, int64_t rows,
                             int32_t block_rows, void *codes, void *scales, moe_stream stream)
 {
     MOE_TRY(check_fp8_values("quantize", values, val_dtype, rows, K, ld, block_rows, codes, scales));
+    // 256 for each block of a matrix: up to 128 rows of 2^31 - 64 have 2^24
+    if (block_rows == kFp8Block && fp8_blocks(rows) * fp8_blocks(K) >= 1 << 24)
+        return fail(MOE_ERR_UNSUPPORTED, "quantize: 2^24 blocks of 128 x 128 or more");
     HIP_TRY(launch_quantize_fp8(values, val_dtype == MOE_DT_BF16, rows, K, ld, block_rows, (uint8_t *)codes, scales,
                                 S(stream)),
             "quantize launch");

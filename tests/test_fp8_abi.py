@@ -193,3 +193,10 @@ def test_products_refuse_more_records_than_tiles_are_counted_of():
         assert L.moe_matmul_fp8(*p, 0x4000, 0x5000, 0, 0, 0x8000, B.MOE_DT_BF16, 64, None) == UN
         assert L.moe_gate_up_fp8(*p, 0x4000, 0x5000, 0x6000, 0x7000, 0, 0, 0x8000, 0x9000, 0xa0000, 1 << 40, None) == UN
         assert B.moe_gate_up_fp8_workspace_bytes(M, 64, 64) == 0
+
+
+def test_quantise_refuses_more_blocks_than_a_launch_has_threads():
+    """256 threads a block of 128 x 128, fewer than 2^32 a launch."""
+    K = 2 ** 31 - 64
+    for rows in (1, 4):
+        assert L.moe_quantize_fp8(0x1000, B.MOE_DT_BF16, rows, K, K, 128, 0x2000, 0x3000, None) == UN

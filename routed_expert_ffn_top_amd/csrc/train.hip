@@ -408,16 +408,15 @@ __global__ __launch_bounds__(1024) void k_balance_sequences(BalanceArgs a, int c
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) loss += __shfl_xor(loss, o, 64);
         if (tid == 0) {
-            // past the L2, as the reads below: once it has arrived there (a release would write the L2 back)
-            __hip_atomic_store(&part[seq * gridDim.y + blockIdx.y], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)blocks - 1;
+            part[seq * gridDim.y + blockIdx.y] = loss;
+            // release: its part is there before it arrives; acquire: the last one to arrive sees all of them
+            s_last = __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)blocks - 1;
         }
     }
     __syncthreads();
     if (!s_last || tid >= 64) return;
     loss = 0.0;
-    for (int i = tid; i < blocks; i += 64) loss += __hip_atomic_load(&part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = tid; i < blocks; i += 64) loss += part[i];
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) loss += __shfl_xor(loss, o, 64);
     if (tid == 0) *a.loss = (float)loss;

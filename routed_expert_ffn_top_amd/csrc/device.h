@@ -21,6 +21,20 @@ __device__ __forceinline__ int wave_incl_scan(int v, int lane)
     return v;
 }
 
+// Of a grouped product's arguments: slot s holds the records [lo, hi), brought into [0, M), and
+// record rec takes row row_of of A.
+template <class Args>
+__device__ __forceinline__ void slot_range(const Args &a, int s, int *lo, int *hi)
+{
+    *lo = a.slot_offset ? min(max(a.slot_offset[s], 0), a.M) : 0;
+    *hi = a.slot_offset ? min(max(a.slot_offset[s + 1], *lo), a.M) : a.M;
+}
+template <class Args>
+__device__ __forceinline__ int row_of(const Args &a, int rec)
+{
+    return min(max(a.row_index ? a.row_index[rec] : rec, 0), a.A_rows - 1);
+}
+
 // Two floats rounded to bf16 (nearest even), lo in bits 15:0.
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {
@@ -29,7 +43,6 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 }
 
 #define LDS_AS __attribute__((address_space(3)))
-#define GLOBAL_AS __attribute__((address_space(1)))
 
 // s_waitcnt with only the vector-memory counter constrained (gfx9 encoding:
 // vmcnt[3:0] | expcnt[6:4] | lgkmcnt[11:8] | vmcnt[5:4] at bits 15:14).

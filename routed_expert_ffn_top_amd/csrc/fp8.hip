@@ -204,16 +204,6 @@ __global__ __launch_bounds__(256) void k_dequantize(const uint8_t *__restrict__ 
 // Which of a block's 128 k values a lane supplies in which place is free, as
 // long as it is the same for both operands: they have one scale.
 
-// Slot s holds the records [lo, hi), brought into [0, M).
-__device__ __forceinline__ void slot_range(const Fp8Args &a, int s, int *lo, int *hi)
-{
-    *lo = a.slot_offset ? min(max(a.slot_offset[s], 0), a.M) : 0;
-    *hi = a.slot_offset ? min(max(a.slot_offset[s + 1], *lo), a.M) : a.M;
-}
-__device__ __forceinline__ int row_of(const Fp8Args &a, int rec)
-{
-    return min(max(a.row_index ? a.row_index[rec] : rec, 0), a.A_rows - 1);
-}
 // Row tile `tile` of R records: its slot (-1: there is none), first record and
 // records. Every wave finds it for itself.
 template <int R>
@@ -396,7 +386,6 @@ __global__ __launch_bounds__(64 * W, NT == 4 ? 2 : NT == 2 ? 3 : 4) void k_few(F
         }
     }
 }
-
 
 // ---------------------------------------------------------------------------
 // Many records a slot: a persistent kernel. Tile 256 records x 256 weight rows,

@@ -16,7 +16,6 @@
 namespace moe {
 namespace {
 
-
 // Scale byte of a block from the bits of its largest magnitude, and the factor
 // 2^(127 - byte) that its values are quantised with (1 for a NaN block).
 __device__ __forceinline__ uint32_t block_scale(uint32_t top)
@@ -145,17 +144,6 @@ __device__ __forceinline__ uint32_t bf16_bits(float x)
 // Every element of C is one chain of these instructions in ascending k, in
 // both kernels below, so a record's bits hang neither on the size of its group
 // nor on which kernel runs.
-
-// Slot s holds the records [lo, hi), brought into [0, M).
-__device__ __forceinline__ void slot_range(const MxArgs &a, int s, int *lo, int *hi)
-{
-    *lo = a.slot_offset ? min(max(a.slot_offset[s], 0), a.M) : 0;
-    *hi = a.slot_offset ? min(max(a.slot_offset[s + 1], *lo), a.M) : a.M;
-}
-__device__ __forceinline__ int row_of(const MxArgs &a, int rec)
-{
-    return min(max(a.row_index ? a.row_index[rec] : rec, 0), a.A_rows - 1);
-}
 
 // Few records a slot: 64 records x 64 columns per workgroup, 32 x 32 per wave,
 // operands straight from global memory, 8 steps of 64 k requested at a time.

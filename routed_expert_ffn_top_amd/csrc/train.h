@@ -29,7 +29,7 @@ constexpr int kMaxSeq = 4096;    // sequences of a balance call
 constexpr int kMaxChunk = 256;   // tokens of a chunk of it, 64 a wave
 
 struct BalanceArgs {
-    int T, E, k, kp, renorm;
+    int T, E, k, kp;
     const float *logits;         // [T][E]
     const int32_t *idx;          // [T][kp]
     const int32_t *seq_offset;   // [S+1] or null (S == 1: every token)

@@ -49,13 +49,15 @@ struct BalanceLayout {
     int ch, chunks, V;
 };
 // Tokens a chunk: what a workgroup sums, 4 waves of its tokens each, at most 64 a wave.
-// 1024 chunks and more fill the GPU, more than that lengthen the sums over them (65536
-// tokens of 256 experts: 1024 chunks 30 us for both steps, 4096 40, 256 48). A chunk has an entry for each
+// Up to 16384 tokens 16, whose chunks are done soonest; then 64, and as many more as keep 1024 chunks, which
+// fill the GPU, where more of them lengthen the sums over them. Both steps on 256 experts: 16384 tokens 21.1 us
+// with 16, 16385 20.2 with 64 and 21.2 with 20; 65537 30.5 with 68, 41.6 with 256; 131072
+// 45.8 with 128, 54.5 with 256. A chunk has an entry for each
 // sequence that it meets, one of them the one behind the last: V at most.
 inline BalanceLayout balance_layout(int64_t T, int E, int S)
 {
     BalanceLayout w{};
-    w.ch = T <= 16384 ? 16 : T <= 65536 ? 64 : kMaxChunk;
+    w.ch = T <= 16384 ? 16 : (int)std::min<int64_t>(std::max<int64_t>((T + 4095) / 4096 * 4, 64), kMaxChunk);
     w.chunks = (int)std::max<int64_t>((T + w.ch - 1) / w.ch, 1);
     w.V = w.chunks + S;
     size_t o = 0;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from routed_expert_ffn_top_amd import binding as B
-from test_gpu_train import choice
+from test_gpu_train import check_balance, choice
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,10 @@ def test_slope_with_ids_out_of_range():
     grad = p * (u - (u * p).sum(-1, keepdim=True))
     # 2^-50: this formula's own differences, of numbers below 1, in 64 bits
     assert bool(((out.cpu().double() - grad).abs() <= lim + 2.0 ** -24 * grad.abs() + 2.0 ** -50).all())
+
+
+@pytest.mark.parametrize("T", [16385, 40001, 131073, 262145, 300001])
+def test_chunks_of_every_length(T):
+    """Chunks of 64 tokens and, past 65536, of more in steps of 4 up to 256."""
+    off = torch.tensor([0, 7, T // 3, T // 3 + 1, T])
+    check_balance(T, 5, 2, 0, 4, off, (torch.rand(T, generator=torch.Generator().manual_seed(T)) < 0.7).to(torch.uint8), True, True)

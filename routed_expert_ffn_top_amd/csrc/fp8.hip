@@ -1019,15 +1019,14 @@ hipError_t launch_dequantize_fp8(const uint8_t *codes, const void *scales, int64
 // at most this many row tiles of R records: one partial tile per slot with records
 static int64_t row_tiles(const Fp8Args &a, int R) { return (int64_t)(a.M + R - 1) / R + std::min(a.P, a.M) - 1; }
 
-// Whether the persistent kernel is ahead, by what the two take (us; the rates are
-// those of single calls at sizes from 8 records of 2048 x 2048 to 16384 of 64 slices):
-// the few-records kernel 4 and 0.16 for each million of weights that a tile of 16
+// Whether the persistent kernel is ahead, by what the two take (us; fitted to calls at sizes from 8 records
+// of 2048 x 2048 to 16384 of 64 slices): the few-records kernel 4 and 0.16 for each million of weights that a tile of 16
 // records meets, the persistent one a round of tiles of 5 and a time for each
-// stage, by whether a slot has more than 128 records (1.7, fp32 C 2.9) or not (0.85, 1.4). 64
-// slices of 2048 x 1024: 8 records each 27 against 29 us, 16 38 against 30, 64 100
-// against 36; one of 8192 x 2048: 64 records 14 against 22, 128 23 and 23, 256 42 against
-// 34; one of 1024 x 4096, where 4 tiles of the persistent kernel are all there are: 1024
-// records 45 against 60. Only the device knows the slots' records, the rule goes by the mean.
+// stage, by whether a slot has more than 128 records (1.7, fp32 C 2.9) or not (0.85, 1.4). On
+// weights that no cache holds (few, persistent): 64 slices of 2048 x 1024, 8 records each 31 and 36 us, 16 42 and
+// 37, 64 97 and 42; one of 8192 x 2048, 64 records 15 and 28, 128 26 and 30 (the rule takes the
+// second there), 256 45 and 38; one of 1024 x 4096, where 4 tiles of the persistent kernel are all there are, 1024
+// records 46 and 61. Only the device knows the slots' records, the rule goes by the mean.
 static bool ring_pays(const Fp8Args &a, int sides, bool f32)
 {
     const int64_t slots = std::min(a.P, a.M), rows = a.M / slots, cols = sides == 2 ? 128 : 256;
@@ -1046,13 +1045,14 @@ static hipError_t launch_ring(const Fp8Args &a, hipStream_t st)
     return hipGetLastError();
 }
 
-// Weight rows a workgroup, 16 nt: 64 where that leaves 256 workgroups (64 records of 8
-// slices of 4096 x 14336: 77 us, 83 with 32 and 92 with 16), else 32, for one product only from 192 of
-// them on (one record of 7168 x 2048: 5.3 and 5.7 us), else 16 (4096 x 4096: 6.4, with 32 7.7).
-// Waves: as many as find a batch of 4 steps each (64 slices of 2048 x 512, 16 records: 6.1 us
-// with 1 and 13.6 with 4; of 2048 x 1024, 128 records: 22 with 2, 39 with 4), 8 only
-// where workgroups are few (one record of 2048 x 7168: 7.8, with 4 8.6; 64 of 8 slices
-// of 4096 x 14336 92 and 78).
+// Weight rows a workgroup, 16 nt: 64 where that leaves 256 workgroups, else 32, for one product only from 192 of
+// them on, else 16. Waves: 4; 1 where there is one step of K; 8 from 16 steps on where workgroups are fewer than 512.
+// Measured in a graph of calls on 5 to 24 sets of weights in turn, which no cache holds together (us, rows x waves,
+// the rule's first): 64 records of 8 slices of 4096 x 14336 64 x 4 93.6, 64 x 8 95.1, 32 x 4 98.5, 16 x 4 108; one record
+// of 7168 x 2048 32 x 8 5.9, 32 x 4 6.8, 16 x 8 6.1, 64 x 8 7.5, of 4096 x 4096 16 x 8 7.3, 16 x 4 8.6, 32 x 8 9.2, of 2048 x
+// 7168 16 x 8 8.9, 16 x 4 10.3; 64 slices of 2048 x 1024, 8 records 64 x 4 6.2, 64 x 1 8.5, 64 x 8 6.3, 128 64 x 4 27.1, 64 x
+// 2 29.7, 64 x 8 32.7; 16 of 2048 x 512 64 x 4 6.2, 64 x 1 7.5. Between 32 and 64 rows there is no clear border: 32 x
+// 4 takes 27.2 of the 128 records, 155 where gate/up of 32 records of 8 slices of 14336 x 4096 takes 169 with 64 x 4.
 template <int EPI>
 static hipError_t launch_few(const Fp8Args &a, float *hw, hipStream_t st)
 {
@@ -1060,7 +1060,7 @@ static hipError_t launch_few(const Fp8Args &a, float *hw, hipStream_t st)
     const int64_t tiles = row_tiles(a, 16), KB = fp8_blocks(a.K);
     auto groups = [&](int nt) { return tiles * ((a.N + 16 * nt / G - 1) / (16 * nt / G)); };
     const int nt = groups(4) >= 256 ? 4 : groups(2) >= 192 || G == 2 ? 2 : 1;
-    const int w = KB < 8 ? 1 : KB < 16 ? 2 : KB < 32 || groups(nt) >= 512 ? 4 : 8;
+    const int w = KB == 1 ? 1 : KB < 16 || groups(nt) >= 512 ? 4 : 8;
     auto go = [&](auto nt_t, auto w_t) {
         constexpr int NT = decltype(nt_t)::value, W = decltype(w_t)::value;
         if constexpr (NT >= G)
@@ -1068,7 +1068,6 @@ static hipError_t launch_few(const Fp8Args &a, float *hw, hipStream_t st)
     };
     auto with = [&](auto nt_t) {
         if (w == 1) go(nt_t, std::integral_constant<int, 1>());
-        else if (w == 2) go(nt_t, std::integral_constant<int, 2>());
         else if (w == 4) go(nt_t, std::integral_constant<int, 4>());
         else go(nt_t, std::integral_constant<int, 8>());
     };

@@ -25,7 +25,7 @@ def slices(g, P, N, K):
     return v.cuda().to(torch.float8_e4m3fn).view(torch.uint8), s.cuda(), d
 
 
-SHAPES = [(5, 192, 448, 2), (130, 128, 2048, 1)] + [s for s in FEW + MANY if s[0] <= 4500 and s[2] <= 2112 and s[3] <= 40]
+SHAPES = [(5, 192, 448, 2), (130, 128, 2048, 1), (20, 3200, 320, 1)] + [s for s in FEW + MANY if s[0] <= 4500 and s[2] <= 2112 and s[3] <= 40]
 
 
 @pytest.mark.parametrize("M,N,K,P", SHAPES)
@@ -44,7 +44,7 @@ def test_products_of_whole_numbers(M, N, K, P, out):
         assert torch.equal(got[r], (x[r].double() @ d[p].t()).float().to(out)), f"slot {p}"
 
 
-GATE = [(5, 192, 448, 2)] + [s for s in GATE_FEW + GATE_MANY if s[2] <= 2112 and s[3] <= 40]
+GATE = [(5, 192, 448, 2), (200, 640, 128, 2), (60, 1408, 2048, 4)] + [s for s in GATE_FEW + GATE_MANY if s[2] <= 2112 and s[3] <= 40]
 
 
 @pytest.mark.parametrize("M,f,K,P", GATE)

@@ -537,8 +537,7 @@ moe_status moe_dequantize_fp8(const void *codes, const void *scales,
  * Product of quantised rows and fp8 weights, one weight slice per group of
  * rows, as the expert projections are grouped by the route map:
  *   C[p][n] = sum_k A[row(p)][k] * B_s[n][k]   for the records p of slot s,
- * both sides as they are stored (scaled matrix instructions), fp32 sums, C
- * rounded once.
+ * both sides as they are stored, fp32 sums, C rounded once.
  *   M            records, rows of C; M >= 0
  *   N, K         multiples of 64, K <= MOE_FP8_MAX_K
  *   A_codes, A_scales   device [A_rows][K] and [A_rows][MOE_FP8_SCALE_BYTES(K)],

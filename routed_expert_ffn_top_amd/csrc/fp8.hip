@@ -101,8 +101,8 @@ __device__ __forceinline__ uint32_t max_over(uint32_t v)
 // Rows: 16 lanes a block, 8 values a lane; a row's last block may be 64 wide.
 // One pass: the maximum goes over 16 lanes while the values stay in registers. 8 values a
 // lane make whole 16-byte loads of bf16 and let one row of 2048 fill 4 waves (1.7 us, all of
-// it latency). Bound by HBM: 4 or 2 bytes read and 1 written a value; 32768 x 1408 bf16 28.6
-// us, 4.8 TB/s, a large copy 5.0.
+// it latency). Bound by HBM: 4 or 2 bytes read and 1 written a value; 32768 x 1408 bf16 26.6
+// us, 5.2 TB/s, a large copy 5.0 to 5.2.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_quantize_rows(const void *__restrict__ src, int64_t blocks, int KB, int K,
                                                        int64_t ld, int64_t lds, uint8_t *__restrict__ codes,
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256) void k_quantize_rows(const void *__restrict__ 
 // Weights: a workgroup a block, which it holds in registers, 8 rows of 8 values
 // a thread: 16 lanes read a row's 128 values, so that the loads are whole lines and all 8 (of
 // bf16; 16 of fp32) are in flight before the maximum is taken. Bound by HBM: 65536 x 2048
-// fp32 133 us, 5.0 TB/s, as a large copy.
+// fp32 118 us, 5.7 TB/s; a large copy reaches 5.0 to 5.2.
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_quantize_blocks(const void *__restrict__ src, int64_t rows, int KB, int K,
                                                          int64_t ld, uint8_t *__restrict__ codes,
@@ -152,7 +152,8 @@ __global__ __launch_bounds__(256) void k_quantize_blocks(const void *__restrict_
 
 // 8 values a lane: code value times scale in fp32, rounded once more to bf16
 // (exact in both for scales that are powers of two, unless the result leaves the
-// normal numbers). Bound by HBM: 65536 x 2048 to bf16 59.5 us, 6.8 TB/s; 75.5 with stores that
+// normal numbers). Bound by HBM: 65536 x 2048 to bf16 behind the quantisation, whose 134 MB of codes the
+// last-level cache still holds in part, 69 us; over and over on the same codes 59.5, and 75.5 with stores that
 // go through the caches, where nothing reads the values again before they leave them.
 template <bool BF16, bool ROWS>
 __global__ __launch_bounds__(256) void k_dequantize(const uint8_t *__restrict__ codes, const void *__restrict__ scales,
@@ -286,8 +287,8 @@ __device__ __forceinline__ float swiglu(float g, float u) { return g < kSiluTail
 // and one alone reads 50 GB/s at most (one record of 2048 x 2048: 20 us).
 // Weights pass through registers, each read once and by one wave: nothing would be shared in
 // LDS. 16 rows of an instruction are the least the matrix units take, so that up to 16 records
-// of a slot cost what one does. 64 records of 8 slices of 4096 x 14336: 93 us, 5.05 TB/s of
-// weights; one token's 8 slices of 2048 x 1024: 7.9 us, 2.1 TB/s, five trips to memory in a row
+// of a slot cost what one does. 64 records of 8 slices of 4096 x 14336: 94 us, 5.0 TB/s of
+// weights; one token's 8 slices of 2048 x 1024: 6.2 us, 2.7 TB/s, five trips to memory in a row
 // (offsets, row index, codes, and the join) with a launch.
 enum { EPI_STORE = 0, EPI_GATE_UP = 1 };
 template <int EPI, int NT, int W>
@@ -393,8 +394,8 @@ __global__ __launch_bounds__(64 * W, NT == 4 ? 2 : NT == 2 ? 3 : 4) void k_few(F
 // straight into LDS (16 bytes a lane), one stage in use and one on its way; 8 waves as
 // 2 x 4. Wave row wm takes the 32-record blocks wm, wm + 2, ..., so that a tile with
 // fewer records takes less time (2 or 4 blocks a wave). Rows are stored with their
-// 16-byte chunk c at c ^ ((row >> 1) & 7), which keeps the fragment reads free of
-// bank conflicts. The scales come in panels of 2048 k: 16 bytes a record, 16 numbers for
+// 16-byte chunk c at c ^ ((row >> 1) & 7), which spreads the 16 rows that a fragment read takes
+// at a time over all banks. The scales come in panels of 2048 k: 16 bytes a record, 16 numbers for
 // each of the tile's two blocks of 128 weight rows.
 //
 // The records' scales, powers of two, are operands of the matrix instruction. So
@@ -404,12 +405,15 @@ __global__ __launch_bounds__(64 * W, NT == 4 ? 2 : NT == 2 ? 3 : 4) void k_few(F
 // so that sums in units of it are no larger than the sums, and nothing overflows on the way. Where
 // the weights' scales are powers of two there is nothing to multiply.
 //
-// Bound by the matrix instructions and the LDS reads that feed them: a stage of 128 k takes 1.1
-// us multiplied from registers alone, its fragments 192 KB of LDS reads (0.65 us), its copies
-// 64 KB; together 1.7 to 1.9. One slice 8192 x 8192 x 8192 in bf16: 2.2 to 2.3 PFLOP/s, 2.37
-// with scales that are powers of two (fp32 C, decoded: half the instruction rate). Gate/up of
-// 4096 tokens on 64 slices of 2 x 1024 x 2048 184 us, down 107, 32768 records of 66 slices of 2048 x 1408
-// 143, in fp32 238. Two stages of 128 k and not four of 64: half of the barriers, whole lines
+// Bound by how little of it overlaps. Multiplied from registers alone a stage of 128 k takes 1.1 us; it takes
+// 1.7 to 1.9. Counted (gate/up and down of 4096 tokens on 64 experts, one slice of 8192 x 8192 x 8192): the matrix
+// units are busy 39, 33 and 50 % of the time, LDS 22, 18 and 25 % (of which bank conflicts are a fifth),
+// waves sit at a wait or barrier 38, 41 and 35 %; with a multiply of 64 cycles come about 18, 19 and 14 vector
+// instructions of 4, 8 of them for the change of units: a SIMD issues these for as long as it multiplies, and only its
+// two waves can do the one beside the other.
+// 8192 x 8192 x 8192 in bf16: 533 us, 2.1 PFLOP/s, with scales that are powers of two 471, 2.3. Gate/up of
+// 4096 tokens on 64 slices of 2 x 1024 x 2048 182 to 190 us, down 110, 32768 records of 66 slices of 2048 x 1408
+// 139, in fp32, decoded, at half of the instruction rate, 226. Two stages of 128 k and not four of 64: half of the barriers, whole lines
 // of memory. Without gain: lines of later stages requested into the L2 ahead, other wave
 // priorities, copies left out where a tile has no rows (gate/up -2 %, down +3 %), tiles of more than
 // 128 records before the others (gate/up -2 %, down +7 %: small tiles, bound by their copies, all

@@ -113,8 +113,8 @@ __global__ __launch_bounds__(256) void k_combine_rows(CombineArgs a, int blocks_
 
 // A workgroup a token: dC[pos] = w dY[t], dw = <dY[t], C[pos]>, the sums over a
 // thread's columns ascending, then over the lanes and the waves in a fixed order. dY is read
-// once for 8 routes. Bound by HBM: rows read and written once; the same sizes 64 us behind the forward
-// pass on the same rows, 4.7 TB/s, 74 alone. Stores past the caches: 8 us less for both passes, 5 for
+// once for 8 routes. Bound by HBM: rows read and written once; the same sizes 63 us behind the forward
+// pass on the same rows, 4.8 TB/s, 74 alone. Stores past the caches: 8 us less for both passes, 5 for
 // this one alone; loads past them gain 5 forward and cost 12 here, whose rows may still be there.
 template <bool BF16, int V>
 __global__ __launch_bounds__(256) void k_combine_rows_backward(CombineArgs a)
@@ -181,9 +181,11 @@ __global__ __launch_bounds__(256) void k_combine_rows_backward(CombineArgs a)
 // workgroups sums the loss. Every sum is in a fixed order. Entry b + s is chunk b's of
 // sequence s: that is in ascending order of both, and every entry is written.
 //
-// Bound by instructions issued, not by the logits read (67 MB, 13 us): 65536 tokens of 256
-// experts in 16 sequences 18.1 us and 8.5 for the second step, 16 tokens of 8 experts 3.6 and 4.3, all
-// latency. Chunks of 16, 64, 256 tokens there: 22.6 + 17.9, 20.5 + 9.8, 41.0 + 7.4.
+// Bound by instructions issued more than by the logits read (67 MB, 13 us): 65536 tokens of 256
+// experts in 16 sequences, a fifth of them masked, 17.4 us (134 vector instructions a counted token, two thirds of the
+// time) and 10.6 for the second step, trips to memory in a row; of 64 or of 8 experts 12.5 and 8, a token takes a wave
+// whatever E; 16 tokens of 8 experts 3.5 and 4.0, all latency. Before the second step's last part took its acquire
+// and release, chunks of 16, 64, 256 tokens on 256 experts: 22.6 + 17.9, 20.5 + 9.8, 41.0 + 7.4.
 
 // C experts a lane: with V, C lane + c, read and written together (rows of whole 4 C bytes), else lane + 64 c.
 template <int C, bool V>
@@ -426,8 +428,10 @@ __global__ __launch_bounds__(1024) void k_balance_sequences(BalanceArgs a, int c
 // weights that are not renormalised, their gradients; renormalised ones, a
 // softmax over the chosen, add w (dw - sum w dw). A wave a token; lane j holds route j's
 // id and gradient, which pass to the others through scalar registers. Bound by instructions
-// issued: 65536 tokens of 256 experts, 8 routes, 37 us (its 136 MB take 27), 41 with stores through the
-// caches; then two tokens a wave with their loads together 43.6, four 46.6.
+// issued: 65536 tokens of 256 experts, 8 routes, 35 us (its 136 MB take 27): 317 vector instructions a token, 64
+// tokens a SIMD, 4 cycles each, are 34 us at 2.4 GHz. 41 with stores through the
+// caches; then two tokens a wave with their loads together 43.6, four 46.6. Of 64 experts 24.5 us (173 a token), of 8
+// with 2 routes 20.4 (143): a token takes a wave whatever E.
 template <int C, bool V>
 __global__ __launch_bounds__(256) void k_router_backward(RouterBackArgs a)
 {

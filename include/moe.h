@@ -592,7 +592,8 @@ moe_status moe_matmul_fp8(int32_t M, int32_t N, int32_t K, const void *A_codes,
  *                do) where many records a slot make one kernel of it, else 4 M f
  * The other arguments and the limits are those of moe_matmul_fp8, which takes
  * H for the down projection. SiLU(g) * u is within (|g| + 8) 2^-22 of its
- * value for the g and u of the fp32 sums, relative. Sums that are off as C's in
+ * value for the g and u of the fp32 sums, relative, down to g = -174, and 0 below
+ * (where it is under 2^-116 whatever u). Sums that are off as C's in
  * bf16 are move a value that lies near the middle between two codes to the other
  * one (0.16 % of them for normally distributed operands); for H of sums of 24 bits
  * take g and u as fp32 C of moe_matmul_fp8 and quantise SiLU(g) * u.

@@ -70,3 +70,33 @@ def test_hidden_of_whole_numbers(M, f, K, P):
         lim = err + torch.maximum(2.0 ** -4 * (h.abs() + err), 2.0 ** -10 * unit[r])
         off_by = (got[r] - h).abs()
         assert bool((off_by <= lim).all()), f"slot {p}: {float((off_by / lim).max()):.3g} of the bound"
+
+
+@pytest.mark.parametrize("M,f", [(5, 64), (4096, 832)])
+@pytest.mark.parametrize("gate", [88.0, -86.5, -87.5, -100.0, -150.0, -174.0, -200.0])
+def test_hidden_of_far_gates(M, f, gate):
+    """One product each, exact: g = gate and u = 2^126 (2^30 for a positive gate), at both sides of where exp(-g) leaves
+    fp32. Within (|g| + 8) 2^-22 and half a step of the code down to g = -174, 0 below."""
+    K = 64
+    x = torch.zeros((M, K))
+    x[:, 0] = 1.0
+    a, as_ = quantise(x.cuda())
+    w = codes_of_one(f, K)
+    u = 2.0 ** (30 if gate > 0 else 126)
+    scale = lambda v: torch.full((-(-f // 128), 1), v, device="cuda")
+    H = torch.empty((M, f), dtype=torch.uint8, device="cuda")
+    Hs = torch.zeros((M, B.fp8_scale_bytes(f)), dtype=torch.uint8, device="cuda")
+    B.moe_gate_up_fp8(a, as_, w, scale(gate), w, scale(u), H, Hs)
+    unit = spread(unit64(Hs.cpu()[:, :-(-f // 128)]), 1, M, f)
+    got = decode(H) * unit
+    g = torch.tensor(gate, dtype=torch.float64)
+    h = float(g * torch.sigmoid(g) * u) if gate >= -174.0 else 0.0
+    err = (abs(gate) + 8) * 2.0 ** -22 * abs(h)
+    assert bool(((got - h).abs() <= err + torch.clamp(2.0 ** -10 * unit, min=2.0 ** -4 * (abs(h) + err))).all()) if h else bool((got == 0).all())
+
+
+def codes_of_one(f, K):
+    """Weights of 1 in the first column."""
+    w = torch.zeros((f, K), dtype=torch.uint8, device="cuda")
+    w[:, 0] = 0x38
+    return w
